@@ -584,3 +584,10 @@ class BoundLayer:
         rc = self._f[4](*self._fused)
         if rc:
             raise EpError(rc, "ep_dispatch_fused")
+
+
+# The experts and the backward pass (include/ep_experts.h) have a module of their own.
+from . import experts as _experts  # noqa: E402
+from .experts import *  # noqa: E402,F401,F403
+
+EXPORTS += _experts.EXPORTS

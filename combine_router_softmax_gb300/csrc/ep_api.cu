@@ -127,10 +127,11 @@ int ep_version(void) { return 100; }
 
 ep_status ep_device_error(int32_t *flags) {
     if (!flags) return EP_ERR_INVALID_ARG;
-    int32_t *words[3] = {nullptr, nullptr, nullptr};
+    int32_t *words[4] = {nullptr, nullptr, nullptr, nullptr};
     if (ep::dispatch_error_word(&words[0]) != cudaSuccess) return EP_ERR_CUDA;
     if (ep::fused_error_word(&words[1]) != cudaSuccess) return EP_ERR_CUDA;
     if (ep::sp_error_word(&words[2]) != cudaSuccess) return EP_ERR_CUDA;
+    if (ep::expert_error_word(&words[3]) != cudaSuccess) return EP_ERR_CUDA;
     int32_t all = 0;
     for (int32_t *word : words) {
         int32_t v = 0;

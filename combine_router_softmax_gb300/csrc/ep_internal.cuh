@@ -1,9 +1,10 @@
 // ep_internal.cuh -- shared declarations of the CUDA side of the C ABI.
 //
 // Kernels live in route.cu, layout.cu, dispatch.cu, combine.cu, fused.cu,
-// gather.cu, sp.cu and tff.cu; each file exposes its host launchers, declared
-// here. The C entry points in ep_api.cu validate arguments, then call the
-// launchers.
+// gather.cu, sp.cu and tff.cu, those of the experts and of the backward pass in
+// expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu; each file exposes
+// its host launchers, declared here. The C entry points in ep_api.cu and
+// experts_api.cu validate arguments, then call the launchers.
 #pragma once
 
 #include <atomic>
@@ -13,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "ep.h"
+#include "ep_experts.h"
 
 namespace ep {
 
@@ -279,9 +281,11 @@ constexpr int32_t kErrDispatchWait = 1;  // a dispatch CTA gave up waiting for a
 constexpr int32_t kErrFusedWait = 2;     // a fused-dispatch CTA gave up waiting (barrier or bulk copy)
 constexpr int32_t kErrSpWait = 4;        // a sentinel-polling CTA gave up waiting
 constexpr int32_t kErrGatherWait = 8;    // a schedule-driven dispatch CTA gave up waiting (or a bad table)
+constexpr int32_t kErrExpertWait = 16;   // an expert product's CTA gave up waiting
 cudaError_t dispatch_error_word(int32_t **addr);
 cudaError_t fused_error_word(int32_t **addr);
 cudaError_t sp_error_word(int32_t **addr);
+cudaError_t expert_error_word(int32_t **addr);
 
 // Schedule-driven dispatch (gather.cu).
 int64_t gather_ctas(const ep_config &c, int32_t W);
@@ -319,5 +323,15 @@ cudaError_t launch_dispatch_fused(const ep_config &c, int32_t W, const float *lo
                                   int32_t *rank_count, int32_t *rank_offset, int32_t *slot, ep_chunk *chunks,
                                   int32_t *n_chunks, int32_t *worker_begin, ep_bf16 *send, int32_t *meta,
                                   void *workspace, cudaStream_t s);
+
+// The experts' gated block (expert_ffn.cu).
+cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
+                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s);
+cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+                                       const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
+                                       const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
+                                       ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
+                                       ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s);
 
 }  // namespace ep

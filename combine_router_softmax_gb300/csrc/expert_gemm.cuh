@@ -1,0 +1,443 @@
+// expert_gemm.cuh -- the experts' matrix products on the tensor cores, grouped by expert.
+//
+// The rows of the send buffer lie grouped by expert: expert e owns rows
+// [expert_offset[e], expert_offset[e + 1]), known on the device only. Five products share
+// one kernel (S rows, the weights of expert e in brackets, s the owner's rows):
+//   GateUp   g = x Wg[e]^T, u = x Wu[e]^T, and h = silu(g) u from the accumulators
+//   Down     y = h Wd[e]^T
+//   DGateUp  dh = dy Wd[e], and from the accumulators du = dh silu(g),
+//            dg = dh u s (1 + g (1 - s)), s = sigmoid(g)
+//   DRows    dx = dg Wg[e] + du Wu[e]: one accumulation over 2 I
+//   DWeight  dWd[e] = dy^T h, dWg[e] = dg^T x, dWu[e] = du^T x over the expert's rows
+// Operands are bf16, sums fp32 (in TMEM), results are rounded to bf16 once. h, dg and du are
+// rounded to bf16 where they become operands of the next product.
+//
+// One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
+// holding half of either operand): warp 0 feeds a ring of shared-memory stages by TMA, warp
+// 1 issues the MMAs into one of two accumulators, warps 2 to 5 turn the other one into
+// results. Every wait has a time limit (kErrExpertWait).
+#pragma once
+
+#include "tcgen05.cuh"
+
+namespace ep {
+
+enum class ExpertOp { kGateUp, kDown, kDGateUp, kDRows, kDWeight };
+
+constexpr int kGemmThreads = 192;
+constexpr int kGemmBK = 64;   // contraction per stage: 128 bytes of bf16, one swizzled row
+constexpr int kGemmBM = 128;  // rows of a CTA's tile: the TMEM lanes
+
+struct GemmParams {
+    CUtensorMap a[3];    // K-major: box 64 k x 128 rows; MN-major: box 64 m x 64 k
+    CUtensorMap a16[2];  // K-major: box 64 k x 16 rows, for tiles with few rows
+    CUtensorMap b[3];
+    const int32_t *expert_offset;
+    int32_t E, S;
+    int32_t K;         // contraction of the row products (of each half, DRows)
+    int32_t M[3];      // DWeight: output rows of each problem
+    int32_t N[3];      // output columns of each problem (row products: N[0])
+    int32_t problems;  // DWeight: how many of the three are wanted
+    ep_bf16 *out[3];   // GateUp: h; DGateUp: dg, du; DWeight: the gradients [E, M, N]
+    ep_bf16 *g, *u;    // GateUp: written when not null; DGateUp: read
+    int32_t *error;
+};
+
+template <ExpertOp OP, int CG, int NB>
+struct GemmShape {
+    static constexpr bool kDW = OP == ExpertOp::kDWeight;
+    static constexpr bool kAMn = kDW;
+    static constexpr bool kBMn = OP == ExpertOp::kDGateUp || OP == ExpertOp::kDRows || kDW;
+    static constexpr int kOutN = OP == ExpertOp::kGateUp ? NB / 2 : NB;  // output columns of a tile
+    static constexpr int kBRows = NB / CG;                               // B rows a CTA holds
+    static constexpr int kABytes = kGemmBM * 128;
+    static constexpr int kBBytes = kBRows * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = 196608 / kStageBytes;
+    static constexpr int kTmemCols = 2 * NB;
+    static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
+};
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// Up to 32 results of one row: columns [n, n + 32) of N, N % 8 == 0.
+__device__ __forceinline__ void store_row_32(ep_bf16 *row, int n, int N, const uint32_t (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + 8 * i < N)
+            st_v4(reinterpret_cast<uint4 *>(row + n + 8 * i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+}
+__device__ __forceinline__ void load_row_32(const ep_bf16 *row, int n, int N, uint32_t (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (n + 8 * i < N) q = *reinterpret_cast<const uint4 *>(row + n + 8 * i);
+        v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    }
+}
+
+// One tile of the kernel's list, the same for every warp.
+struct Tile {
+    int e, problem;
+    int m0;     // first row (row products), first output row (DWeight)
+    int valid;  // rows of the expert from m0 on / output rows from m0 on
+    int n0;     // first output column
+    int row0, rows;  // DWeight: the expert's rows
+};
+
+// Walks the tiles of one CTA (pair): first, first + step, ... The tables are in shared memory.
+template <ExpertOp OP, int CG, int NB>
+struct Walk {
+    using Sh = GemmShape<OP, CG, NB>;
+    static constexpr int kBM = kGemmBM * CG;
+    const GemmParams &p;
+    const int *lo, *count;  // first row and rows of an expert
+    const int64_t *prefix;  // m-tiles before it
+    int64_t tile, step;
+    int e = 0;
+
+    __device__ Walk(const GemmParams &p_, const int *lo_, const int *count_, const int64_t *prefix_)
+        : p(p_), lo(lo_), count(count_), prefix(prefix_), tile(blockIdx.x / CG), step(gridDim.x / CG) {}
+
+    __device__ bool next(Tile &t) {
+        if constexpr (Sh::kDW) {
+            int64_t per_e = 0;
+            for (int i = 0; i < p.problems; ++i)
+                per_e += (int64_t)((p.M[i] + kBM - 1) / kBM) * ((p.N[i] + NB - 1) / NB);
+            t.e = (int)(tile / per_e);
+            if (t.e >= p.E) return false;
+            int64_t rest = tile % per_e;
+            int i = 0;
+            for (; i < p.problems - 1; ++i) {
+                const int64_t n = (int64_t)((p.M[i] + kBM - 1) / kBM) * ((p.N[i] + NB - 1) / NB);
+                if (rest < n) break;
+                rest -= n;
+            }
+            const int mt = (p.M[i] + kBM - 1) / kBM;
+            t.problem = i;
+            t.m0 = (int)(rest % mt) * kBM;
+            t.n0 = (int)(rest / mt) * NB;
+            t.valid = p.M[i] - t.m0;
+            t.row0 = lo[t.e];
+            t.rows = count[t.e];
+        } else {
+            const int nt = (p.N[0] + Sh::kOutN - 1) / Sh::kOutN;
+            if (tile >= prefix[p.E] * nt) return false;
+            while (tile >= prefix[e + 1] * nt) ++e;
+            const int64_t rest = tile - prefix[e] * nt;
+            const int64_t mt = prefix[e + 1] - prefix[e];
+            const int m = (int)(rest % mt);
+            t.e = e;
+            t.problem = 0;
+            t.m0 = lo[e] + m * kBM;
+            t.valid = count[e] - m * kBM;
+            t.n0 = (int)(rest / mt) * Sh::kOutN;
+        }
+        tile += step;
+        return true;
+    }
+    // stages that the tile's contraction takes
+    __device__ int blocks(const Tile &t) const {
+        if constexpr (Sh::kDW) return (t.rows + kGemmBK - 1) / kGemmBK;
+        const int kb = (p.K + kGemmBK - 1) / kGemmBK;
+        return OP == ExpertOp::kDRows ? 2 * kb : kb;
+    }
+};
+
+// Rows of A that are fetched for a CTA with `valid` rows left: one box of 128, or as many of
+// 16 as hold them. The MMA computes all 128 rows; what lies in the others reaches only
+// result rows that are not stored.
+__device__ __forceinline__ int a_rows_fetched(int valid) {
+    return valid <= 0 ? 0 : valid > 96 ? kGemmBM : (valid + 15) / 16 * 16;
+}
+
+template <ExpertOp OP, int CG, int NB>
+__global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using Sh = GemmShape<OP, CG, NB>;
+    static_assert(!(Sh::kDW && CG == 2), "the rows past an expert's end are zeroed by the issuing CTA alone");
+    constexpr int kStages = Sh::kStages;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_addr;
+    __shared__ volatile int failed;
+
+    unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    int64_t *prefix = reinterpret_cast<int64_t *>(stages + kStages * Sh::kStageBytes);
+    int *lo = reinterpret_cast<int *>(prefix + p.E + 1), *count = lo + p.E;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0;
+
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4 * CG);
+        mbar_init(&drained, 1);
+        failed = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&p.a[0]);
+        tma_prefetch_map(&p.b[0]);
+    }
+    if (warp == 1) tmem_alloc<CG>(&tmem_addr, Sh::kTmemCols);
+    // bounds come from device memory: kept inside the row buffer whatever they hold
+    for (int e = threadIdx.x; e < p.E; e += kGemmThreads) {
+        const int first = min(max(p.expert_offset[e], 0), p.S);
+        lo[e] = first;
+        count[e] = min(max(p.expert_offset[e + 1], first), p.S) - first;
+    }
+    __syncthreads();
+    if (!Sh::kDW && warp == 2) {
+        int64_t sum = 0;
+        for (int base = 0; base < p.E; base += 32) {
+            const int e = base + lane;
+            int64_t v = e < p.E ? (count[e] + (int64_t)kGemmBM * CG - 1) / (kGemmBM * CG) : 0;
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (lane >= d) v += o;
+            }
+            if (e < p.E) prefix[e + 1] = sum + v;
+            sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    tmem_fence_before();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_addr;
+
+    Walk<OP, CG, NB> walk(p, lo, count, prefix);
+    Tile t;
+
+    if (warp == 0) {
+        // ---- producer: one lane fetches the stages of every tile in turn
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && walk.next(t)) {
+                const int kb = walk.blocks(t);
+                const int fetched = Sh::kDW ? 0 : a_rows_fetched(t.valid - (int)rank * kGemmBM);
+                uint32_t bytes = Sh::kBBytes * CG;
+                if constexpr (Sh::kDW)
+                    bytes += Sh::kABytes;
+                else
+                    for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * kGemmBM) * 128;
+                for (int b = 0; b < kb; ++b, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait_limited(&empty[s], (it / kStages - 1) & 1, &failed)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    const uint32_t bar = CG == 2 ? cluster_smem_u32(&full[s], 0) : smem_u32(&full[s]);
+                    unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
+                    if constexpr (Sh::kDW) {
+                        const int k = t.row0 + b * kGemmBK;
+#pragma unroll
+                        for (int i = 0; i < kGemmBM / 64; ++i)
+                            tma_load_2d<CG>(sa + i * 8192, &p.a[t.problem], t.m0 + 64 * i, k, bar);
+#pragma unroll
+                        for (int i = 0; i < Sh::kBRows / 64; ++i)
+                            tma_load_2d<CG>(sb + i * 8192, &p.b[t.problem], t.n0 + 64 * i, k, bar);
+                    } else {
+                        const int half = OP == ExpertOp::kDRows && b >= kb / 2 ? 1 : 0;
+                        const int k = (half ? b - kb / 2 : b) * kGemmBK;
+                        const int row = t.m0 + (int)rank * kGemmBM;
+                        if (fetched == kGemmBM)
+                            tma_load_2d<CG>(sa, &p.a[half], k, row, bar);
+                        else
+                            for (int i = 0; i < fetched; i += 16)
+                                tma_load_2d<CG>(sa + i * 128, &p.a16[half], k, row + i, bar);
+                        if constexpr (OP == ExpertOp::kGateUp) {
+                            if constexpr (CG == 2)
+                                tma_load_3d<CG>(sb, &p.b[rank], k, t.n0, t.e, bar);
+                            else {
+                                tma_load_3d<CG>(sb, &p.b[0], k, t.n0, t.e, bar);
+                                tma_load_3d<CG>(sb + Sh::kBBytes / 2, &p.b[1], k, t.n0, t.e, bar);
+                            }
+                        } else if constexpr (!Sh::kBMn) {
+                            tma_load_3d<CG>(sb, &p.b[0], k, t.n0 + (int)rank * Sh::kBRows, t.e, bar);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < Sh::kBRows / 64; ++i)
+                                tma_load_3d<CG>(sb + i * 8192, &p.b[half], t.n0 + (int)rank * Sh::kBRows + 64 * i, k,
+                                                t.e, bar);
+                        }
+                    }
+                }
+            }
+            // no copy may be under way when the CTA ends: after a failure nobody else waits for them
+            if (failed && rank == 0)
+                for (int i = 0; i < kStages; ++i)
+                    if (it > (uint32_t)i) {
+                        const uint32_t last = (it - 1 - i) / kStages;  // how often stage i was filled again
+                        int never = 0;
+                        mbar_wait_limited(&full[i], last & 1, &never);
+                    }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA issuer (CG = 2: of the pair's first CTA)
+        if (rank == 0) {
+            constexpr uint32_t idesc = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
+            uint32_t it = 0, acc_it = 0;
+            bool ok = true;
+            while (ok && walk.next(t)) {
+                const int kb = walk.blocks(t);
+                if (kb == 0) continue;
+                const uint32_t slot = acc_it & 1;
+                if (acc_it >= 2 && !mbar_wait_limited(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed)) break;
+                ++acc_it;
+                tmem_fence_after();
+                const uint32_t d = tmem + slot * NB;
+                for (int b = 0; b < kb; ++b, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait_limited(&full[s], (it / kStages) & 1, &failed)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
+                    int steps = kGemmBK / 16;
+                    if constexpr (Sh::kDW) {
+                        // the last stage also holds rows of the next expert: they count for nothing
+                        const int left = t.rows - b * kGemmBK;
+                        if (left < kGemmBK) {
+                            steps = (left + 15) / 16;
+                            const int zero = (steps * 16 - left) * 8;  // 16-byte words of a 64-wide column block
+                            for (int i = lane; i < (kGemmBM + Sh::kBRows) / 64 * zero; i += 32)
+                                reinterpret_cast<uint4 *>(sa + i / zero * 8192 + left * 128)[i % zero] = make_uint4(0, 0, 0, 0);
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
+                    }
+                    tmem_fence_after();
+                    if (lane == 0) {
+                        const uint64_t da = smem_desc(smem_u32(sa), Sh::kAMn ? 8192 : 16);
+                        const uint64_t db = smem_desc(smem_u32(sb), Sh::kBMn ? 8192 : 16);
+                        for (int k = 0; k < steps; ++k)
+                            mma_bf16<CG>(d, da + k * (Sh::kAMn ? 128 : 2), db + k * (Sh::kBMn ? 128 : 2), idesc, b + k > 0);
+                        mma_commit<CG>(&empty[s]);
+                        if (b == kb - 1) mma_commit<CG>(&acc_full[slot]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (failed) {  // MMAs may still read the stages and write TMEM
+                if (lane == 0) mma_commit<CG>(&drained);
+                __syncwarp();
+                int never = 0;
+                mbar_wait_limited(&drained, 0, &never);
+            }
+        }
+    } else {
+        // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread
+        const int quarter = warp % 4;
+        const int r = (int)rank * kGemmBM + quarter * 32 + lane;  // row within the tile
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        uint32_t acc_it = 0;
+        while (walk.next(t)) {
+            const bool none = walk.blocks(t) == 0;
+            const uint32_t slot = acc_it & 1;
+            if (!none) {
+                if (!mbar_wait_limited(&acc_full[slot], (acc_it / 2) & 1, &failed)) break;
+                ++acc_it;
+                tmem_fence_after();
+            }
+            const bool mine = r < t.valid;
+            const bool any = r - lane < t.valid;  // the same in the whole warp
+            const uint32_t src = tmem + lanes + slot * NB;
+            const int N = p.N[t.problem];
+            if (any) {
+                const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r : (size_t)t.m0 + r;
+                for (int c = 0; c < Sh::kOutN && t.n0 + c < N; c += 32) {
+                    uint32_t v[32], o[16];
+                    if (!none) tmem_load_32(src + c, v);
+                    const int n = t.n0 + c;
+                    if constexpr (OP == ExpertOp::kGateUp) {
+                        uint32_t w[32];
+                        tmem_load_32(src + Sh::kOutN + c, w);
+                        tmem_wait_ld(v);
+                        tmem_wait_ld(w);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
+                            o[i] = bf16_pair(g0 * sigmoid(g0) * __uint_as_float(w[2 * i]),
+                                             g1 * sigmoid(g1) * __uint_as_float(w[2 * i + 1]));
+                        }
+                        if (mine) {
+                            store_row_32(p.out[0] + row * N, n, N, o);
+                            if (p.g) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                                store_row_32(p.g + row * N, n, N, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = bf16_pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+                                store_row_32(p.u + row * N, n, N, o);
+                            }
+                        }
+                    } else if constexpr (OP == ExpertOp::kDGateUp) {
+                        uint32_t g[16] = {}, u[16] = {};
+                        if (mine) {
+                            load_row_32(p.g + row * N, n, N, g);
+                            load_row_32(p.u + row * N, n, N, u);
+                        }
+                        tmem_wait_ld(v);
+                        uint32_t o2[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float dg[2], du[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float dh = __uint_as_float(v[2 * i + k]);
+                                const float gg = k ? bf16_hi(g[i]) : bf16_lo(g[i]), uu = k ? bf16_hi(u[i]) : bf16_lo(u[i]);
+                                const float s = sigmoid(gg);
+                                du[k] = dh * gg * s;
+                                dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
+                            }
+                            o[i] = bf16_pair(dg[0], dg[1]);
+                            o2[i] = bf16_pair(du[0], du[1]);
+                        }
+                        if (mine) {
+                            store_row_32(p.out[0] + row * N, n, N, o);
+                            store_row_32(p.out[1] + row * N, n, N, o2);
+                        }
+                    } else {
+                        if (!none) tmem_wait_ld(v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        if (mine) store_row_32(p.out[t.problem] + row * N, n, N, o);
+                    }
+                }
+            }
+            if (!none) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster(cluster_smem_u32(&acc_empty[slot], 0));
+                    else
+                        mbar_arrive(&acc_empty[slot]);
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // no arrival may reach a CTA that has ended
+    if (threadIdx.x == 0 && failed) atomicOr(p.error, kErrExpertWait);
+    if (warp == 1) tmem_free<CG>(tmem, Sh::kTmemCols);
+}
+
+}  // namespace ep

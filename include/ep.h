@@ -112,6 +112,8 @@ int ep_version(void);
  *              arrived, or a bulk copy); its rows were not all written.
  *   bit 3 (8): an ep_dispatch_scheduled CTA gave up waiting on a bulk copy,
  *              or its chunk table named rows outside the send buffer.
+ *   bit 4 (16): a CTA of an expert product (ep_experts.h) gave up waiting; its
+ *              results were not all written.
  * (ep_layout reports its own bounded wait through *n_chunks = -1.) */
 ep_status ep_device_error(int32_t *flags);
 
@@ -473,5 +475,8 @@ ep_status ep_layout_static(const ep_config *cfg, const int32_t *topk_idx,
 #ifdef __cplusplus
 }
 #endif
+
+/* The experts between dispatch and combine, and the backward pass. */
+#include "ep_experts.h"
 
 #endif /* EP_GB300_H */
