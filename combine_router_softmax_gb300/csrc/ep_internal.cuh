@@ -334,4 +334,23 @@ cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *ro
                                        ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
                                        ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s);
 
+// 4-bit weights (expert_w4.cu).
+cudaError_t launch_w4_pack(const ep_w4_config &c, const ep_bf16 *w, uint8_t *q, ep_bf16 *scale, cudaStream_t s);
+cudaError_t launch_w4_linear(const ep_w4_config &c, const ep_bf16 *x, const int32_t *expert_offset, const uint8_t *q,
+                             const ep_bf16 *scale, ep_bf16 *y, cudaStream_t s);
+cudaError_t launch_expert_ffn_w4(const ep_ffn_config &c, int group, const ep_bf16 *rows, const int32_t *expert_offset,
+                                 const uint8_t *q_gate, const ep_bf16 *s_gate, const uint8_t *q_up, const ep_bf16 *s_up,
+                                 const uint8_t *q_down, const ep_bf16 *s_down, ep_bf16 *h, ep_bf16 *y, cudaStream_t s);
+
+// Backward of combine and router (backward.cu).
+cudaError_t launch_combine_backward(const ep_config &c, const ep_bf16 *d_out, const ep_bf16 *y, const int32_t *slot,
+                                    const float *w, ep_bf16 *d_y, float *d_w, cudaStream_t s);
+cudaError_t launch_route_backward(const ep_config &c, const float *logits, const int32_t *idx, const float *w,
+                                  const float *d_w, float *d_logits, cudaStream_t s);
+
+// Gradient norm and clipping (grad_clip.cu); scale false: the norm alone.
+size_t grad_workspace_bytes(int32_t n);
+cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm,
+                             double *partial, cudaStream_t s);
+
 }  // namespace ep

@@ -8,15 +8,14 @@ status. The package re-exports everything here.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
 
 import torch
 
-from . import _check, _lib, _ptr, _stream
+from . import EpConfig, _check, _lib, _ptr, _stream
 
-__all__ = ["EpFfnConfig", "ep_expert_ffn", "ep_expert_ffn_backward"]
-
-EXPORTS = ("ep_expert_ffn", "ep_expert_ffn_backward")
+EXPORTS = ("ep_expert_ffn", "ep_expert_ffn_backward", "ep_w4_sizes", "ep_w4_pack", "ep_w4_linear", "ep_expert_ffn_w4",
+           "ep_combine_backward", "ep_route_backward", "ep_grad_workspace_size", "ep_grad_norm", "ep_grad_clip")
+__all__ = [*EXPORTS, "EpFfnConfig", "EpW4Config", "EpGradTensor", "GradList"]
 
 
 class EpFfnConfig(ctypes.Structure):
@@ -28,9 +27,33 @@ class EpFfnConfig(ctypes.Structure):
         return cls(rows, H, I, E)
 
 
+class EpW4Config(ctypes.Structure):
+    """``ep_w4_config`` of include/ep_experts.h."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "N", "K", "E", "group")]
+
+    @classmethod
+    def make(cls, *, rows=0, N, K, E=1, group=128) -> "EpW4Config":
+        return cls(rows, N, K, E, group)
+
+
+class EpGradTensor(ctypes.Structure):
+    """``ep_grad_tensor`` of include/ep_experts.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def _declare() -> None:
-    P, vp = ctypes.POINTER, ctypes.c_void_p
-    ffn = P(EpFfnConfig)
+    P, vp, i32, size = ctypes.POINTER, ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    ffn, w4, layer, grads = P(EpFfnConfig), P(EpW4Config), P(EpConfig), P(EpGradTensor)
+    _lib.ep_w4_sizes.argtypes = [w4, P(size), P(size)]
+    _lib.ep_w4_pack.argtypes = [w4] + [vp] * 4
+    _lib.ep_w4_linear.argtypes = [w4] + [vp] * 6
+    _lib.ep_expert_ffn_w4.argtypes = [ffn, i32] + [vp] * 11
+    _lib.ep_combine_backward.argtypes = [layer] + [vp] * 7
+    _lib.ep_route_backward.argtypes = [layer] + [vp] * 6
+    _lib.ep_grad_workspace_size.argtypes = [i32, P(size)]
+    _lib.ep_grad_norm.argtypes = [grads, i32, vp, vp, size, vp]
+    _lib.ep_grad_clip.argtypes = [grads, i32, ctypes.c_float, vp, vp, size, vp]
     _lib.ep_expert_ffn.argtypes = [ffn] + [vp] * 10
     _lib.ep_expert_ffn_backward.argtypes = [ffn] + [vp] * 16
     for name in EXPORTS:
@@ -70,3 +93,116 @@ def ep_expert_ffn_backward(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, 
         _bf16(d_g, (S, I), "d_g"), _bf16(d_u, (S, I), "d_u"), _bf16(d_rows, (S, H), "d_rows"),
         _bf16(d_w_gate, (E, I, H), "d_w_gate"), _bf16(d_w_up, (E, I, H), "d_w_up"),
         _bf16(d_w_down, (E, H, I), "d_w_down"), _stream(stream)), "ep_expert_ffn_backward")
+
+
+def ep_w4_sizes(cfg: EpW4Config) -> tuple[int, int]:
+    """Bytes of a packed weight's q and scale."""
+    q, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(_lib.ep_w4_sizes(ctypes.byref(cfg), ctypes.byref(q), ctypes.byref(s)), "ep_w4_sizes")
+    return q.value, s.value
+
+
+def _packed(cfg: EpW4Config, q, scale, name):
+    """Pointers of a packed weight: q uint8 [E, N, Kp / 2], scale bf16 [E, N, Kp / group]."""
+    q_bytes, s_bytes = ep_w4_sizes(cfg)
+    rows = cfg.E * cfg.N
+    return (_ptr(q, torch.uint8, (cfg.E, cfg.N, q_bytes // rows), "q" + name),
+            _bf16(scale, (cfg.E, cfg.N, s_bytes // 2 // rows), "scale" + name))
+
+
+def ep_w4_pack(cfg: EpW4Config, w, q, scale, stream=None) -> None:
+    """w bf16 [E, N, K] -> q uint8 [E, N, Kp / 2], scale bf16 [E, N, Kp / group]; Kp is K filled up to 128."""
+    _check(_lib.ep_w4_pack(ctypes.byref(cfg), _bf16(w, (cfg.E, cfg.N, cfg.K), "w"), *_packed(cfg, q, scale, ""),
+                           _stream(stream)), "ep_w4_pack")
+
+
+def ep_w4_linear(cfg: EpW4Config, x, expert_offset, q, scale, y, stream=None) -> None:
+    """y[s] = W[e(s)] x[s] with packed 4-bit weights; x bf16 [rows, K], y bf16 [rows, N]."""
+    _check(_lib.ep_w4_linear(ctypes.byref(cfg), _bf16(x, (cfg.rows, cfg.K), "x"),
+                             _ptr(expert_offset, torch.int32, (cfg.E + 1,), "expert_offset"),
+                             *_packed(cfg, q, scale, ""), _bf16(y, (cfg.rows, cfg.N), "y"), _stream(stream)),
+           "ep_w4_linear")
+
+
+def ep_expert_ffn_w4(cfg: EpFfnConfig, group: int, rows, expert_offset, q_gate, s_gate, q_up, s_up, q_down, s_down, h,
+                     y, stream=None) -> None:
+    """ep_expert_ffn's forward pass with packed 4-bit weights."""
+    S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
+    wide = EpW4Config.make(N=I, K=H, E=E, group=group)
+    down = EpW4Config.make(N=H, K=I, E=E, group=group)
+    _check(_lib.ep_expert_ffn_w4(ctypes.byref(cfg), ctypes.c_int32(group), _bf16(rows, (S, H), "rows"),
+                                 _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
+                                 *_packed(wide, q_gate, s_gate, "_gate"), *_packed(wide, q_up, s_up, "_up"),
+                                 *_packed(down, q_down, s_down, "_down"), _bf16(h, (S, I), "h"),
+                                 _bf16(y, (S, H), "y"), _stream(stream)), "ep_expert_ffn_w4")
+
+
+def ep_combine_backward(cfg: EpConfig, d_out, y, slot, topk_w, d_y, d_topk_w, stream=None) -> None:
+    """d_out bf16 [T, H], y bf16 [T*k, H] -> d_y bf16 [T*k, H] (slot order), d_topk_w fp32 [T, k]."""
+    T, H, k = cfg.T, cfg.H, cfg.k
+    _check(_lib.ep_combine_backward(ctypes.byref(cfg), _bf16(d_out, (T, H), "d_out"), _bf16(y, (T * k, H), "y"),
+                                    _ptr(slot, torch.int32, (T, k), "slot"),
+                                    _ptr(topk_w, torch.float32, (T, k), "topk_w"), _bf16(d_y, (T * k, H), "d_y"),
+                                    _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(stream)),
+           "ep_combine_backward")
+
+
+def ep_route_backward(cfg: EpConfig, logits, topk_idx, topk_w, d_topk_w, d_logits, stream=None) -> None:
+    """d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]; logits may be None where cfg.renormalize is 1."""
+    T, E, k = cfg.T, cfg.E, cfg.k
+    _check(_lib.ep_route_backward(ctypes.byref(cfg), _ptr(logits, torch.float32, (T, E), "logits"),
+                                  _ptr(topk_idx, torch.int32, (T, k), "topk_idx"),
+                                  _ptr(topk_w, torch.float32, (T, k), "topk_w"),
+                                  _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"),
+                                  _ptr(d_logits, torch.float32, (T, E), "d_logits"), _stream(stream)),
+           "ep_route_backward")
+
+
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def ep_grad_workspace_size(n: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(_lib.ep_grad_workspace_size(n, ctypes.byref(b)), "ep_grad_workspace_size")
+    return b.value
+
+
+class GradList:
+    """A list of gradient tensors with its C records and workspace, made once and used every step.
+
+    ``out``: where the clipped values go (same shapes and types); the tensors themselves if None."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
+        self._keep = (grads, out)
+        self.n = len(grads)
+        self.records = (EpGradTensor * max(self.n, 1))()
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if not isinstance(g, torch.Tensor) or g.dtype not in _GRAD_TYPES:
+                raise TypeError(f"grads[{i}]: expected a float32, bfloat16 or float16 tensor")
+            data, to = _ptr(g, g.dtype, None, f"grads[{i}]"), _ptr(o, g.dtype, tuple(g.shape), f"out[{i}]")
+            self.records[i] = EpGradTensor(data, to, g.numel(), _GRAD_TYPES[g.dtype], 0)
+        self.workspace = torch.empty((ep_grad_workspace_size(self.n),), dtype=torch.uint8, device="cuda")
+
+    def norm(self, norm, stream=None) -> None:
+        ep_grad_norm(self, norm, stream)
+
+    def clip(self, max_norm: float, norm, stream=None) -> None:
+        ep_grad_clip(self, max_norm, norm, stream)
+
+
+def ep_grad_norm(grads: GradList, norm, stream=None) -> None:
+    """norm fp32 [1]: the 2-norm over all values of all tensors of the list."""
+    ws = grads.workspace
+    _check(_lib.ep_grad_norm(grads.records, grads.n, _ptr(norm, torch.float32, (1,), "norm"),
+                             _ptr(ws, torch.uint8, None, "workspace"), ws.numel(), _stream(stream)), "ep_grad_norm")
+
+
+def ep_grad_clip(grads: GradList, max_norm: float, norm, stream=None) -> None:
+    """The norm, and every tensor times min(1, max_norm / (norm + 1e-6)) to its ``out``."""
+    ws = grads.workspace
+    _check(_lib.ep_grad_clip(grads.records, grads.n, float(max_norm), _ptr(norm, torch.float32, (1,), "norm"),
+                             _ptr(ws, torch.uint8, None, "workspace"), ws.numel(), _stream(stream)), "ep_grad_clip")

@@ -82,6 +82,128 @@ ep_status ep_expert_ffn_backward(const ep_ffn_config *cfg, const ep_bf16 *rows, 
                                  ep_bf16 *d_rows, ep_bf16 *d_w_gate, ep_bf16 *d_w_up, ep_bf16 *d_w_down,
                                  cudaStream_t stream);
 
+/*
+ * Products with 4-bit weights, for few rows (decoding): each weight is
+ * scale (q - 8) with q in 0 .. 15 and one bf16 scale for `group` consecutive k.
+ *
+ * Packed form of a weight [E, N, K]: K is filled up to Kp, a multiple of 128,
+ * with q = 8.
+ *   q     : uint8 [E, N, Kp / 2]. A row is 32-bit little-endian words; word
+ *           16 c + 4 t + j (t, j = 0 .. 3) holds k = k0 .. k0 + 7 with
+ *           k0 = 128 c + 32 j + 8 t, and its nibble i (bits 4 i .. 4 i + 3) the
+ *           one at k0 + 2 (i mod 4) + i / 4.
+ *   scale : bf16 [E, N, Kp / group], scale[e, n, k / group]
+ */
+typedef struct ep_w4_config {
+    int32_t rows;  /* rows of x and y (>= 0)                    */
+    int32_t N;     /* outputs (> 0)                              */
+    int32_t K;     /* inputs (> 0, a multiple of 8)              */
+    int32_t E;     /* experts (1 .. 1024); 1: an ordinary layer  */
+    int32_t group; /* k of one scale: 32, 64 or 128              */
+} ep_w4_config;
+
+/* Bytes of the packed form's q and scale (rows is not looked at). */
+ep_status ep_w4_sizes(const ep_w4_config *cfg, size_t *q_bytes, size_t *scale_bytes);
+
+/*
+ * ep_w4_pack -- rounds bf16 weights to 4 bits: per group
+ *   scale = bf16(max |w| / 7), q = clamp(rint(w / scale), -8, 7) + 8
+ * (q = 8 where scale is 0). Weights must be finite.
+ *
+ * w : const bf16 [E, N, K], 16-byte aligned; q and scale 16-byte aligned.
+ */
+ep_status ep_w4_pack(const ep_w4_config *cfg, const ep_bf16 *w, uint8_t *q, ep_bf16 *scale, cudaStream_t stream);
+
+/*
+ * ep_w4_linear -- y[s, n] = sum_k x[s, k] w[e, n, k], e the expert that owns
+ * row s, w the packed weight's values. The products are exact, sums fp32, y is
+ * rounded to bf16 once. Right for any number of rows; made for few: the weights
+ * are read once for every 16 rows of an expert.
+ *
+ * x : const bf16 [rows, K], 16-byte aligned       y : bf16 [rows, N] output
+ */
+ep_status ep_w4_linear(const ep_w4_config *cfg, const ep_bf16 *x, const int32_t *expert_offset, const uint8_t *q,
+                       const ep_bf16 *scale, ep_bf16 *y, cudaStream_t stream);
+
+/*
+ * ep_expert_ffn_w4 -- ep_expert_ffn's forward pass with 4-bit weights: q_gate,
+ * q_up packed [E, I, H], q_down packed [E, H, I], all with the same group. Two
+ * kernels, as there; h is rounded to bf16 between them.
+ */
+ep_status ep_expert_ffn_w4(const ep_ffn_config *cfg, int32_t group, const ep_bf16 *rows, const int32_t *expert_offset,
+                           const uint8_t *q_gate, const ep_bf16 *s_gate, const uint8_t *q_up, const ep_bf16 *s_up,
+                           const uint8_t *q_down, const ep_bf16 *s_down, ep_bf16 *h, ep_bf16 *y, cudaStream_t stream);
+
+/*
+ * ep_combine_backward -- the gradients of ep_combine for d_out, the gradient of
+ * its out:
+ *   d_y[slot[t, j], :] = bf16(topk_w[t, j] d_out[t, :])
+ *   d_topk_w[t, j]     = sum_h d_out[t, h] y[slot[t, j], h]
+ * Sums in fp32. A slot outside [0, T k) writes no row, and 0 to d_topk_w. The
+ * gradient of ep_dispatch is ep_combine itself with weights of one: it sums the
+ * k rows of every token's gradient.
+ *
+ * d_out    : const bf16 [T, H]           y   : const bf16 [T k, H]
+ * slot     : const int32 [T, k]          topk_w : const float [T, k]
+ * d_y      : bf16 [T k, H] output        d_topk_w : float [T, k] output
+ * d_out, y, d_y 16-byte aligned; d_y may not overlap y.
+ */
+ep_status ep_combine_backward(const ep_config *cfg, const ep_bf16 *d_out, const ep_bf16 *y, const int32_t *slot,
+                              const float *topk_w, ep_bf16 *d_y, float *d_topk_w, cudaStream_t stream);
+
+/*
+ * ep_route_backward -- the gradient of ep_route's weights with respect to the
+ * logits (the choice itself has none). With inner = sum_i topk_w_i d_topk_w_i:
+ *   renormalize: d_logits[t, idx_j] = topk_w_j (d_topk_w_j - inner), 0 elsewhere
+ *   else       : d_logits[t, e] = p_e (d_e - inner), p the softmax over all E
+ *                logits, d_e = d_topk_w_j for e = idx_j and 0 for the others
+ *
+ * logits   : const float [T, E]; read only without renormalize (else may be NULL)
+ * topk_idx : const int32 [T, k], distinct in a row; ids outside [0, E) count
+ *            for inner only
+ * topk_w, d_topk_w : const float [T, k]
+ * d_logits : float [T, E] output
+ */
+ep_status ep_route_backward(const ep_config *cfg, const float *logits, const int32_t *topk_idx, const float *topk_w,
+                            const float *d_topk_w, float *d_logits, cudaStream_t stream);
+
+/* One gradient tensor of a list: numel values at `data` (device), dense. */
+typedef enum ep_dtype { EP_F32 = 0, EP_BF16 = 1, EP_F16 = 2 } ep_dtype;
+
+typedef struct ep_grad_tensor {
+    const void *data; /* aligned to its values                                     */
+    void *out;        /* ep_grad_clip: where the clipped values go; data itself, or
+                         memory that overlaps no tensor of the list                */
+    int64_t numel;    /* >= 0                                                      */
+    int32_t dtype;    /* ep_dtype                                                  */
+    int32_t reserved; /* 0                                                         */
+} ep_grad_tensor;
+
+/* Bytes of device scratch that the two calls below need for n tensors. */
+ep_status ep_grad_workspace_size(int32_t n, size_t *bytes);
+
+/*
+ * ep_grad_norm -- norm[0] = sqrt(sum of the squares of all values of all
+ * tensors), fp32. Values are squared in fp32 (one beyond 1.8e19 gives
+ * infinity); the sums go on in 64 bits, in an order that depends on the sizes
+ * and on the tensors' alignment only, so the result repeats bit by bit.
+ *
+ * tensors   : HOST array of n records (n >= 0), read during the call
+ * workspace : device, 8-byte aligned, >= ep_grad_workspace_size bytes
+ */
+ep_status ep_grad_norm(const ep_grad_tensor *tensors, int32_t n, float *norm, void *workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/*
+ * ep_grad_clip -- ep_grad_norm, then for every value
+ *   out = data min(1, max_norm / (norm + 1e-6))
+ * in fp32, rounded to the tensor's type. No host synchronisation. A NaN in the
+ * norm passes to every value; an infinite norm gives a factor of 0.
+ * max_norm >= 0.
+ */
+ep_status ep_grad_clip(const ep_grad_tensor *tensors, int32_t n, float max_norm, float *norm, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
