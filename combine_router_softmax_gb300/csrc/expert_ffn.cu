@@ -8,6 +8,14 @@ namespace {
 
 __device__ int32_t g_expert_error;
 
+}  // namespace
+
+cudaError_t expert_error_word(int32_t **addr) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(addr), g_expert_error);
+}
+
+namespace {
+
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -84,16 +92,10 @@ GemmParams base_params(const ep_ffn_config &c, const int32_t *expert_offset) {
     return p;
 }
 
-}  // namespace
-
-cudaError_t expert_error_word(int32_t **addr) {
-    return cudaGetSymbolAddress(reinterpret_cast<void **>(addr), g_expert_error);
-}
-
-cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+template <int CG, int NB>
+cudaError_t run_forward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                               const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
-                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
-    constexpr int NB = 256, CG = 1;
+                        ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
     GemmParams p = base_params(c, expert_offset);
     p.K = c.H;
     p.N[0] = c.I;
@@ -114,12 +116,12 @@ cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const
     return launch<ExpertOp::kDown, CG, NB>(p, row_tiles(p, kGemmBM * CG, NB), s);
 }
 
-cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+template <int CG, int NB>
+cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
                                        const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
                                        ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
-                                       ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
-    constexpr int NB = 256, CG = 1;
+                         ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
     GemmParams p = base_params(c, expert_offset);
     p.K = c.H;
     p.N[0] = c.I;
@@ -158,9 +160,30 @@ cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *ro
         p.out[i] = w.out;
         if (!make_map(&p.a[i], w.a, w.M, p.S, 0, 64, kGemmBK) || !make_map(&p.b[i], w.b, w.N, p.S, 0, 64, kGemmBK))
             return cudaErrorInvalidValue;
-        tiles += (int64_t)c.E * ((w.M + kGemmBM - 1) / kGemmBM) * ((w.N + NB - 1) / NB);
+        tiles += (int64_t)c.E * ((w.M + kGemmBM * CG - 1) / (kGemmBM * CG)) * ((w.N + NB - 1) / NB);
     }
-    return p.problems ? launch<ExpertOp::kDWeight, 1, NB>(p, tiles, s) : cudaSuccess;
+    return p.problems ? launch<ExpertOp::kDWeight, CG, NB>(p, tiles, s) : cudaSuccess;
+}
+
+// A CTA pair takes tiles of 256 rows: worth it once an expert has more than one tile of 128.
+bool pairs(const ep_ffn_config &c) { return c.rows > (int64_t)kGemmBM * c.E; }
+
+}  // namespace
+
+cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
+                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
+    const auto run = pairs(c) ? run_forward<2, 256> : run_forward<1, 256>;
+    return run(c, rows, expert_offset, w_gate, w_up, w_down, g, u, h, y, s);
+}
+
+cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+                                       const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
+                                       const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
+                                       ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
+                                       ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
+    const auto run = pairs(c) ? run_backward<2, 256> : run_backward<1, 256>;
+    return run(c, rows, expert_offset, w_gate, w_up, w_down, g, u, h, d_y, d_g, d_u, d_rows, d_w_gate, d_w_up, d_w_down, s);
 }
 
 }  // namespace ep

@@ -27,6 +27,7 @@ enum class ExpertOp { kGateUp, kDown, kDGateUp, kDRows, kDWeight };
 constexpr int kGemmThreads = 192;
 constexpr int kGemmBK = 64;   // contraction per stage: 128 bytes of bf16, one swizzled row
 constexpr int kGemmBM = 128;  // rows of a CTA's tile: the TMEM lanes
+constexpr int kSlabBytes = 32 * 128;
 
 struct GemmParams {
     CUtensorMap a[3];    // K-major: box 64 k x 128 rows; MN-major: box 64 m x 64 k
@@ -55,7 +56,7 @@ struct GemmShape {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = 196608 / kStageBytes;
     static constexpr int kTmemCols = 2 * NB;
-    static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
+    static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + 4 * kSlabBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -68,20 +69,57 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 // exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-// Up to 32 results of one row: columns [n, n + 32) of N, N % 8 == 0.
-__device__ __forceinline__ void store_row_32(ep_bf16 *row, int n, int N, const uint32_t (&v)[16]) {
+// An epilogue warp's results lie one row to a thread, 64 columns at a time; they pass through a slab
+// of shared memory (32 rows of 128 bytes, 16-byte words swizzled by the row) so that global memory
+// is written, and read, in whole 128-byte lines: 8 threads to a row. Stores straight from the
+// registers touch 32 rows at once, 16 bytes of each, and took longer than the main loop of a short
+// contraction.
+
+// 32 values of this thread's row, columns 32 half ..: into the slab.
+__device__ __forceinline__ void slab_put(unsigned char *slab, int lane, int half, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (n + 8 * i < N)
-            st_v4(reinterpret_cast<uint4 *>(row + n + 8 * i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        *reinterpret_cast<uint4 *>(slab + lane * 128 + (((half * 4 + i) ^ (lane & 7)) * 16)) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-__device__ __forceinline__ void load_row_32(const ep_bf16 *row, int n, int N, uint32_t (&v)[16]) {
+__device__ __forceinline__ void slab_get(const unsigned char *slab, int lane, int half, uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (n + 8 * i < N) q = *reinterpret_cast<const uint4 *>(row + n + 8 * i);
+        const uint4 q = *reinterpret_cast<const uint4 *>(slab + lane * 128 + (((half * 4 + i) ^ (lane & 7)) * 16));
         v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
+}
+// The slab's first `rows` rows to columns [n, n + 64) of N, N % 8 == 0, of the rows from `base` on.
+__device__ __forceinline__ void slab_store(const unsigned char *slab, int lane, ep_bf16 *base, int N, int n, int rows) {
+    __syncwarp();
+    const int c = lane % 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = 4 * j + lane / 8;
+        if (r < rows && n + 8 * c < N)
+            st_v4(reinterpret_cast<uint4 *>(base + (size_t)r * N + n + 8 * c),
+                  *reinterpret_cast<const uint4 *>(slab + r * 128 + ((c ^ (r & 7)) * 16)));
+    }
+    __syncwarp();
+}
+// The other way round, as loads that are put into the slab once they are there (slab_fill).
+__device__ __forceinline__ void slab_load(uint4 (&q)[8], int lane, const ep_bf16 *base, int N, int n, int rows) {
+    const int c = lane % 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = 4 * j + lane / 8;
+        q[j] = r < rows && n + 8 * c < N ? *reinterpret_cast<const uint4 *>(base + (size_t)r * N + n + 8 * c)
+                                         : make_uint4(0, 0, 0, 0);
+    }
+}
+__device__ __forceinline__ void slab_fill(unsigned char *slab, int lane, const uint4 (&q)[8]) {
+    const int c = lane % 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = 4 * j + lane / 8;
+        *reinterpret_cast<uint4 *>(slab + r * 128 + ((c ^ (r & 7)) * 16)) = q[j];
+    }
+    __syncwarp();
 }
 
 // One tile of the kernel's list, the same for every warp.
@@ -159,25 +197,45 @@ __device__ __forceinline__ int a_rows_fetched(int valid) {
     return valid <= 0 ? 0 : valid > 96 ? kGemmBM : (valid + 15) / 16 * 16;
 }
 
+// DWeight: a stage whose rows go past the expert's end also holds rows of the next one, which
+// count for nothing: zeroed, in both operands, up to a whole step of 16. `left` rows are the
+// expert's. Returns the steps the stage takes. By one warp.
+template <typename Sh>
+__device__ __forceinline__ int zero_rows_past_end(unsigned char *stage, int left, int lane) {
+    if (left >= kGemmBK) return kGemmBK / 16;
+    const int steps = (left + 15) / 16;
+    const int zero = (steps * 16 - left) * 8;  // 16-byte words of a 64-wide column block
+    for (int i = lane; i < (kGemmBM + Sh::kBRows) / 64 * zero; i += 32)
+        reinterpret_cast<uint4 *>(stage + i / zero * 8192 + left * 128)[i % zero] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    return steps;
+}
+
 template <ExpertOp OP, int CG, int NB>
 __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __grid_constant__ GemmParams p) {
     using Sh = GemmShape<OP, CG, NB>;
-    static_assert(!(Sh::kDW && CG == 2), "the rows past an expert's end are zeroed by the issuing CTA alone");
     constexpr int kStages = Sh::kStages;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    // CG = 2: both CTAs' copies report to the first CTA's `full`. Only the last stage of a DWeight
+    // tile, when it goes past the expert's end, differs: the second CTA's copies report to its own
+    // `full`, it zeroes those rows and arrives on the first one's `other`. Both barriers of a stage
+    // count such uses alone, so their parities are kept as bits, one a stage.
+    constexpr bool kRelay = Sh::kDW && CG == 2;
+    __shared__ uint64_t full[kStages], empty[kStages], other[kStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_addr;
     __shared__ volatile int failed;
 
     unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    int64_t *prefix = reinterpret_cast<int64_t *>(stages + kStages * Sh::kStageBytes);
+    unsigned char *slabs = stages + kStages * Sh::kStageBytes;
+    int64_t *prefix = reinterpret_cast<int64_t *>(slabs + 4 * kSlabBytes);
     int *lo = reinterpret_cast<int *>(prefix + p.E + 1), *count = lo + p.E;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0;
 
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1), mbar_init(&other[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4 * CG);
         mbar_init(&drained, 1);
         failed = 0;
@@ -221,14 +279,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
     if (warp == 0) {
         // ---- producer: one lane fetches the stages of every tile in turn
         if (lane == 0) {
-            uint32_t it = 0;
+            uint32_t it = 0, relayed = 0, ever = 0;
             bool ok = true;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
                 const int fetched = Sh::kDW ? 0 : a_rows_fetched(t.valid - (int)rank * kGemmBM);
                 uint32_t bytes = Sh::kBBytes * CG;
                 if constexpr (Sh::kDW)
-                    bytes += Sh::kABytes;
+                    bytes += Sh::kABytes * CG;
                 else
                     for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * kGemmBM) * 128;
                 for (int b = 0; b < kb; ++b, ++it) {
@@ -237,17 +295,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                    const uint32_t bar = CG == 2 ? cluster_smem_u32(&full[s], 0) : smem_u32(&full[s]);
+                    const bool relay = kRelay && t.rows - b * kGemmBK < kGemmBK;
+                    if (rank == 0 || relay) mbar_arrive_expect_tx(&full[s], relay ? bytes / 2 : bytes);
+                    if (relay) relayed ^= 1u << s, ever |= 1u << s;
+                    const uint32_t bar = CG == 2 && !relay ? cluster_smem_u32(&full[s], 0) : smem_u32(&full[s]);
                     unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
                     if constexpr (Sh::kDW) {
                         const int k = t.row0 + b * kGemmBK;
 #pragma unroll
                         for (int i = 0; i < kGemmBM / 64; ++i)
-                            tma_load_2d<CG>(sa + i * 8192, &p.a[t.problem], t.m0 + 64 * i, k, bar);
+                            tma_load_2d<CG>(sa + i * 8192, &p.a[t.problem], t.m0 + (int)rank * kGemmBM + 64 * i, k, bar);
 #pragma unroll
                         for (int i = 0; i < Sh::kBRows / 64; ++i)
-                            tma_load_2d<CG>(sb + i * 8192, &p.b[t.problem], t.n0 + 64 * i, k, bar);
+                            tma_load_2d<CG>(sb + i * 8192, &p.b[t.problem], t.n0 + (int)rank * Sh::kBRows + 64 * i, k, bar);
                     } else {
                         const int half = OP == ExpertOp::kDRows && b >= kb / 2 ? 1 : 0;
                         const int k = (half ? b - kb / 2 : b) * kGemmBK;
@@ -276,26 +336,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 }
             }
             // no copy may be under way when the CTA ends: after a failure nobody else waits for them
-            if (failed && rank == 0)
-                for (int i = 0; i < kStages; ++i)
-                    if (it > (uint32_t)i) {
+            if (failed) {
+                for (int i = 0; i < kStages; ++i) {
+                    int never = 0;
+                    if (rank == 0 && it > (uint32_t)i) {
                         const uint32_t last = (it - 1 - i) / kStages;  // how often stage i was filled again
-                        int never = 0;
                         mbar_wait_limited(&full[i], last & 1, &never);
                     }
+                    if (rank == 1 && (ever >> i & 1)) mbar_wait_limited(&full[i], (relayed >> i & 1) ^ 1, &never);
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer (CG = 2: of the pair's first CTA)
         if (rank == 0) {
             constexpr uint32_t idesc = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
-            uint32_t it = 0, acc_it = 0;
+            uint32_t it = 0, acc_it = 0, relayed = 0;
             bool ok = true;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
                 if (kb == 0) continue;
                 const uint32_t slot = acc_it & 1;
-                if (acc_it >= 2 && !mbar_wait_limited(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed)) break;
+                if (acc_it >= 2 && !mbar_wait_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed)) break;
                 ++acc_it;
                 tmem_fence_after();
                 const uint32_t d = tmem + slot * NB;
@@ -307,18 +370,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     }
                     unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
                     int steps = kGemmBK / 16;
-                    if constexpr (Sh::kDW) {
-                        // the last stage also holds rows of the next expert: they count for nothing
-                        const int left = t.rows - b * kGemmBK;
-                        if (left < kGemmBK) {
-                            steps = (left + 15) / 16;
-                            const int zero = (steps * 16 - left) * 8;  // 16-byte words of a 64-wide column block
-                            for (int i = lane; i < (kGemmBM + Sh::kBRows) / 64 * zero; i += 32)
-                                reinterpret_cast<uint4 *>(sa + i / zero * 8192 + left * 128)[i % zero] = make_uint4(0, 0, 0, 0);
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
+                    if constexpr (Sh::kDW) steps = zero_rows_past_end<Sh>(sa, t.rows - b * kGemmBK, lane);
+                    if constexpr (kRelay)
+                        if (t.rows - b * kGemmBK < kGemmBK) {
+                            if (!mbar_wait_limited<true>(&other[s], relayed >> s & 1, &failed)) {
+                                ok = false;
+                                break;
+                            }
+                            relayed ^= 1u << s;
                         }
-                    }
                     tmem_fence_after();
                     if (lane == 0) {
                         const uint64_t da = smem_desc(smem_u32(sa), Sh::kAMn ? 8192 : 16);
@@ -337,11 +397,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 int never = 0;
                 mbar_wait_limited(&drained, 0, &never);
             }
+        } else if (kRelay) {
+            // the pair's second CTA: its part of the stages that go past an expert's end
+            uint32_t it = 0, relayed = 0;
+            while (walk.next(t)) {
+                const int kb = walk.blocks(t);
+                it += kb;
+                if (t.rows % kGemmBK == 0) continue;
+                const int s = (it - 1) % kStages;
+                if (!mbar_wait_limited(&full[s], relayed >> s & 1, &failed)) break;
+                relayed ^= 1u << s;
+                zero_rows_past_end<Sh>(stages + s * Sh::kStageBytes, t.rows - (kb - 1) * kGemmBK, lane);
+                if (lane == 0) mbar_arrive_cluster(cluster_smem_u32(&other[s], 0));
+                __syncwarp();
+            }
         }
     } else {
         // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread
         const int quarter = warp % 4;
-        const int r = (int)rank * kGemmBM + quarter * 32 + lane;  // row within the tile
+        const int r0 = (int)rank * kGemmBM + quarter * 32;  // the warp's first row within the tile
+        unsigned char *slab = slabs + quarter * kSlabBytes;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         uint32_t acc_it = 0;
         while (walk.next(t)) {
@@ -352,73 +427,88 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 ++acc_it;
                 tmem_fence_after();
             }
-            const bool mine = r < t.valid;
-            const bool any = r - lane < t.valid;  // the same in the whole warp
+            const int rows = min(t.valid - r0, 32);  // of this warp's 32 that count
             const uint32_t src = tmem + lanes + slot * NB;
             const int N = p.N[t.problem];
-            if (any) {
-                const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r : (size_t)t.m0 + r;
-                for (int c = 0; c < Sh::kOutN && t.n0 + c < N; c += 32) {
-                    uint32_t v[32], o[16];
-                    if (!none) tmem_load_32(src + c, v);
-                    const int n = t.n0 + c;
-                    if constexpr (OP == ExpertOp::kGateUp) {
-                        uint32_t w[32];
-                        tmem_load_32(src + Sh::kOutN + c, w);
+            const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r0 : (size_t)t.m0 + r0;
+            for (int c = 0; rows > 0 && c < Sh::kOutN && t.n0 + c < N; c += 64) {
+                const int n = t.n0 + c;
+                if constexpr (OP == ExpertOp::kDGateUp) {
+                    uint4 gq[8], uq[8];
+                    slab_load(gq, lane, p.g + row * N, N, n, rows);
+                    slab_load(uq, lane, p.u + row * N, N, n, rows);
+                    uint32_t g[2][16], u[2][16];
+                    slab_fill(slab, lane, gq);
+                    slab_get(slab, lane, 0, g[0]);
+                    slab_get(slab, lane, 1, g[1]);
+                    __syncwarp();
+                    slab_fill(slab, lane, uq);
+                    slab_get(slab, lane, 0, u[0]);
+                    slab_get(slab, lane, 1, u[1]);
+                    __syncwarp();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[32], o[16];
+                        tmem_load_32(src + c + 32 * half, v);
                         tmem_wait_ld(v);
-                        tmem_wait_ld(w);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
-                            o[i] = bf16_pair(g0 * sigmoid(g0) * __uint_as_float(w[2 * i]),
-                                             g1 * sigmoid(g1) * __uint_as_float(w[2 * i + 1]));
-                        }
-                        if (mine) {
-                            store_row_32(p.out[0] + row * N, n, N, o);
-                            if (p.g) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                                store_row_32(p.g + row * N, n, N, o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] = bf16_pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-                                store_row_32(p.u + row * N, n, N, o);
-                            }
-                        }
-                    } else if constexpr (OP == ExpertOp::kDGateUp) {
-                        uint32_t g[16] = {}, u[16] = {};
-                        if (mine) {
-                            load_row_32(p.g + row * N, n, N, g);
-                            load_row_32(p.u + row * N, n, N, u);
-                        }
-                        tmem_wait_ld(v);
-                        uint32_t o2[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float dg[2], du[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const float dh = __uint_as_float(v[2 * i + k]);
-                                const float gg = k ? bf16_hi(g[i]) : bf16_lo(g[i]), uu = k ? bf16_hi(u[i]) : bf16_lo(u[i]);
+                                const float gg = k ? bf16_hi(g[half][i]) : bf16_lo(g[half][i]);
+                                const float uu = k ? bf16_hi(u[half][i]) : bf16_lo(u[half][i]);
                                 const float s = sigmoid(gg);
                                 du[k] = dh * gg * s;
                                 dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
                             }
                             o[i] = bf16_pair(dg[0], dg[1]);
-                            o2[i] = bf16_pair(du[0], du[1]);
+                            u[half][i] = bf16_pair(du[0], du[1]);
                         }
-                        if (mine) {
-                            store_row_32(p.out[0] + row * N, n, N, o);
-                            store_row_32(p.out[1] + row * N, n, N, o2);
+                        slab_put(slab, lane, half, o);
+                    }
+                    slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
+                    slab_put(slab, lane, 0, u[0]);
+                    slab_put(slab, lane, 1, u[1]);
+                    slab_store(slab, lane, p.out[1] + row * N, N, n, rows);
+                } else if constexpr (OP == ExpertOp::kGateUp) {
+                    // what: 0 h, 1 g, 2 u; each takes its columns from TMEM anew
+                    for (int what = 0; what < (p.g ? 3 : 1); ++what) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[32], w[32], o[16];
+                            tmem_load_32(src + c + 32 * half, v);
+                            tmem_load_32(src + Sh::kOutN + c + 32 * half, w);
+                            tmem_wait_ld(v);
+                            tmem_wait_ld(w);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
+                                const float u0 = __uint_as_float(w[2 * i]), u1 = __uint_as_float(w[2 * i + 1]);
+                                o[i] = what == 0   ? bf16_pair(g0 * sigmoid(g0) * u0, g1 * sigmoid(g1) * u1)
+                                       : what == 1 ? bf16_pair(g0, g1)
+                                                   : bf16_pair(u0, u1);
+                            }
+                            slab_put(slab, lane, half, o);
                         }
-                    } else {
-                        if (!none) tmem_wait_ld(v);
+                        ep_bf16 *out = what == 0 ? p.out[0] : what == 1 ? p.g : p.u;
+                        slab_store(slab, lane, out + row * N, N, n, rows);
+                    }
+                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[32], o[16];
+                        if (!none) {
+                            tmem_load_32(src + c + 32 * half, v);
+                            tmem_wait_ld(v);
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if (mine) store_row_32(p.out[t.problem] + row * N, n, N, o);
+                        slab_put(slab, lane, half, o);
                     }
+                    slab_store(slab, lane, p.out[t.problem] + row * N, N, n, rows);
                 }
             }
             if (!none) {

@@ -10,7 +10,7 @@ namespace ep {
 
 // A wait on an mbarrier that is not satisfied after this long gives up (ns). No wait of a
 // kernel that works comes near it: the longest one spans a single tile's main loop.
-constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ uint64_t global_timer_ns() {
     uint64_t t;
@@ -18,14 +18,29 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
+// mbar_try_wait that also sees what another CTA of the cluster wrote before it arrived.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits for the phase of `parity` to complete; false after kWaitLimitNs, or once another
 // warp of the CTA has given up (*failed).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t *bar, uint32_t parity, volatile int *failed) {
-    if (mbar_try_wait(bar, parity)) return true;
+    const auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (done()) return true;
     const uint64_t begin = global_timer_ns();
     for (;;) {
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (done()) return true;
         if (*failed || global_timer_ns() - begin > kWaitLimitNs) {
             *failed = 1;
             return false;
