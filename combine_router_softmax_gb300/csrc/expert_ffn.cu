@@ -69,19 +69,15 @@ cudaError_t launch(GemmParams &p, int64_t most_tiles, cudaStream_t s) {
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// An upper bound of a row product's tiles: every expert can end inside one.
-int64_t row_tiles(const GemmParams &p, int bm, int out_n) {
-    const int64_t m = (int64_t)p.S / bm + (p.E < p.S ? p.E : p.S);
-    return m * ((p.N[0] + out_n - 1) / out_n);
 }
 
 GemmParams base_params(const ep_ffn_config &c, const int32_t *expert_offset) {
@@ -92,36 +88,82 @@ GemmParams base_params(const ep_ffn_config &c, const int32_t *expert_offset) {
     return p;
 }
 
-template <int CG, int NB>
-cudaError_t run_forward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles of bm rows, at most: every expert that has rows can end inside one.
+int64_t row_tiles(const GemmParams &p, int bm) { return p.S / bm + (p.E < p.S ? p.E : p.S); }
+
+// Which tile a product takes. Few tiles leave SMs idle and make each one's epilogue a large part of
+// the whole, so below two tiles of 128 x 256 an SM they are 64 wide; with more than 128 rows an
+// expert a CTA pair takes 256 rows at once, which halves what each SM reads of the weights.
+enum class TileShape { kNarrow, kWide, kPair };
+TileShape choose(const GemmParams &p, int64_t wide_tiles) {
+    if (wide_tiles < 2 * (int64_t)current_device_sm_count()) return TileShape::kNarrow;
+    return p.S > (int64_t)kGemmBM * p.E ? TileShape::kPair : TileShape::kWide;
+}
+
+// rows x k of the row product's A: halves [0, n) of it.
+struct RowProduct {
+    const ep_bf16 *a[2], *b[2];
+};
+
+template <ExpertOp OP, int CG, int NB>
+cudaError_t run_rows(GemmParams &p, const RowProduct &r, cudaStream_t s) {
+    using Sh = GemmShape<OP, CG, NB>;
+    for (int i = 0; i < 2; ++i) {
+        if (r.a[i] && !rows_map(p, i, r.a[i], p.K)) return cudaErrorInvalidValue;
+        if (!r.b[i]) continue;
+        // weights [E, N, K], or [E, K, N] where the product contracts their rows
+        constexpr int kBoxN = OP == ExpertOp::kGateUp ? NB / 2 : Sh::kBRows;
+        const bool ok = Sh::kBMn ? make_map(&p.b[i], r.b[i], p.N[0], p.K, p.E, 64, kGemmBK)
+                                 : make_map(&p.b[i], r.b[i], p.K, p.N[0], p.E, kGemmBK, kBoxN);
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    return launch<OP, CG, NB>(p, row_tiles(p, kGemmBM * CG) * ceil_div(p.N[0], Sh::kOutN), s);
+}
+
+template <ExpertOp OP>
+cudaError_t row_product(GemmParams &p, const RowProduct &r, cudaStream_t s) {
+    const int64_t n = ceil_div(p.N[0], GemmShape<OP, 1, 256>::kOutN);
+    const int64_t m = p.S / kGemmBM > p.E ? p.S / kGemmBM : p.E < p.S ? p.E : p.S;
+    switch (choose(p, m * n)) {
+        case TileShape::kNarrow: return run_rows<OP, 1, 64>(p, r, s);
+        case TileShape::kWide: return run_rows<OP, 1, 256>(p, r, s);
+        default: return run_rows<OP, 2, 256>(p, r, s);
+    }
+}
+
+int64_t weight_tiles(const GemmParams &p, int bm, int bn) {
+    int64_t n = 0;
+    for (int i = 0; i < p.problems; ++i) n += ceil_div(p.M[i], bm) * ceil_div(p.N[i], bn);
+    return n * p.E;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                               const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
-                        ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
+                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
     GemmParams p = base_params(c, expert_offset);
     p.K = c.H;
     p.N[0] = c.I;
     p.out[0] = h;
     p.g = g;
     p.u = u;
-    if (!rows_map(p, 0, rows, c.H) || !make_map(&p.b[0], w_gate, c.H, c.I, c.E, kGemmBK, NB / 2) ||
-        !make_map(&p.b[1], w_up, c.H, c.I, c.E, kGemmBK, NB / 2))
-        return cudaErrorInvalidValue;
-    cudaError_t e = launch<ExpertOp::kGateUp, CG, NB>(p, row_tiles(p, kGemmBM * CG, NB / 2), s);
+    const cudaError_t e = row_product<ExpertOp::kGateUp>(p, {{rows}, {w_gate, w_up}}, s);
     if (e != cudaSuccess) return e;
-
     p = base_params(c, expert_offset);
     p.K = c.I;
     p.N[0] = c.H;
     p.out[0] = y;
-    if (!rows_map(p, 0, h, c.I) || !make_map(&p.b[0], w_down, c.I, c.H, c.E, kGemmBK, NB / CG)) return cudaErrorInvalidValue;
-    return launch<ExpertOp::kDown, CG, NB>(p, row_tiles(p, kGemmBM * CG, NB), s);
+    return row_product<ExpertOp::kDown>(p, {{h}, {w_down}}, s);
 }
 
-template <int CG, int NB>
-cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
+cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
                                        const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
                                        ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
-                         ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
+                                       ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
     GemmParams p = base_params(c, expert_offset);
     p.K = c.H;
     p.N[0] = c.I;
@@ -129,8 +171,7 @@ cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int3
     p.out[1] = d_u;
     p.g = const_cast<ep_bf16 *>(g);
     p.u = const_cast<ep_bf16 *>(u);
-    if (!rows_map(p, 0, d_y, c.H) || !make_map(&p.b[0], w_down, c.I, c.H, c.E, 64, kGemmBK)) return cudaErrorInvalidValue;
-    cudaError_t e = launch<ExpertOp::kDGateUp, CG, NB>(p, row_tiles(p, kGemmBM * CG, NB), s);
+    cudaError_t e = row_product<ExpertOp::kDGateUp>(p, {{d_y}, {w_down}}, s);
     if (e != cudaSuccess) return e;
 
     if (d_rows) {
@@ -138,10 +179,7 @@ cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int3
         p.K = c.I;
         p.N[0] = c.H;
         p.out[0] = d_rows;
-        if (!rows_map(p, 0, d_g, c.I) || !rows_map(p, 1, d_u, c.I) ||
-            !make_map(&p.b[0], w_gate, c.H, c.I, c.E, 64, kGemmBK) || !make_map(&p.b[1], w_up, c.H, c.I, c.E, 64, kGemmBK))
-            return cudaErrorInvalidValue;
-        e = launch<ExpertOp::kDRows, CG, NB>(p, row_tiles(p, kGemmBM * CG, NB), s);
+        e = row_product<ExpertOp::kDRows>(p, {{d_g, d_u}, {w_gate, w_up}}, s);
         if (e != cudaSuccess) return e;
     }
 
@@ -151,7 +189,6 @@ cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int3
         int32_t M, N;
         ep_bf16 *out;
     } want[3] = {{d_y, h, c.H, c.I, d_w_down}, {d_g, rows, c.I, c.H, d_w_gate}, {d_u, rows, c.I, c.H, d_w_up}};
-    int64_t tiles = 0;
     for (const auto &w : want) {
         if (!w.out) continue;
         const int i = p.problems++;
@@ -160,30 +197,13 @@ cudaError_t run_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int3
         p.out[i] = w.out;
         if (!make_map(&p.a[i], w.a, w.M, p.S, 0, 64, kGemmBK) || !make_map(&p.b[i], w.b, w.N, p.S, 0, 64, kGemmBK))
             return cudaErrorInvalidValue;
-        tiles += (int64_t)c.E * ((w.M + kGemmBM * CG - 1) / (kGemmBM * CG)) * ((w.N + NB - 1) / NB);
     }
-    return p.problems ? launch<ExpertOp::kDWeight, CG, NB>(p, tiles, s) : cudaSuccess;
-}
-
-// A CTA pair takes tiles of 256 rows: worth it once an expert has more than one tile of 128.
-bool pairs(const ep_ffn_config &c) { return c.rows > (int64_t)kGemmBM * c.E; }
-
-}  // namespace
-
-cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
-                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
-                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
-    const auto run = pairs(c) ? run_forward<2, 256> : run_forward<1, 256>;
-    return run(c, rows, expert_offset, w_gate, w_up, w_down, g, u, h, y, s);
-}
-
-cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
-                                       const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
-                                       const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
-                                       ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
-                                       ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
-    const auto run = pairs(c) ? run_backward<2, 256> : run_backward<1, 256>;
-    return run(c, rows, expert_offset, w_gate, w_up, w_down, g, u, h, d_y, d_g, d_u, d_rows, d_w_gate, d_w_up, d_w_down, s);
+    if (p.problems == 0) return cudaSuccess;
+    switch (choose(p, weight_tiles(p, kGemmBM, 256))) {
+        case TileShape::kNarrow: return launch<ExpertOp::kDWeight, 1, 64>(p, weight_tiles(p, kGemmBM, 64), s);
+        case TileShape::kWide: return launch<ExpertOp::kDWeight, 1, 256>(p, weight_tiles(p, kGemmBM, 256), s);
+        default: return launch<ExpertOp::kDWeight, 2, 256>(p, weight_tiles(p, 2 * kGemmBM, 256), s);
+    }
 }
 
 }  // namespace ep

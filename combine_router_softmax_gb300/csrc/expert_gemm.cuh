@@ -50,6 +50,7 @@ struct GemmShape {
     static constexpr bool kAMn = kDW;
     static constexpr bool kBMn = OP == ExpertOp::kDGateUp || OP == ExpertOp::kDRows || kDW;
     static constexpr int kOutN = OP == ExpertOp::kGateUp ? NB / 2 : NB;  // output columns of a tile
+    static constexpr int kCols = kOutN < 64 ? kOutN : 64;  // columns the epilogue takes at a time
     static constexpr int kBRows = NB / CG;                               // B rows a CTA holds
     static constexpr int kABytes = kGemmBM * 128;
     static constexpr int kBBytes = kBRows * 128;
@@ -89,20 +90,21 @@ __device__ __forceinline__ void slab_get(const unsigned char *slab, int lane, in
         v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
 }
-// The slab's first `rows` rows to columns [n, n + 64) of N, N % 8 == 0, of the rows from `base` on.
+// The slab's first `rows` rows to columns [n, n + COLS) of N, N % 8 == 0, of the rows from `base` on.
+template <int COLS>
 __device__ __forceinline__ void slab_store(const unsigned char *slab, int lane, ep_bf16 *base, int N, int n, int rows) {
     __syncwarp();
     const int c = lane % 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int r = 4 * j + lane / 8;
-        if (r < rows && n + 8 * c < N)
+        if (r < rows && 8 * c < COLS && n + 8 * c < N)
             st_v4(reinterpret_cast<uint4 *>(base + (size_t)r * N + n + 8 * c),
                   *reinterpret_cast<const uint4 *>(slab + r * 128 + ((c ^ (r & 7)) * 16)));
     }
     __syncwarp();
 }
-// The other way round, as loads that are put into the slab once they are there (slab_fill).
+// The other way round (64 columns), as loads that are put into the slab once they are there (slab_fill).
 __device__ __forceinline__ void slab_load(uint4 (&q)[8], int lane, const ep_bf16 *base, int N, int n, int rows) {
     const int c = lane % 8;
 #pragma unroll
@@ -244,6 +246,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
         tma_prefetch_map(&p.b[0]);
     }
     if (warp == 1) tmem_alloc<CG>(&tmem_addr, Sh::kTmemCols);
+    grid_dependency_wait();
+    grid_launch_dependents();
     // bounds come from device memory: kept inside the row buffer whatever they hold
     for (int e = threadIdx.x; e < p.E; e += kGemmThreads) {
         const int first = min(max(p.expert_offset[e], 0), p.S);
@@ -278,9 +282,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
 
     if (warp == 0) {
         // ---- producer: one lane fetches the stages of every tile in turn
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0, relayed = 0, ever = 0;
-            bool ok = true;
+            bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
                 const int fetched = Sh::kDW ? 0 : a_rows_fetched(t.valid - (int)rank * kGemmBM);
@@ -291,10 +295,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * kGemmBM) * 128;
                 for (int b = 0; b < kb; ++b, ++it) {
                     const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait_limited(&empty[s], (it / kStages - 1) & 1, &failed)) {
+                    if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], (it / kStages - 1) & 1, &failed)) {
                         ok = false;
                         break;
                     }
+                    ready = it + 1 >= kStages && mbar_test(&empty[(it + 1) % kStages], ((it + 1) / kStages - 1) & 1);
                     const bool relay = kRelay && t.rows - b * kGemmBK < kGemmBK;
                     if (rank == 0 || relay) mbar_arrive_expect_tx(&full[s], relay ? bytes / 2 : bytes);
                     if (relay) relayed ^= 1u << s, ever |= 1u << s;
@@ -353,46 +358,54 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
         if (rank == 0) {
             constexpr uint32_t idesc = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
             uint32_t it = 0, acc_it = 0, relayed = 0;
-            bool ok = true;
+            bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
                 if (kb == 0) continue;
                 const uint32_t slot = acc_it & 1;
-                if (acc_it >= 2 && !mbar_wait_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed)) break;
-                ++acc_it;
-                tmem_fence_after();
                 const uint32_t d = tmem + slot * NB;
-                for (int b = 0; b < kb; ++b, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait_limited(&full[s], (it / kStages) & 1, &failed)) {
-                        ok = false;
-                        break;
+                // the stage's MMAs; one thread
+                const auto issue = [&](uint32_t s, int steps, int b) {
+                    const uint32_t sa = smem_u32(stages + s * Sh::kStageBytes);
+                    const uint64_t da = smem_desc(sa, Sh::kAMn ? 8192 : 16);
+                    const uint64_t db = smem_desc(sa + Sh::kABytes, Sh::kBMn ? 8192 : 16);
+                    for (int k = 0; k < steps; ++k)
+                        mma_bf16<CG>(d, da + k * (Sh::kAMn ? 128 : 2), db + k * (Sh::kBMn ? 128 : 2), idesc, b + k > 0);
+                    mma_commit<CG>(&empty[s]);
+                    if (b == kb - 1) mma_commit<CG>(&acc_full[slot]);
+                };
+                const int whole = Sh::kDW ? t.rows / kGemmBK : kb;  // stages without a row past the expert's end
+                if (elect_one()) {
+                    if (acc_it >= 2) ok = mbar_poll_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed);
+                    tmem_fence_after();
+                    for (int b = 0; ok && b < whole; ++b) {
+                        const uint32_t i = it + b, s = i % kStages;
+                        ok = ready || mbar_poll_limited(&full[s], (i / kStages) & 1, &failed);
+                        ready = mbar_test(&full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
+                        if (ok) issue(s, kGemmBK / 16, b);
                     }
-                    unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
-                    int steps = kGemmBK / 16;
-                    if constexpr (Sh::kDW) steps = zero_rows_past_end<Sh>(sa, t.rows - b * kGemmBK, lane);
-                    if constexpr (kRelay)
-                        if (t.rows - b * kGemmBK < kGemmBK) {
-                            if (!mbar_wait_limited<true>(&other[s], relayed >> s & 1, &failed)) {
-                                ok = false;
-                                break;
-                            }
+                }
+                __syncwarp();
+                if constexpr (Sh::kDW)
+                    if (whole < kb) {
+                        const uint32_t s = (it + whole) % kStages;
+                        ready = false;
+                        // every lane waits: each is to see the copies that it zeroes a part of
+                        ok = !failed && mbar_wait_limited(&full[s], ((it + whole) / kStages) & 1, &failed);
+                        const int steps = zero_rows_past_end<Sh>(stages + s * Sh::kStageBytes, t.rows - whole * kGemmBK, lane);
+                        if (kRelay && ok) {
+                            ok = mbar_wait_limited<true>(&other[s], relayed >> s & 1, &failed);
                             relayed ^= 1u << s;
                         }
-                    tmem_fence_after();
-                    if (lane == 0) {
-                        const uint64_t da = smem_desc(smem_u32(sa), Sh::kAMn ? 8192 : 16);
-                        const uint64_t db = smem_desc(smem_u32(sb), Sh::kBMn ? 8192 : 16);
-                        for (int k = 0; k < steps; ++k)
-                            mma_bf16<CG>(d, da + k * (Sh::kAMn ? 128 : 2), db + k * (Sh::kBMn ? 128 : 2), idesc, b + k > 0);
-                        mma_commit<CG>(&empty[s]);
-                        if (b == kb - 1) mma_commit<CG>(&acc_full[slot]);
+                        if (elect_one() && ok) issue(s, steps, whole);
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
+                ok = !failed;
+                it += kb;
+                ++acc_it;
             }
             if (failed) {  // MMAs may still read the stages and write TMEM
-                if (lane == 0) mma_commit<CG>(&drained);
+                if (elect_one()) mma_commit<CG>(&drained);
                 __syncwarp();
                 int never = 0;
                 mbar_wait_limited(&drained, 0, &never);
@@ -423,7 +436,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
             const bool none = walk.blocks(t) == 0;
             const uint32_t slot = acc_it & 1;
             if (!none) {
-                if (!mbar_wait_limited(&acc_full[slot], (acc_it / 2) & 1, &failed)) break;
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait_limited(&acc_full[slot], (acc_it / 2) & 1, &failed);
+                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 ++acc_it;
                 tmem_fence_after();
             }
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
             const uint32_t src = tmem + lanes + slot * NB;
             const int N = p.N[t.problem];
             const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r0 : (size_t)t.m0 + r0;
-            for (int c = 0; rows > 0 && c < Sh::kOutN && t.n0 + c < N; c += 64) {
+            for (int c = 0; rows > 0 && c < Sh::kOutN && t.n0 + c < N; c += Sh::kCols) {
                 const int n = t.n0 + c;
                 if constexpr (OP == ExpertOp::kDGateUp) {
                     uint4 gq[8], uq[8];
@@ -468,15 +483,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                         }
                         slab_put(slab, lane, half, o);
                     }
-                    slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
+                    slab_store<Sh::kCols>(slab, lane, p.out[0] + row * N, N, n, rows);
                     slab_put(slab, lane, 0, u[0]);
                     slab_put(slab, lane, 1, u[1]);
-                    slab_store(slab, lane, p.out[1] + row * N, N, n, rows);
+                    slab_store<Sh::kCols>(slab, lane, p.out[1] + row * N, N, n, rows);
                 } else if constexpr (OP == ExpertOp::kGateUp) {
                     // what: 0 h, 1 g, 2 u; each takes its columns from TMEM anew
                     for (int what = 0; what < (p.g ? 3 : 1); ++what) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
+                        for (int half = 0; half < Sh::kCols / 32; ++half) {
                             uint32_t v[32], w[32], o[16];
                             tmem_load_32(src + c + 32 * half, v);
                             tmem_load_32(src + Sh::kOutN + c + 32 * half, w);
@@ -493,11 +508,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                             slab_put(slab, lane, half, o);
                         }
                         ep_bf16 *out = what == 0 ? p.out[0] : what == 1 ? p.g : p.u;
-                        slab_store(slab, lane, out + row * N, N, n, rows);
+                        slab_store<Sh::kCols>(slab, lane, out + row * N, N, n, rows);
                     }
                 } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int half = 0; half < Sh::kCols / 32; ++half) {
                         uint32_t v[32], o[16];
                         if (!none) {
                             tmem_load_32(src + c + 32 * half, v);
@@ -508,7 +523,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                             o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                         slab_put(slab, lane, half, o);
                     }
-                    slab_store(slab, lane, p.out[t.problem] + row * N, N, n, rows);
+                    slab_store<Sh::kCols>(slab, lane, p.out[t.problem] + row * N, N, n, rows);
                 }
             }
             if (!none) {

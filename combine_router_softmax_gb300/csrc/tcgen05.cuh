@@ -8,44 +8,101 @@
 
 namespace ep {
 
-// A wait on an mbarrier that is not satisfied after this long gives up (ns). No wait of a
-// kernel that works comes near it: the longest one spans a single tile's main loop.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// mbarrier.try_wait puts the thread to sleep until the phase completes, for kWaitSliceNs at most.
+// (Polled without that hint, by the epilogue's warps above all, the waits slowed the whole CTA: a
+// block of 8 rows took 91 us.) A wait that is not satisfied after kWaitSlices of them, about two
+// seconds, gives up; no wait of a kernel that works comes near it.
+constexpr uint32_t kWaitSliceNs = 2000000;
+constexpr int kWaitSlices = 1000;
+constexpr int64_t kPollLimitCycles = 4000000000ll;  // the same for a thread that polls
 
-__device__ __forceinline__ uint64_t global_timer_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// mbar_try_wait that also sees what another CTA of the cluster wrote before it arrived.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+// CLUSTER: what another CTA of the cluster wrote before it arrived is seen as well.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSliceNs)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSliceNs)
+            : "memory");
     return ok != 0;
 }
 
-// Waits for the phase of `parity` to complete; false after kWaitLimitNs, or once another
-// warp of the CTA has given up (*failed).
+// Waits for the phase of `parity` to complete; false when it did not in time, or once another warp
+// of the CTA has given up (*failed).
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t *bar, uint32_t parity, volatile int *failed) {
-    const auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (done()) return true;
-    const uint64_t begin = global_timer_ns();
+    for (int i = 0; i < kWaitSlices; ++i) {
+        if (mbar_sleep_wait<CLUSTER>(bar, parity)) return true;
+        if (*failed) return false;
+    }
+    *failed = 1;
+    return false;
+}
+
+// Whether the phase of `parity` is complete by now. A loop over stages asks for the next one before it
+// works on the present one, so that the answer's latency is behind that work.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    return ok != 0;
+}
+
+// mbar_wait_limited for one thread whose waits are short and on the path of every stage: it polls, as a
+// thread that sleeps is woken late.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_poll_limited(uint64_t *bar, uint32_t parity, volatile int *failed) {
+    int64_t begin = 0;
     for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (done()) return true;
-        if (*failed || global_timer_ns() - begin > kWaitLimitNs) {
+        for (int i = 0; i < 1024; ++i)
+            if (mbar_test<CLUSTER>(bar, parity)) return true;
+        const int64_t now = clock64();
+        if (begin == 0) begin = now;
+        if (*failed || now - begin > kPollLimitCycles) {
             *failed = 1;
             return false;
         }
     }
+}
+
+// True in one lane of the warp, all of which are active. The compiler knows of this predicate that
+// one lane alone passes: the instructions below take uniform operands, and behind an ordinary
+// `lane == 0` each of them becomes a loop over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
 }
 
 // The address of `p`, a shared-memory address of this CTA, in the cluster's CTA `rank`.
