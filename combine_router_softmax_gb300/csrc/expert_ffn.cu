@@ -1,6 +1,7 @@
 // expert_ffn.cu -- launchers of the experts' gated block, forward and backward
 // (the kernel: expert_gemm.cuh).
 #include "expert_gemm.cuh"
+#include "expert_stream.cuh"
 
 namespace ep {
 
@@ -34,22 +35,25 @@ EncodeTiled encoder() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A bf16 matrix [y][x], or [z][y][x], read in boxes of bx by by elements, 128-byte swizzled.
-// What lies outside reads as zero.
-bool make_map(CUtensorMap *m, const ep_bf16 *base, int64_t x, int64_t y, int64_t z, int bx, int by) {
+}  // namespace
+
+bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by) {
     EncodeTiled encode = encoder();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
-    const cuuint64_t strides[2] = {(cuuint64_t)x * 2, (cuuint64_t)x * (cuuint64_t)y * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)x * bytes, (cuuint64_t)x * (cuuint64_t)y * bytes};
     const cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1}, ones[3] = {1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z > 0 ? 3 : 2, const_cast<ep_bf16 *>(base), dims, strides, box,
-                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, z > 0 ? 3 : 2,
+                  const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
 // A operand of a row product: rows x k.
 bool rows_map(GemmParams &p, int i, const ep_bf16 *base, int64_t k) {
-    return make_map(&p.a[i], base, k, p.S, 0, kGemmBK, kGemmBM) && make_map(&p.a16[i], base, k, p.S, 0, kGemmBK, 16);
+    return make_map(&p.a[i], base, 2, k, p.S, 0, kGemmBK, kGemmBM) && make_map(&p.a16[i], base, 2, k, p.S, 0, kGemmBK, 16);
 }
 
 template <ExpertOp OP, int CG, int NB>
@@ -93,14 +97,25 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row tiles of bm rows, at most: every expert that has rows can end inside one.
 int64_t row_tiles(const GemmParams &p, int bm) { return p.S / bm + (p.E < p.S ? p.E : p.S); }
 
-// Which tile a product takes. Few tiles leave SMs idle and make each one's epilogue a large part of
-// the whole, so below two tiles of 128 x 256 an SM they are 64 wide; with more than 128 rows an
-// expert a CTA pair takes 256 rows at once, which halves what each SM reads of the weights.
-enum class TileShape { kNarrow, kWide, kPair };
-TileShape choose(const GemmParams &p, int64_t wide_tiles) {
-    if (wide_tiles < 2 * (int64_t)current_device_sm_count()) return TileShape::kNarrow;
-    return p.S > (int64_t)kGemmBM * p.E ? TileShape::kPair : TileShape::kWide;
+// Which tile a product takes: the narrowest whose tiles are all resident at once, as a narrower one
+// gives each SM less and ends sooner (8 experts x 128 rows, 2048 to 1024 and back, forward: 64 wide
+// 35 us, 128 wide 30, 256 wide 37; at half the experts 21, 22, 30; at twice the rows 57, 42, 37). With
+// more tiles than SMs, 256 wide, and by CTA pairs of 256 rows where an expert has more than
+// `pair_rows`: a pair halves what each SM reads of the weights (16 experts, 2048 to 1024 and back,
+// forward: 200 rows each 63 us single, 59 pairs; 512 rows 106 and 90).
+enum class TileShape { k64, k128, k256, kPair };
+template <typename Tiles>
+TileShape choose(const GemmParams &p, int pair_rows, Tiles tiles) {
+    const int64_t sms = current_device_sm_count();
+    if (tiles(64) <= sms) return TileShape::k64;
+    if (tiles(128) <= sms) return TileShape::k128;
+    return tiles(256) > sms && p.S > (int64_t)pair_rows * p.E ? TileShape::kPair : TileShape::k256;
 }
+
+// Few rows: the weights are streamed past the rows' registers (expert_stream.cuh), 5% faster than tiles
+// (8 experts with one row each, 4096 to 1024: 39 us against 41). Up to as many rows as one pass takes;
+// with more, an expert that has most of them would be streamed again and again.
+bool streams(const ep_ffn_config &c) { return c.rows <= kStreamTokens; }
 
 // rows x k of the row product's A: halves [0, n) of it.
 struct RowProduct {
@@ -115,8 +130,8 @@ cudaError_t run_rows(GemmParams &p, const RowProduct &r, cudaStream_t s) {
         if (!r.b[i]) continue;
         // weights [E, N, K], or [E, K, N] where the product contracts their rows
         constexpr int kBoxN = OP == ExpertOp::kGateUp ? NB / 2 : Sh::kBRows;
-        const bool ok = Sh::kBMn ? make_map(&p.b[i], r.b[i], p.N[0], p.K, p.E, 64, kGemmBK)
-                                 : make_map(&p.b[i], r.b[i], p.K, p.N[0], p.E, kGemmBK, kBoxN);
+        const bool ok = Sh::kBMn ? make_map(&p.b[i], r.b[i], 2, p.N[0], p.K, p.E, 64, kGemmBK)
+                                 : make_map(&p.b[i], r.b[i], 2, p.K, p.N[0], p.E, kGemmBK, kBoxN);
         if (!ok) return cudaErrorInvalidValue;
     }
     return launch<OP, CG, NB>(p, row_tiles(p, kGemmBM * CG) * ceil_div(p.N[0], Sh::kOutN), s);
@@ -124,11 +139,12 @@ cudaError_t run_rows(GemmParams &p, const RowProduct &r, cudaStream_t s) {
 
 template <ExpertOp OP>
 cudaError_t row_product(GemmParams &p, const RowProduct &r, cudaStream_t s) {
-    const int64_t n = ceil_div(p.N[0], GemmShape<OP, 1, 256>::kOutN);
+    constexpr int kPerColumn = 256 / GemmShape<OP, 1, 256>::kOutN;  // accumulator columns of an output column
     const int64_t m = p.S / kGemmBM > p.E ? p.S / kGemmBM : p.E < p.S ? p.E : p.S;
-    switch (choose(p, m * n)) {
-        case TileShape::kNarrow: return run_rows<OP, 1, 64>(p, r, s);
-        case TileShape::kWide: return run_rows<OP, 1, 256>(p, r, s);
+    switch (choose(p, kGemmBM, [&](int width) { return m * ceil_div((int64_t)p.N[0] * kPerColumn, width); })) {
+        case TileShape::k64: return run_rows<OP, 1, 64>(p, r, s);
+        case TileShape::k128: return run_rows<OP, 1, 128>(p, r, s);
+        case TileShape::k256: return run_rows<OP, 1, 256>(p, r, s);
         default: return run_rows<OP, 2, 256>(p, r, s);
     }
 }
@@ -144,6 +160,23 @@ int64_t weight_tiles(const GemmParams &p, int bm, int bn) {
 cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                               const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
                               ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
+    if (!g && streams(c)) {
+        StreamParams q = {};
+        q.x = rows;
+        q.expert_offset = expert_offset;
+        q.y = h;
+        q.S = c.rows;
+        q.N = c.I;
+        q.K = c.H;
+        q.E = c.E;
+        const cudaError_t e = launch_stream<true, 0>(q, w_gate, w_up, s);
+        if (e != cudaSuccess) return e;
+        q.x = h;
+        q.y = y;
+        q.N = c.H;
+        q.K = c.I;
+        return launch_stream<false, 0>(q, w_down, nullptr, s);
+    }
     GemmParams p = base_params(c, expert_offset);
     p.K = c.H;
     p.N[0] = c.I;
@@ -195,14 +228,17 @@ cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *ro
         p.M[i] = w.M;
         p.N[i] = w.N;
         p.out[i] = w.out;
-        if (!make_map(&p.a[i], w.a, w.M, p.S, 0, 64, kGemmBK) || !make_map(&p.b[i], w.b, w.N, p.S, 0, 64, kGemmBK))
+        if (!make_map(&p.a[i], w.a, 2, w.M, p.S, 0, 64, kGemmBK) || !make_map(&p.b[i], w.b, 2, w.N, p.S, 0, 64, kGemmBK))
             return cudaErrorInvalidValue;
     }
     if (p.problems == 0) return cudaSuccess;
-    switch (choose(p, weight_tiles(p, kGemmBM, 256))) {
-        case TileShape::kNarrow: return launch<ExpertOp::kDWeight, 1, 64>(p, weight_tiles(p, kGemmBM, 64), s);
-        case TileShape::kWide: return launch<ExpertOp::kDWeight, 1, 256>(p, weight_tiles(p, kGemmBM, 256), s);
-        default: return launch<ExpertOp::kDWeight, 2, 256>(p, weight_tiles(p, 2 * kGemmBM, 256), s);
+    // the epilogue is a large part of these tiles: between 64 and 256 wide there is nothing to gain, and
+    // pairs, which share it less evenly, pay later (2048 x 1024, 16 experts: 256 rows each 64 us single,
+    // 87 pairs; 512 rows 98 and 92)
+    switch (choose(p, 3 * kGemmBM, [&](int width) { return weight_tiles(p, kGemmBM, width < 128 ? 64 : 256); })) {
+        case TileShape::k64: return launch<ExpertOp::kDWeight, 1, 64>(p, weight_tiles(p, kGemmBM, 64), s);
+        case TileShape::kPair: return launch<ExpertOp::kDWeight, 2, 256>(p, weight_tiles(p, 2 * kGemmBM, 256), s);
+        default: return launch<ExpertOp::kDWeight, 1, 256>(p, weight_tiles(p, kGemmBM, 256), s);
     }
 }
 

@@ -1,0 +1,356 @@
+// expert_stream.cuh -- products of few rows with the experts' weights: the weights are streamed once.
+//
+// y[s, n] = sum_k x[s, k] w[e, n, k], e the expert that owns row s, and the gated block's first half
+// silu(g) u from two such products. For single tokens the weights are the traffic (N K values of
+// every expert that has rows, against 2 rows N K operations), so what counts is to keep enough of
+// them on their way: one producer thread per CTA fetches stages of 128 weight rows x 256 bytes by TMA
+// into a ring of four (128 KB, so 19 MB on the GPU; HBM needs about 10 MB under way), on across work
+// items. Sixteen warps consume a stage: warp (m, half) takes 16 weight rows and half of the stage's k.
+//
+// The product is the matrix instruction m16n8k16 with the weights as its 16 rows and 8 rows of x as
+// its columns. Which k a lane's register stands for is free as long as both operands agree, so a
+// lane takes 8 consecutive k of a row of x, 16 bytes, and the same 8 k of its two weight rows.
+//
+// Weights are bf16, or 4 bits with one bf16 scale for G consecutive k. There a nibble v becomes the
+// bf16 value 128 + v by setting the bits 0x4300 over it (bf16 has 7 bits of fraction, so at 128 its
+// step is 1): one logic operation for two nibbles; minus 136 gives v - 8, exactly. Products with
+// bf16 activations are exact in fp32; a group is summed in fp32 and scaled once as a whole.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "tcgen05.cuh"
+
+namespace ep {
+
+constexpr int kStreamWarps = 16;                      // consumers
+constexpr int kStreamThreads = (kStreamWarps + 1) * 32;
+constexpr int kStreamRows = 128;                      // weight rows of a work item (gated: 64 of either projection)
+constexpr int kStreamBox = kStreamRows * 128;         // bytes of 128 bytes of every row: a stage has two
+constexpr int kStreamStageBytes = 2 * kStreamBox;
+constexpr int kStreamStages = 4;
+constexpr int kStreamTokens = 16;                     // rows of x that one pass over the weights serves
+
+struct StreamParams {
+    CUtensorMap w[2];         // [E][N][bytes of a row], boxes of 128 bytes x 64 or 128 rows, swizzled
+    const ep_bf16 *scale[2];  // 4-bit weights: [E][N][Kp / G]
+    const ep_bf16 *x;
+    const int32_t *expert_offset;
+    ep_bf16 *y;
+    int32_t S, N, K, E;
+    int32_t *error;
+};
+
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
+    uint32_t v;
+    // (word >> 4 i) & 0x000F000F | 0x43004300
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)));
+    const __nv_bfloat162 m = __float2bfloat162_rn(136.0f);
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), m);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// G = 0: bf16 weights, 128 k a stage; else 4-bit weights, 512 k a stage. The stage's first 128 bytes
+// of the rows are one half's, the second 128 the other's.
+template <int G>
+struct StreamShape {
+    static constexpr int kStageK = G == 0 ? 128 : 512;
+    static constexpr int kWarpK = kStageK / 2;     // k of a stage that one warp takes
+    static constexpr int kPartK = kWarpK / 2;      // taken at a time: 64 bytes of a weight row
+    static constexpr int kVecs = kPartK / 32;      // 16-byte words of x for it
+};
+
+// The scales of 128 k of a row, from k `off` on: one bf16 (G = 128), two or four of them.
+template <int G>
+__device__ __forceinline__ uint2 load_scales(const ep_bf16 *row, int off) {
+    if constexpr (G == 128)
+        return make_uint2(row[off / 128], 0);
+    else if constexpr (G == 64)
+        return make_uint2(*reinterpret_cast<const uint32_t *>(row + off / 64), 0);
+    else if constexpr (G == 32)
+        return *reinterpret_cast<const uint2 *>(row + off / 32);
+    else
+        return make_uint2(0, 0);
+}
+
+// What one consumer warp does with the work items' stages.
+struct StreamWarp {
+    unsigned char *stages;
+    uint64_t *full, *empty;
+    volatile int *failed;
+    uint32_t it;
+    int lane, m, half;
+};
+
+// One pass over an item's stages for up to NT * 8 rows of x (`tokens` of them exist); red[half]
+// [token][row] gets the warp's sums.
+template <bool GATED, int G, int NT>
+__device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w, int e, int n0, int64_t x0, int tokens,
+                                            float *red) {
+    using Sh = StreamShape<G>;
+    const int g = w.lane / 4, t = w.lane % 4;
+    // weight rows of the fragment's rows g and g + 8: with g's order changed so that the eight lanes of
+    // one shared-memory phase, two rows, meet different banks of the swizzled stage
+    const int r0 = w.m * 16 + (g >> 1) + 4 * (g & 1);
+    const uint4 *at = reinterpret_cast<const uint4 *>(w.stages + w.half * kStreamBox + r0 * 128);
+    // scales of the two rows, activations of this lane's row: at the warp's part of the present stage
+    const ep_bf16 *sc[2] = {nullptr, nullptr};
+    if constexpr (G > 0) {
+        const size_t row_groups = (size_t)((p.K + 127) / 128) * (128 / G);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = n0 + (GATED ? r0 % 64 : r0) + 8 * h;  // past the last: that one, not stored
+            sc[h] = p.scale[GATED && w.m >= 4] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.half * (Sh::kWarpK / G);
+        }
+    }
+    const ep_bf16 *x[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)  // past the last row: the first again; its sums are not stored
+        x[i] = p.x + (size_t)(x0 + (i * 8 + g < tokens ? i * 8 + g : 0)) * p.K + w.half * Sh::kWarpK + 8 * t;
+    const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
+
+    // the activations and scales (G = 128: one a row; 64: two, 32: four, in 4 or 8 bytes) of one part;
+    // CHECK: of a stage that goes past K
+    struct Ahead {
+        uint4 x[NT][Sh::kVecs];
+        uint2 scale[2];
+    };
+    const auto fetch = [&](auto check, int b, int part, Ahead &a) {
+        const int off = part * Sh::kPartK;
+        const int left = p.K - b * Sh::kStageK - w.half * Sh::kWarpK - off;  // k from the part's first on
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < Sh::kVecs; ++j)
+                a.x[i][j] = !check || 32 * j + 8 * t < left ? *reinterpret_cast<const uint4 *>(x[i] + off + 32 * j)
+                                                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a.scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc[h], off);
+    };
+    const auto fetch_any = [&](int b, int part, Ahead &a) {
+        if ((b + 1) * Sh::kStageK <= p.K)
+            fetch(std::false_type{}, b, part, a);
+        else
+            fetch(std::true_type{}, b, part, a);
+    };
+    const auto scale_of = [](const uint2 &v, int i) {
+        return __uint_as_float(((i / 2 ? v.y : v.x) >> (16 * (i % 2))) << 16);
+    };
+
+    float acc[NT][4] = {};
+    const auto multiply = [&](const Ahead &a, const uint4 &q0, const uint4 &q1) {
+        if constexpr (G == 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                mma_16816(acc[i], q0.x, q1.x, q0.y, q1.y, a.x[i][0].x, a.x[i][0].y);
+                mma_16816(acc[i], q0.z, q1.z, q0.w, q1.w, a.x[i][0].z, a.x[i][0].w);
+            }
+        } else {
+            float part[NT][4] = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w0 = word_of(q0, j), w1 = word_of(q1, j);
+#pragma unroll
+                for (int step = 0; step < 2; ++step) {
+                    const uint32_t a0 = w4_pair(w0, 2 * step), a1 = w4_pair(w1, 2 * step);
+                    const uint32_t a2 = w4_pair(w0, 2 * step + 1), a3 = w4_pair(w1, 2 * step + 1);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        mma_16816(part[i], a0, a1, a2, a3, step ? a.x[i][j].z : a.x[i][j].x, step ? a.x[i][j].w : a.x[i][j].y);
+                }
+                if ((32 * (j + 1)) % G == 0) {
+                    const float f[2] = {scale_of(a.scale[0], 32 * j / G), scale_of(a.scale[1], 32 * j / G)};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            acc[i][r] = fmaf(f[r / 2], part[i][r], acc[i][r]);
+                            part[i][r] = 0.0f;
+                        }
+                }
+            }
+        }
+    };
+    const int u0 = t ^ (r0 & 7), u1 = (4 + t) ^ (r0 & 7);  // the two parts' words of the row
+    // one row of tokens leaves registers for a stage's first part ahead of it; the second is fetched
+    // ahead of the wait
+    constexpr bool kDeep = NT == 1;
+    Ahead a0, a1;
+    if (kDeep) fetch_any(0, 0, a0);
+    for (int b = 0; b < kb; ++b, ++w.it) {
+        const uint32_t s = w.it % kStreamStages;
+        const uint4 *from = at + s * (kStreamStageBytes / 16);
+        fetch_any(b, kDeep ? 1 : 0, kDeep ? a1 : a0);
+        if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
+        __syncwarp();
+        // the barrier's completion was seen by one lane; the others' reads are ordered behind it here
+        const uint4 q00 = from[u0], q01 = from[u0 + 64], q10 = from[u1], q11 = from[u1 + 64];
+        __syncwarp();
+        if (w.lane == 0) mbar_arrive(&w.empty[s]);
+        multiply(a0, q00, q01);
+        if (!kDeep) fetch_any(b, 1, a1);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) x[i] += Sh::kStageK;
+        if constexpr (G > 0) sc[0] += Sh::kStageK / G, sc[1] += Sh::kStageK / G;
+        if (kDeep && b + 1 < kb) fetch_any(b + 1, 0, a0);
+        multiply(a1, q10, q11);
+    }
+    float *mine = red + (size_t)w.half * kStreamTokens * kStreamRows;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mine[(i * 8 + 2 * t + r % 2) * kStreamRows + r0 + r / 2 * 8] = acc[i][r];
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory"); }
+
+template <bool GATED, int G>
+__global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const __grid_constant__ StreamParams p) {
+    using Sh = StreamShape<G>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[kStreamStages], empty[kStreamStages];
+    __shared__ int hits;
+    __shared__ volatile int failed;
+    unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    // two buffers [half][token][row]: one takes a pass's sums while the other is still read
+    float *red = reinterpret_cast<float *>(stages + kStreamStages * kStreamStageBytes);
+    constexpr int kRed = 2 * kStreamTokens * kStreamRows;
+    int *hit = reinterpret_cast<int *>(red + 2 * kRed);  // experts that have rows
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStreamStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kStreamWarps);
+        failed = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&p.w[0]);
+        if (GATED) tma_prefetch_map(&p.w[1]);
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (warp == 0) {
+        int n = 0;
+        for (int base = 0; base < p.E; base += 32) {
+            const int e = base + lane;
+            bool has = false;
+            if (e < p.E) {
+                const int first = min(max(p.expert_offset[e], 0), p.S);
+                has = min(p.expert_offset[e + 1], p.S) > first;
+            }
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
+            if (has) hit[n + __popc(m & ((1u << lane) - 1))] = e;
+            n += __popc(m);
+        }
+        if (lane == 0) hits = n;
+    }
+    __syncthreads();
+    constexpr int kOut = GATED ? kStreamRows / 2 : kStreamRows;  // output columns of a work item
+    const int blocks = (p.N + kOut - 1) / kOut;
+    const int64_t items = (int64_t)hits * blocks;
+    const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
+
+    if (warp == kStreamWarps) {
+        // ---- producer
+        if (elect_one()) {
+            uint32_t it = 0;
+            bool ok = true, ready = false;
+            for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
+                const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
+                const int first = min(max(p.expert_offset[e], 0), p.S);
+                const int rows = min(p.expert_offset[e + 1], p.S) - first;
+                const int64_t fills = (int64_t)((rows + kStreamTokens - 1) / kStreamTokens) * kb;
+                int b = 0;
+                for (int64_t f = 0; f < fills; ++f, ++it) {
+                    const int s = it % kStreamStages;
+                    if (it >= kStreamStages && !ready &&
+                        !mbar_poll_limited(&empty[s], (it / kStreamStages - 1) & 1, &failed)) {
+                        ok = false;
+                        break;
+                    }
+                    ready = it + 1 >= kStreamStages &&
+                            mbar_test(&empty[(it + 1) % kStreamStages], ((it + 1) / kStreamStages - 1) & 1);
+                    mbar_arrive_expect_tx(&full[s], kStreamStageBytes);
+                    unsigned char *to = stages + s * kStreamStageBytes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int at = (2 * b + h) * (G == 0 ? 64 : 128);  // the map's elements: bf16, or bytes of nibbles
+                        tma_load_3d<1>(to + h * kStreamBox, &p.w[0], at, n0, e, smem_u32(&full[s]));
+                        if (GATED)
+                            tma_load_3d<1>(to + h * kStreamBox + kStreamBox / 2, &p.w[1], at, n0, e, smem_u32(&full[s]));
+                    }
+                    if (++b == kb) b = 0;
+                }
+            }
+            if (failed)  // no copy may be under way when the CTA ends
+                for (int i = 0; i < kStreamStages; ++i)
+                    if (it > (uint32_t)i) {
+                        int never = 0;
+                        mbar_wait_limited(&full[i], ((it - 1 - i) / kStreamStages) & 1, &never);
+                    }
+        }
+        __syncwarp();
+    } else {
+        // ---- consumers. After a failure they go on without waiting: every warp reaches the barriers.
+        float *const red_begin = red;
+        StreamWarp w{stages, full, empty, &failed, 0, lane, warp / 2, warp % 2};
+        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+            const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
+            const int first = min(max(p.expert_offset[e], 0), p.S);
+            const int rows = min(p.expert_offset[e + 1], p.S) - first;
+            for (int done = 0; done < rows; done += kStreamTokens) {
+                const int tokens = min(rows - done, kStreamTokens);
+                const int64_t x0 = (int64_t)first + done;
+                if (tokens <= 8)
+                    stream_pass<GATED, G, 1>(p, w, e, n0, x0, tokens, red);
+                else
+                    stream_pass<GATED, G, 2>(p, w, e, n0, x0, tokens, red);
+                consumers_sync();
+                const float *sums = red;
+                for (int i = threadIdx.x; i < tokens * kOut; i += kStreamWarps * 32) {
+                    const int token = i / kOut, n = i % kOut;
+                    const float *r = sums + token * kStreamRows + n;
+                    constexpr int kHalf = kStreamTokens * kStreamRows;
+                    float v = r[0] + r[kHalf];
+                    if constexpr (GATED) v = __fdividef(v, 1.0f + __expf(-v)) * (r[kOut] + r[kHalf + kOut]);
+                    if (n0 + n < p.N)
+                        reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)(x0 + token) * p.N + n0 + n] = __float2bfloat16_rn(v);
+                }
+                red = red == red_begin ? red_begin + kRed : red_begin;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && failed) atomicOr(p.error, kErrExpertWait);
+}
+
+template <bool GATED, int G>
+cudaError_t launch_stream(StreamParams &p, const void *w0, const void *w1, cudaStream_t s) {
+    auto kernel = expert_stream_kernel<GATED, G>;
+    cudaError_t e = expert_error_word(&p.error);
+    if (e != cudaSuccess) return e;
+    const int64_t row = G == 0 ? p.K : (int64_t)(p.K + 127) / 128 * 64;
+    constexpr int kBoxRows = GATED ? kStreamRows / 2 : kStreamRows;
+    constexpr int kBytes = G == 0 ? 2 : 1;
+    if (!make_map(&p.w[0], w0, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
+    if (GATED && !make_map(&p.w[1], w1, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + 4 * kStreamTokens * kStreamRows * sizeof(float) +
+                        (size_t)p.E * sizeof(int);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    constexpr int kOut = GATED ? kStreamRows / 2 : kStreamRows;
+    const int64_t most = (int64_t)(p.E < p.S ? p.E : p.S) * ((p.N + kOut - 1) / kOut);
+    const int sms = current_device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    return launch_dependent(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(kStreamThreads), smem, s, p);
+}
+
+}  // namespace ep

@@ -8,6 +8,10 @@
 
 namespace ep {
 
+// A dense matrix [y][x], or [z][y][x], of bf16 (bytes = 2) or bytes (1), to be read in boxes of bx by
+// by elements, 128 bytes wide and swizzled over 128 bytes. What lies outside reads as zero.
+bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by);
+
 // mbarrier.try_wait puts the thread to sleep until the phase completes, for kWaitSliceNs at most.
 // (Polled without that hint, by the epilogue's warps above all, the waits slowed the whole CTA: a
 // block of 8 rows took 91 us.) A wait that is not satisfied after kWaitSlices of them, about two

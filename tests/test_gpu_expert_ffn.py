@@ -260,3 +260,33 @@ def test_gradients_against_differences(ep):
         got = b.o[k].double().reshape(v.shape)
         bound = (r["tol_" + k] * v.abs()).sum().item() + 1e-6 * abs(exact) + 2 * abs(d1 - d2)
         assert abs((got * v).sum().item() - exact) <= bound, k
+
+
+@pytest.mark.parametrize("counts,H,I,before,after", [
+    ([1], 8, 8, 0, 0), ([1, 0, 2, 0, 0, 1], 72, 40, 1, 2), ([16], 264, 200, 0, 0), ([9, 7], 1000, 360, 0, 0),
+    ([1] * 7 + [0] * 25, 4096, 1024, 0, 0), ([0] * 9 + [33] + [0] * 10, 520, 136, 0, 3), ([3] * 170, 128, 64, 0, 0),
+])
+def test_few_rows(ep, counts, H, I, before, after):
+    """Forward calls with few rows an expert, saved halves not wanted: more rows than one pass takes,
+    experts without rows, widths that end inside a stage."""
+    b = Block(ep, counts, H, I, before, after, seed=H)
+    b.forward(ep, save=False)
+    torch.cuda.synchronize()
+    assert ep.ep_device_error() == 0
+    for e, s, f, _ in b.experts():
+        if s.stop > s.start:
+            ref.check(b.o["h"][s], f["h"], f["tol_h"], f"h of expert {e}")
+            ref.check(b.o["y"][s], f["y"], f["tol_y"], f"y of expert {e}")
+    outside = list(range(b.bounds[0])) + list(range(b.bounds[-1], b.cfg.rows))
+    assert (b.o["y"][outside] == 7.0).all() and (b.o["h"][outside] == 7.0).all()
+
+
+def test_few_rows_with_nan_neighbours(ep):
+    b, clean = (Block(ep, [2, 0, 3, 1], 136, 72, before=1, after=1) for _ in range(2))
+    b.x[0] = float("nan")
+    b.x[1 + 2:1 + 4] = float("nan")  # two of expert 2's three rows
+    b.x[-1] = float("inf")
+    for c in (b, clean):
+        c.forward(ep, save=False)
+    keep = [1, 2, 5, 6]
+    assert torch.equal(b.o["y"][keep], clean.o["y"][keep]) and torch.isnan(b.o["y"][3:5]).all()
