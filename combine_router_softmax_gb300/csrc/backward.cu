@@ -6,7 +6,6 @@ namespace ep {
 namespace {
 
 constexpr int kBwdThreads = 256;
-constexpr int kBwdJ = 8;  // positions whose products a thread keeps in registers at once
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
@@ -81,10 +80,11 @@ constexpr int kRouteBwdWarps = 8;
 // in shared memory, so that the row goes out in whole lines:
 //   renormalised: d_l[e] = w_e (dw_e - sum_i w_i dw_i) for the chosen experts, 0 for the others
 //   otherwise:    d_l[e] = p_e (dw_e - sum_i w_i dw_i), p the softmax over all E, dw_e 0 if not chosen
-__global__ void __launch_bounds__(kRouteBwdWarps * 32) route_backward_kernel(int T, int E, int k, int renormalize,
-                                                                            const float *logits, const int32_t *idx,
-                                                                            const float *w, const float *d_w,
-                                                                            float *d_logits) {
+// VPL: logits a lane holds. A small call is a chain of latencies, so everything is fetched at once.
+template <int VPL, bool RENORM>
+__global__ void __launch_bounds__(kRouteBwdWarps * 32) route_backward_kernel(int T, int E, int k, const float *logits,
+                                                                            const int32_t *idx, const float *w,
+                                                                            const float *d_w, float *d_logits) {
     extern __shared__ float rows[];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -94,25 +94,43 @@ __global__ void __launch_bounds__(kRouteBwdWarps * 32) route_backward_kernel(int
     const int64_t at = (int64_t)t * k + lane;
     const int e = lane < k ? idx[at] : -1;
     const float wj = lane < k ? w[at] : 0.0f, dw = lane < k ? d_w[at] : 0.0f;
+    float p[VPL], top = -INFINITY, sum = 0.0f;
+    if constexpr (!RENORM) {
+        const float *l = logits + (size_t)t * E;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) p[i] = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
+    }
+    for (int i = lane; i < E; i += 32) row[i] = 0.0f;
     float inner = wj * dw;
     for (int d = 16; d > 0; d /= 2) inner += __shfl_xor_sync(0xFFFFFFFFu, inner, d);
-    for (int i = lane; i < E; i += 32) row[i] = 0.0f;
     __syncwarp();
-    if (e >= 0 && e < E) row[e] = renormalize ? wj * (dw - inner) : dw;
+    if (e >= 0 && e < E) row[e] = RENORM ? wj * (dw - inner) : dw;
     __syncwarp();
     float *out = d_logits + (size_t)t * E;
-    if (renormalize) {
+    if constexpr (RENORM) {
         for (int i = lane; i < E; i += 32) out[i] = row[i];
-        return;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) top = fmaxf(top, p[i]);
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            p[i] = i * 32 + lane < E ? expf(p[i] - top) : 0.0f;
+            sum += p[i];
+        }
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (i * 32 + lane < E) out[i * 32 + lane] = p[i] / sum * (row[i * 32 + lane] - inner);
     }
-    const float *l = logits + (size_t)t * E;
-    float top = -INFINITY;
-    for (int i = lane; i < E; i += 32) top = fmaxf(top, l[i]);
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    float sum = 0.0f;
-    for (int i = lane; i < E; i += 32) sum += expf(l[i] - top);
-    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    for (int i = lane; i < E; i += 32) out[i] = expf(l[i] - top) / sum * (row[i] - inner);
+}
+
+template <int VPL, bool RENORM>
+cudaError_t launch_rb(const ep_config &c, const float *logits, const int32_t *idx, const float *w, const float *d_w,
+                      float *d_logits, cudaStream_t s) {
+    return launch_dependent(route_backward_kernel<VPL, RENORM>, dim3((unsigned)((c.T + kRouteBwdWarps - 1) / kRouteBwdWarps)),
+                            dim3(kRouteBwdWarps * 32), (size_t)kRouteBwdWarps * c.E * sizeof(float), s, c.T, c.E, c.k, logits,
+                            idx, w, d_w, d_logits);
 }
 
 template <int JPC>
@@ -129,14 +147,21 @@ cudaError_t launch_cb(const ep_config &c, const ep_bf16 *d_out, const ep_bf16 *y
 
 cudaError_t launch_combine_backward(const ep_config &c, const ep_bf16 *d_out, const ep_bf16 *y, const int32_t *slot,
                                     const float *w, ep_bf16 *d_y, float *d_w, cudaStream_t s) {
-    return launch_cb<kBwdJ>(c, d_out, y, slot, w, d_y, d_w, s);
+    // as many positions a CTA as leave two CTAs for every SM: d_out is read once for each CTA
+    const int64_t want = 2 * (int64_t)current_device_sm_count();
+    const auto ctas = [&](int j) { return (int64_t)c.T * ((c.k + j - 1) / j); };
+    if (ctas(8) >= want) return launch_cb<8>(c, d_out, y, slot, w, d_y, d_w, s);
+    if (ctas(4) >= want) return launch_cb<4>(c, d_out, y, slot, w, d_y, d_w, s);
+    if (ctas(2) >= want) return launch_cb<2>(c, d_out, y, slot, w, d_y, d_w, s);
+    return launch_cb<1>(c, d_out, y, slot, w, d_y, d_w, s);
 }
 
 cudaError_t launch_route_backward(const ep_config &c, const float *logits, const int32_t *idx, const float *w,
                                   const float *d_w, float *d_logits, cudaStream_t s) {
-    return launch_dependent(route_backward_kernel, dim3((unsigned)((c.T + kRouteBwdWarps - 1) / kRouteBwdWarps)),
-                            dim3(kRouteBwdWarps * 32), (size_t)kRouteBwdWarps * c.E * sizeof(float), s, c.T, c.E, c.k,
-                            c.renormalize, logits, idx, w, d_w, d_logits);
+    if (c.renormalize) return launch_rb<1, true>(c, logits, idx, w, d_w, d_logits, s);
+    if (c.E <= 128) return launch_rb<4, false>(c, logits, idx, w, d_w, d_logits, s);
+    if (c.E <= 256) return launch_rb<8, false>(c, logits, idx, w, d_w, d_logits, s);
+    return launch_rb<kMaxE / 32, false>(c, logits, idx, w, d_w, d_logits, s);
 }
 
 }  // namespace ep

@@ -13,14 +13,16 @@ constexpr int kClipTensors = 768;  // tensors of one launch: their table is a ke
 // The largest grid of either kernel: four CTAs of 512 threads fill an SM, on 152 of them.
 constexpr int kClipGrid = 4 * 152;
 
-// The tensors of a launch. Work is dealt out in chunks of `chunk` values of one tensor.
+// The tensors of a launch. Work is dealt out in chunks of `chunk` values of one tensor; a CTA takes
+// consecutive ones, from chunk `at` of tensor `tensor` on, up to where the next CTA begins.
 struct ClipTable {
     const void *data[kClipTensors];
     void *out[kClipTensors];
     int64_t numel[kClipTensors];
-    int32_t first[kClipTensors + 1];  // chunks before each tensor
+    int32_t at[kClipGrid + 1];
+    uint16_t tensor[kClipGrid + 1];
     uint8_t dtype[kClipTensors];
-    int32_t n, chunk;
+    int32_t n, chunk, grid;
 };
 static_assert(sizeof(ClipTable) + 64 <= 32764, "kernel arguments");
 
@@ -85,11 +87,10 @@ __device__ __forceinline__ int64_t values_to_boundary(const V *p) {
     return (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(V);
 }
 
-// The sum of the squares of n values, this thread's part. Four independent sums of fp32; a chunk
-// leaves at most chunk / kClipThreads values to a thread, so no sum grows long before it is added
-// up in 64 bits.
+// The sum of the squares of n values, this thread's part: four independent sums of fp32, of at most
+// chunk / kClipThreads / 4 values each.
 template <typename V>
-__device__ double square_sum(const V *p, int64_t n) {
+__device__ float square_sum(const V *p, int64_t n) {
     constexpr int kVec = Io<V>::kVec;
     float acc[4] = {0, 0, 0, 0};
     const int64_t head = min(values_to_boundary(p), n);
@@ -111,7 +112,7 @@ __device__ double square_sum(const V *p, int64_t n) {
         const float v = Io<V>::load(p + tail);
         acc[1] = fmaf(v, v, acc[1]);
     }
-    return ((double)acc[0] + acc[1]) + ((double)acc[2] + acc[3]);
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 template <typename V>
@@ -136,78 +137,104 @@ __device__ void scale_values(const V *p, V *out, int64_t n, float coef) {
     if (tail < n) Io<V>::store(out + tail, Io<V>::load(p + tail) * coef);
 }
 
-// The tensor of chunk c.
-__device__ __forceinline__ int tensor_of(const ClipTable &tab, int c) {
-    int a = 0, b = tab.n;  // first[a] <= c < first[b]
-    while (b - a > 1) {
-        const int m = (a + b) / 2;
-        if (tab.first[m] <= c)
-            a = m;
-        else
-            b = m;
-    }
-    return a;
-}
+// A tensor as the kernels hold it.
+struct ClipTensor {
+    const void *data;
+    void *out;
+    int64_t numel;
+    int32_t chunks;
+    uint8_t dtype;
+    __device__ ClipTensor(const ClipTable &tab, int i)
+        : data(tab.data[i]), out(tab.out[i]), numel(tab.numel[i]),
+          chunks((int32_t)((tab.numel[i] + tab.chunk - 1) / tab.chunk)), dtype(tab.dtype[i]) {}
+};
 
-// The sum of `v` over the CTA, in a fixed order; in every thread.
-__device__ double cta_sum(double v) {
-    __shared__ double part[kClipThreads / 32];
+// The sum of `v` over the CTA as a tree; in thread 0.
+__device__ float cta_sum(float v) {
+    __shared__ float part[kClipThreads / 32];
     for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    __syncthreads();
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    double sum = 0;
-    for (int i = 0; i < kClipThreads / 32; ++i) sum += part[i];
-    return sum;
+    if (threadIdx.x >= 32) return 0;
+    v = threadIdx.x < kClipThreads / 32 ? part[threadIdx.x] : 0.0f;
+    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
 }
 
-// partial[blockIdx.x] = the sum of the squares of this CTA's chunks.
-__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ ClipTable tab, double *partial) {
+// partial[blockIdx.x] = the sum of the squares of this CTA's chunks. fp32 throughout: the chains are
+// short (some hundred steps in a thread, ten in the tree), and the 64-bit units are few: with the
+// tree in 64 bits it took longer than the values (300 tensors, 14 MB, both kernels: 36 us).
+__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ ClipTable tab, float *partial) {
     grid_dependency_wait();
     grid_launch_dependents();
-    double sum = 0;
-    for (int64_t c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
-        const int i = tensor_of(tab, (int)c);
-        const int64_t begin = (c - tab.first[i]) * tab.chunk;
-        const int64_t n = min((int64_t)tab.chunk, tab.numel[i] - begin);
-        if (tab.dtype[i] == EP_F32)
-            sum += square_sum(static_cast<const float *>(tab.data[i]) + begin, n);
-        else if (tab.dtype[i] == EP_BF16)
-            sum += square_sum(static_cast<const __nv_bfloat16 *>(tab.data[i]) + begin, n);
-        else
-            sum += square_sum(static_cast<const __half *>(tab.data[i]) + begin, n);
+    float sum = 0;
+    const int end_tensor = tab.tensor[blockIdx.x + 1], end_at = tab.at[blockIdx.x + 1];
+    int i = tab.tensor[blockIdx.x], c = tab.at[blockIdx.x];
+    while (i < end_tensor || (i == end_tensor && c < end_at)) {
+        const ClipTensor t(tab, i);
+        const int stop = i < end_tensor ? t.chunks : end_at;
+        const int64_t begin = (int64_t)c * tab.chunk, end = min((int64_t)stop * tab.chunk, t.numel);
+        // chunk by chunk, so that no fp32 sum grows long
+        for (int64_t v = begin; v < end; v += tab.chunk) {
+            const int64_t n = min((int64_t)tab.chunk, end - v);
+            if (t.dtype == EP_F32)
+                sum += square_sum(static_cast<const float *>(t.data) + v, n);
+            else if (t.dtype == EP_BF16)
+                sum += square_sum(static_cast<const __nv_bfloat16 *>(t.data) + v, n);
+            else
+                sum += square_sum(static_cast<const __half *>(t.data) + v, n);
+        }
+        ++i;
+        c = 0;
     }
     sum = cta_sum(sum);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
 // norm = sqrt of the partials' sum; out = data * min(1, max_norm / (norm + 1e-6)). Every CTA adds
-// the partials up for itself, all in the same order. Chunks are taken from the last to the first:
-// the last ones are what the sum of squares read last, and so what the L2 cache still holds.
+// the partials up for itself, all in the same order. A CTA takes its chunks from the last to the
+// first: the last ones are what the sum of squares read last, and so what the L2 cache still holds.
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ ClipTable tab,
-                                                                  const double *partial, int partials, float max_norm,
+                                                                  const float *partial, int partials, float max_norm,
                                                                   float *norm) {
     grid_dependency_wait();
     grid_launch_dependents();
-    double v = 0;
-    for (int i = threadIdx.x; i < partials; i += kClipThreads) v += partial[i];
-    const float total = (float)sqrt(cta_sum(v));
+    __shared__ float total_shared;
+    if (threadIdx.x < 32) {  // one warp, in 64 bits: the CTAs' sums may be many
+        double v = 0;
+        for (int i = threadIdx.x; i < partials; i += 32) v += partial[i];
+        for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        if (threadIdx.x == 0) total_shared = (float)sqrt(v);
+    }
+    __syncthreads();
+    const float total = total_shared;
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     if (tab.n == 0) return;
     float coef = max_norm / (total + 1e-6f);
     if (coef > 1.0f) coef = 1.0f;  // a NaN stays one
-    for (int64_t c = (int64_t)tab.first[tab.n] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-        const int i = tensor_of(tab, (int)c);
-        if (coef == 1.0f && tab.out[i] == tab.data[i]) continue;  // in place, and nothing to change
-        const int64_t begin = (c - tab.first[i]) * tab.chunk;
-        const int64_t n = min((int64_t)tab.chunk, tab.numel[i] - begin);
-        if (tab.dtype[i] == EP_F32)
-            scale_values(static_cast<const float *>(tab.data[i]) + begin, static_cast<float *>(tab.out[i]) + begin, n, coef);
-        else if (tab.dtype[i] == EP_BF16)
-            scale_values(static_cast<const __nv_bfloat16 *>(tab.data[i]) + begin,
-                         static_cast<__nv_bfloat16 *>(tab.out[i]) + begin, n, coef);
-        else
-            scale_values(static_cast<const __half *>(tab.data[i]) + begin, static_cast<__half *>(tab.out[i]) + begin, n, coef);
+    const int first_tensor = tab.tensor[blockIdx.x], first_at = tab.at[blockIdx.x];
+    int i = tab.tensor[blockIdx.x + 1], c = tab.at[blockIdx.x + 1];  // c: one past the chunk to take next
+    while (i > first_tensor || (i == first_tensor && c > first_at)) {
+        if (c == 0) {
+            --i;
+            c = (int)((tab.numel[i] + tab.chunk - 1) / tab.chunk);
+            continue;
+        }
+        const ClipTensor t(tab, i);
+        const int stop = i > first_tensor ? 0 : first_at;
+        if (coef != 1.0f || t.out != t.data)  // else in place, and nothing to change
+            for (int k = c - 1; k >= stop; --k) {
+                const int64_t v = (int64_t)k * tab.chunk;
+                const int64_t n = min((int64_t)tab.chunk, t.numel - v);
+                if (t.dtype == EP_F32)
+                    scale_values(static_cast<const float *>(t.data) + v, static_cast<float *>(t.out) + v, n, coef);
+                else if (t.dtype == EP_BF16)
+                    scale_values(static_cast<const __nv_bfloat16 *>(t.data) + v, static_cast<__nv_bfloat16 *>(t.out) + v, n, coef);
+                else
+                    scale_values(static_cast<const __half *>(t.data) + v, static_cast<__half *>(t.out) + v, n, coef);
+            }
+        c = stop;
+        if (i == first_tensor) break;
     }
 }
 
@@ -224,18 +251,23 @@ int32_t fill_table(ClipTable &tab, const ep_grad_tensor *t, int32_t n, int32_t f
         tab.dtype[tab.n++] = (uint8_t)t[i].dtype;
         values += t[i].numel;
     }
-    // at most about 16 chunks for every CTA, so that the last ones leave little of the GPU idle;
-    // a chunk stays below 2^20 values unless their number would not fit an int
+    // at most about 16 chunks for every CTA, so that their shares differ little; a chunk stays at
+    // most 2^20 values unless their number would not fit an int
     int64_t chunk = 4096;
     while (chunk < (1 << 20) && values / chunk > (int64_t)kClipGrid * 16) chunk *= 2;
     while (values / chunk + tab.n > INT32_MAX) chunk *= 2;
-    int64_t first = 0;
-    for (int32_t j = 0; j < tab.n; ++j) {
-        tab.first[j] = (int32_t)first;
-        first += (tab.numel[j] + chunk - 1) / chunk;
-    }
-    tab.first[tab.n] = (int32_t)first;
+    int64_t total = 0;
+    for (int32_t j = 0; j < tab.n; ++j) total += (tab.numel[j] + chunk - 1) / chunk;
     tab.chunk = (int32_t)chunk;
+    tab.grid = (int32_t)(total < kClipGrid ? total : kClipGrid);
+    int64_t before = 0;  // chunks before tensor j
+    int32_t j = 0;
+    for (int32_t b = 0; b <= tab.grid; ++b) {
+        const int64_t c = tab.grid > 0 ? total * b / tab.grid : 0;
+        while (j < tab.n && before + (tab.numel[j] + chunk - 1) / chunk <= c) before += (tab.numel[j++] + chunk - 1) / chunk;
+        tab.tensor[b] = (uint16_t)j;
+        tab.at[b] = (int32_t)(c - before);
+    }
     return i;
 }
 
@@ -243,30 +275,55 @@ int32_t fill_table(ClipTable &tab, const ep_grad_tensor *t, int32_t n, int32_t f
 
 size_t grad_workspace_bytes(int32_t n) {
     const size_t launches = n > 0 ? ((size_t)n + kClipTensors - 1) / kClipTensors : 1;
-    return launches * (size_t)kClipGrid * sizeof(double);
+    return launches * (size_t)kClipGrid * sizeof(float);
 }
 
-cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm, double *partial,
+namespace {
+
+// One launch with the table passed by address: it is large, and copied once, by the runtime.
+cudaError_t launch_clip(const void *kernel, int grid, void **args, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kClipThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+}  // namespace
+
+cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm, float *partial,
                              cudaStream_t s) {
     ClipTable tab;
+    tab.n = 0;
     int partials = 0;
+    int32_t filled_from = -1;  // the first tensor of what `tab` holds
     for (int32_t i = 0; i < n;) {
+        filled_from = i;
         i = fill_table(tab, t, n, i);
         if (tab.n == 0) break;
-        const int grid = tab.first[tab.n] < kClipGrid ? tab.first[tab.n] : kClipGrid;
-        const cudaError_t e = launch_dependent(grad_square_kernel, dim3(grid), dim3(kClipThreads), 0, s, tab, partial + partials);
+        float *to = partial + partials;
+        void *args[] = {&tab, &to};
+        const cudaError_t e = launch_clip((const void *)grad_square_kernel, tab.grid, args, s);
         if (e != cudaSuccess) return e;
-        partials += grid;
+        partials += tab.grid;
     }
     // with nothing to scale one CTA still writes the norm
     int32_t i = 0;
     do {
-        tab.n = 0;
-        tab.first[0] = 0;
-        if (scale && n > 0) i = fill_table(tab, t, n, i);
-        const int grid = tab.n == 0 ? 1 : tab.first[tab.n] < kClipGrid ? tab.first[tab.n] : kClipGrid;
-        const cudaError_t e = launch_dependent(grad_scale_kernel, dim3(grid), dim3(kClipThreads), 0, s, tab,
-                                               const_cast<const double *>(partial), partials, max_norm, norm);
+        if (!scale)
+            tab.n = 0;
+        else if (n > 0 && i == 0 && filled_from == 0)  // the only launch's: still there
+            i = n;
+        else if (n > 0)
+            i = fill_table(tab, t, n, i);
+        const float *sums = partial;
+        void *args[] = {&tab, &sums, &partials, &max_norm, &norm};
+        const cudaError_t e = launch_clip((const void *)grad_scale_kernel, tab.n == 0 ? 1 : tab.grid, args, s);
         if (e != cudaSuccess) return e;
     } while (scale && i < n);
     return cudaSuccess;
