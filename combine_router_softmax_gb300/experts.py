@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import torch
 
 from . import EpConfig, _check, _lib, _ptr, _stream
@@ -104,10 +105,9 @@ def ep_w4_sizes(cfg: EpW4Config) -> tuple[int, int]:
 
 def _packed(cfg: EpW4Config, q, scale, name):
     """Pointers of a packed weight: q uint8 [E, N, Kp / 2], scale bf16 [E, N, Kp / group]."""
-    q_bytes, s_bytes = ep_w4_sizes(cfg)
-    rows = cfg.E * cfg.N
-    return (_ptr(q, torch.uint8, (cfg.E, cfg.N, q_bytes // rows), "q" + name),
-            _bf16(scale, (cfg.E, cfg.N, s_bytes // 2 // rows), "scale" + name))
+    Kp = (cfg.K + 127) // 128 * 128
+    return (_ptr(q, torch.uint8, (cfg.E, cfg.N, Kp // 2), "q" + name),
+            _bf16(scale, (cfg.E, cfg.N, Kp // max(cfg.group, 1)), "scale" + name))
 
 
 def ep_w4_pack(cfg: EpW4Config, w, q, scale, stream=None) -> None:
@@ -159,6 +159,13 @@ def ep_route_backward(cfg: EpConfig, logits, topk_idx, topk_w, d_topk_w, d_logit
 
 
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_GRAD_RECORD = np.dtype([("data", np.uint64), ("out", np.uint64), ("numel", np.int64), ("dtype", np.int32),
+                         ("reserved", np.int32)])  # EpGradTensor
+
+
+def _address(ptr) -> int:
+    """What _ptr gave, as a number."""
+    return (ptr.value if isinstance(ptr, ctypes.c_void_p) else ptr) or 0
 
 
 def ep_grad_workspace_size(n: int) -> int:
@@ -180,11 +187,21 @@ class GradList:
         self._keep = (grads, out)
         self.n = len(grads)
         self.records = (EpGradTensor * max(self.n, 1))()
-        for i, (g, o) in enumerate(zip(grads, out)):
-            if not isinstance(g, torch.Tensor) or g.dtype not in _GRAD_TYPES:
-                raise TypeError(f"grads[{i}]: expected a float32, bfloat16 or float16 tensor")
-            data, to = _ptr(g, g.dtype, None, f"grads[{i}]"), _ptr(o, g.dtype, tuple(g.shape), f"out[{i}]")
-            self.records[i] = EpGradTensor(data, to, g.numel(), _GRAD_TYPES[g.dtype], 0)
+        table = np.frombuffer(self.records, dtype=_GRAD_RECORD)[:self.n]
+        device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2  # -1: the CPU
+        if all(type(g) is torch.Tensor and g.dtype in _GRAD_TYPES and o.dtype is g.dtype and g.shape == o.shape
+               and g.get_device() == device and o.get_device() == device and g.is_contiguous() and o.is_contiguous()
+               for g, o in zip(grads, out)):
+            table["data"] = [g.data_ptr() for g in grads]
+            table["out"] = [o.data_ptr() for o in out]
+        else:  # says which tensor is wrong
+            for i, (g, o) in enumerate(zip(grads, out)):
+                if not isinstance(g, torch.Tensor) or g.dtype not in _GRAD_TYPES:
+                    raise TypeError(f"grads[{i}]: expected a float32, bfloat16 or float16 tensor")
+                table["data"][i] = _address(_ptr(g, g.dtype, None, f"grads[{i}]"))
+                table["out"][i] = _address(_ptr(o, g.dtype, tuple(g.shape), f"out[{i}]"))
+        table["numel"] = [g.numel() for g in grads]
+        table["dtype"] = [_GRAD_TYPES[g.dtype] for g in grads]
         self.workspace = torch.empty((ep_grad_workspace_size(self.n),), dtype=torch.uint8, device="cuda")
 
     def norm(self, norm, stream=None) -> None:
