@@ -326,11 +326,11 @@ cudaError_t launch_dispatch_fused(const ep_config &c, int32_t W, const float *lo
 
 // The experts' gated block (expert_ffn.cu).
 cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
-                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
-                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s);
+                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, uint16_t *g,
+                              uint16_t *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s);
 cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
-                                       const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
+                                       const uint16_t *g, const uint16_t *u, const ep_bf16 *h, const ep_bf16 *d_y,
                                        ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
                                        ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s);
 

@@ -158,8 +158,8 @@ int64_t weight_tiles(const GemmParams &p, int bm, int bn) {
 }  // namespace
 
 cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
-                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g,
-                              ep_bf16 *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
+                              const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, uint16_t *g,
+                              uint16_t *u, ep_bf16 *h, ep_bf16 *y, cudaStream_t s) {
     if (!g && streams(c)) {
         StreamParams q = {};
         q.x = rows;
@@ -194,7 +194,7 @@ cudaError_t launch_expert_ffn(const ep_ffn_config &c, const ep_bf16 *rows, const
 
 cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *rows, const int32_t *expert_offset,
                                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down,
-                                       const ep_bf16 *g, const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y,
+                                       const uint16_t *g, const uint16_t *u, const ep_bf16 *h, const ep_bf16 *d_y,
                                        ep_bf16 *d_g, ep_bf16 *d_u, ep_bf16 *d_rows, ep_bf16 *d_w_gate,
                                        ep_bf16 *d_w_up, ep_bf16 *d_w_down, cudaStream_t s) {
     GemmParams p = base_params(c, expert_offset);
@@ -202,8 +202,8 @@ cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *ro
     p.N[0] = c.I;
     p.out[0] = d_g;
     p.out[1] = d_u;
-    p.g = const_cast<ep_bf16 *>(g);
-    p.u = const_cast<ep_bf16 *>(u);
+    p.g = const_cast<uint16_t *>(g);
+    p.u = const_cast<uint16_t *>(u);
     cudaError_t e = row_product<ExpertOp::kDGateUp>(p, {{d_y}, {w_down}}, s);
     if (e != cudaSuccess) return e;
 

@@ -10,13 +10,17 @@
 //   DRows    dx = dg Wg[e] + du Wu[e]: one accumulation over 2 I
 //   DWeight  dWd[e] = dy^T h, dWg[e] = dg^T x, dWu[e] = du^T x over the expert's rows
 // Operands are bf16, sums fp32 (in TMEM), results are rounded to bf16 once. h, dg and du are
-// rounded to bf16 where they become operands of the next product.
+// rounded to bf16 where they become operands of the next product. g and u are no operands: they are
+// kept for the backward pass in fp16, which rounds eight times finer in the same 16 bits (the weights'
+// gradients are 0.0024 off in norm with it, 0.0031 with bf16); beyond 65504 it has infinity.
 //
 // One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
 // holding half of either operand): warp 0 feeds a ring of shared-memory stages by TMA, warp
 // 1 issues the MMAs into one of two accumulators, warps 2 to 5 turn the other one into
 // results. Every wait has a time limit (kErrExpertWait).
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "tcgen05.cuh"
 
@@ -40,7 +44,7 @@ struct GemmParams {
     int32_t N[3];      // output columns of each problem (row products: N[0])
     int32_t problems;  // DWeight: how many of the three are wanted
     ep_bf16 *out[3];   // GateUp: h; DGateUp: dg, du; DWeight: the gradients [E, M, N]
-    ep_bf16 *g, *u;    // GateUp: written when not null; DGateUp: read
+    uint16_t *g, *u;   // fp16. GateUp: written when not null; DGateUp: read
     int32_t *error;
 };
 
@@ -65,8 +69,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 half_values(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 // exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
@@ -469,11 +476,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float dg[2], du[2];
+                            const float2 g2 = half_values(g[half][i]), u2 = half_values(u[half][i]);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const float dh = __uint_as_float(v[2 * i + k]);
-                                const float gg = k ? bf16_hi(g[half][i]) : bf16_lo(g[half][i]);
-                                const float uu = k ? bf16_hi(u[half][i]) : bf16_lo(u[half][i]);
+                                const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
                                 const float s = sigmoid(gg);
                                 du[k] = dh * gg * s;
                                 dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
@@ -502,8 +509,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                                 const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
                                 const float u0 = __uint_as_float(w[2 * i]), u1 = __uint_as_float(w[2 * i + 1]);
                                 o[i] = what == 0   ? bf16_pair(g0 * sigmoid(g0) * u0, g1 * sigmoid(g1) * u1)
-                                       : what == 1 ? bf16_pair(g0, g1)
-                                                   : bf16_pair(u0, u1);
+                                       : what == 1 ? half_pair(g0, g1)
+                                                   : half_pair(u0, u1);
                             }
                             slab_put(slab, lane, half, o);
                         }

@@ -58,7 +58,7 @@ ep_status check_grads(const ep_grad_tensor *t, int32_t n, const float *norm, con
 extern "C" {
 
 ep_status ep_expert_ffn(const ep_ffn_config *cfg, const ep_bf16 *rows, const int32_t *expert_offset,
-                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g, ep_bf16 *u,
+                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, uint16_t *g, uint16_t *u,
                         ep_bf16 *h, ep_bf16 *y, cudaStream_t stream) {
     const ep_status st = check_ffn(cfg);
     if (st != EP_OK) return st;
@@ -70,8 +70,8 @@ ep_status ep_expert_ffn(const ep_ffn_config *cfg, const ep_bf16 *rows, const int
 }
 
 ep_status ep_expert_ffn_backward(const ep_ffn_config *cfg, const ep_bf16 *rows, const int32_t *expert_offset,
-                                 const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, const ep_bf16 *g,
-                                 const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y, ep_bf16 *d_g, ep_bf16 *d_u,
+                                 const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, const uint16_t *g,
+                                 const uint16_t *u, const ep_bf16 *h, const ep_bf16 *d_y, ep_bf16 *d_g, ep_bf16 *d_u,
                                  ep_bf16 *d_rows, ep_bf16 *d_w_gate, ep_bf16 *d_w_up, ep_bf16 *d_w_down,
                                  cudaStream_t stream) {
     const ep_status st = check_ffn(cfg);

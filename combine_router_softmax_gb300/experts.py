@@ -68,17 +68,23 @@ def _bf16(t, shape, name):
     return _ptr(t, torch.bfloat16, shape, name)
 
 
+def _half(t, shape, name):
+    """Memory for 16-bit values: a float16 tensor, or a bfloat16 one of which nobody reads the values."""
+    return _ptr(t, torch.bfloat16 if t is not None and t.dtype is torch.bfloat16 else torch.float16, shape, name)
+
+
 def ep_expert_ffn(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, h, y, g=None, u=None,
                   stream=None) -> None:
     """y = (silu(rows Wg^T) * (rows Wu^T)) Wd^T with each row's own expert; h is the product before Wd.
 
-    rows, y bf16 [rows, H]; h, g, u bf16 [rows, I]; w_gate, w_up bf16 [E, I, H]; w_down bf16 [E, H, I];
-    expert_offset int32 [E + 1]. g and u (both or neither) are what ep_expert_ffn_backward needs besides h."""
+    rows, y bf16 [rows, H]; h bf16 [rows, I]; w_gate, w_up bf16 [E, I, H]; w_down bf16 [E, H, I]; expert_offset
+    int32 [E + 1]. g and u (float16 [rows, I], both or neither) are what ep_expert_ffn_backward needs besides h;
+    they are written as halves, into bfloat16 tensors too, which are then storage only."""
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
     _check(_lib.ep_expert_ffn(ctypes.byref(cfg), _bf16(rows, (S, H), "rows"),
                               _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
                               _bf16(w_gate, (E, I, H), "w_gate"), _bf16(w_up, (E, I, H), "w_up"),
-                              _bf16(w_down, (E, H, I), "w_down"), _bf16(g, (S, I), "g"), _bf16(u, (S, I), "u"),
+                              _bf16(w_down, (E, H, I), "w_down"), _half(g, (S, I), "g"), _half(u, (S, I), "u"),
                               _bf16(h, (S, I), "h"), _bf16(y, (S, H), "y"), _stream(stream)), "ep_expert_ffn")
 
 
@@ -90,7 +96,7 @@ def ep_expert_ffn_backward(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, 
     _check(_lib.ep_expert_ffn_backward(
         ctypes.byref(cfg), _bf16(rows, (S, H), "rows"), _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
         _bf16(w_gate, (E, I, H), "w_gate"), _bf16(w_up, (E, I, H), "w_up"), _bf16(w_down, (E, H, I), "w_down"),
-        _bf16(g, (S, I), "g"), _bf16(u, (S, I), "u"), _bf16(h, (S, I), "h"), _bf16(d_y, (S, H), "d_y"),
+        _half(g, (S, I), "g"), _half(u, (S, I), "u"), _bf16(h, (S, I), "h"), _bf16(d_y, (S, H), "d_y"),
         _bf16(d_g, (S, I), "d_g"), _bf16(d_u, (S, I), "d_u"), _bf16(d_rows, (S, H), "d_rows"),
         _bf16(d_w_gate, (E, I, H), "d_w_gate"), _bf16(d_w_up, (E, I, H), "d_w_up"),
         _bf16(d_w_down, (E, H, I), "d_w_down"), _stream(stream)), "ep_expert_ffn_backward")

@@ -37,7 +37,8 @@ class MoeLayer:
         self.b = ep.LayerBuffers.allocate(self.cfg)
         new = lambda *s, dtype=BF16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
         S = T * k
-        self.g, self.u, self.h, self.d_g, self.d_u = (new(S, I) for _ in range(5))
+        self.g, self.u = (new(S, I, dtype=torch.float16) for _ in range(2))
+        self.h, self.d_g, self.d_u = (new(S, I) for _ in range(3))
         self.d_send, self.d_y = new(S, H), new(S, H)
         self.d_x = new(T, H)
         self.d_topk_w, self.d_logits = new(T, k, dtype=torch.float32), new(T, E, dtype=torch.float32)

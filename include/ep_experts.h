@@ -46,15 +46,16 @@ typedef struct ep_ffn_config {
  * rows   : const bf16 [rows, H]
  * w_gate : const bf16 [E, I, H]     w_up : const bf16 [E, I, H]
  * w_down : const bf16 [E, H, I]
- * g, u   : bf16 [rows, I] outputs for ep_expert_ffn_backward, both or neither
- *          (NULL); rounded from the same fp32 sums that h is made of
+ * g, u   : 16-bit [rows, I] outputs for ep_expert_ffn_backward, both or neither
+ *          (NULL): the fp32 sums that h is made of, as IEEE halves, which round
+ *          finer than bf16; beyond 65504 they are infinite (h and y are not)
  * h      : bf16 [rows, I] output
  * y      : bf16 [rows, H] output
  * All 16-byte aligned. rows = 0 enqueues nothing. Outputs must not overlap
  * inputs. A CTA that gives up a bounded wait sets ep_device_error bit 4 (16).
  */
 ep_status ep_expert_ffn(const ep_ffn_config *cfg, const ep_bf16 *rows, const int32_t *expert_offset,
-                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, ep_bf16 *g, ep_bf16 *u,
+                        const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, uint16_t *g, uint16_t *u,
                         ep_bf16 *h, ep_bf16 *y, cudaStream_t stream);
 
 /*
@@ -77,8 +78,8 @@ ep_status ep_expert_ffn(const ep_ffn_config *cfg, const ep_bf16 *rows, const int
  * gradients to zero.
  */
 ep_status ep_expert_ffn_backward(const ep_ffn_config *cfg, const ep_bf16 *rows, const int32_t *expert_offset,
-                                 const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, const ep_bf16 *g,
-                                 const ep_bf16 *u, const ep_bf16 *h, const ep_bf16 *d_y, ep_bf16 *d_g, ep_bf16 *d_u,
+                                 const ep_bf16 *w_gate, const ep_bf16 *w_up, const ep_bf16 *w_down, const uint16_t *g,
+                                 const uint16_t *u, const ep_bf16 *h, const ep_bf16 *d_y, ep_bf16 *d_g, ep_bf16 *d_u,
                                  ep_bf16 *d_rows, ep_bf16 *d_w_gate, ep_bf16 *d_w_up, ep_bf16 *d_w_down,
                                  cudaStream_t stream);
 

@@ -1,7 +1,7 @@
 """The experts' block in 64 bits, and how far a bf16 kernel with fp32 sums may be from it.
 
-Every bound is a worst case that counts roundings: u16 = 2^-8 for one rounding to
-bf16, and for a sum of n terms in fp32, n 2^-23 of the sum of their magnitudes
+Every bound is a worst case that counts roundings: 2^-8 for one rounding to bf16,
+2^-11 (and 2^-25 below the normal range) for one to fp16, which g and u are kept in, and for a sum of n terms in fp32, n 2^-23 of the sum of their magnitudes
 (products of bf16 values are exact in fp32; an accumulation step is off by at most
 one unit in the last place, whichever way it rounds). silu' stays within 1.1 and
 silu'' within 0.5 in magnitude; the sigmoid itself is within 2^-20. Terms of
@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-U16, U32, SIG, SLACK = 2.0**-8, 2.0**-23, 2.0**-20, 1.05
+U16, U11, U32, SIG, SLACK = 2.0**-8, 2.0**-11, 2.0**-23, 2.0**-20, 1.05
 
 
 def silu_parts(g):
@@ -26,7 +26,7 @@ def forward(x, wg, wu, wd):
     _, silu, _ = silu_parts(r["g"])
     r["h"] = silu * r["u"]
     r["y"] = r["h"] @ wd.T
-    r["tol_g"], r["tol_u"] = SLACK * (U16 * r["g"].abs() + eg), SLACK * (U16 * r["u"].abs() + eu)
+    r["tol_g"], r["tol_u"] = (SLACK * (U11 * r[k].abs() + e) + 2.0**-25 for k, e in (("g", eg), ("u", eu)))
     r["tol_h"] = SLACK * ((U16 + SIG) * r["h"].abs() + 1.1 * r["u"].abs() * eg + silu.abs() * eu)
     r["tol_y"] = SLACK * (r["tol_h"] @ wd.abs().T + I * U32 * (r["h"].abs() @ wd.abs().T) + U16 * r["y"].abs())
     return r

@@ -37,7 +37,7 @@ class Block:
         self.x, self.dy = n(S, H, s=scale), n(S, H, s=0.1)
         self.w = [n(E, I, H, s=1 / math.sqrt(H)), n(E, I, H, s=1 / math.sqrt(H)), n(E, H, I, s=1 / math.sqrt(I))]
         full = lambda *shape: torch.full(shape, 7.0, dtype=BF16, device="cuda")  # noqa: E731
-        self.o = {**{k: full(S, I) for k in ("g", "u", "h", "d_g", "d_u")}, "y": full(S, H), "d_rows": full(S, H),
+        self.o = {**{k: full(S, I) for k in ("h", "d_g", "d_u")}, "g": full(S, I).half(), "u": full(S, I).half(), "y": full(S, H), "d_rows": full(S, H),
                   "d_w_gate": full(E, I, H), "d_w_up": full(E, I, H), "d_w_down": full(E, H, I)}
 
     def forward(self, ep, save=True, **kw):
@@ -209,6 +209,18 @@ def test_offsets_outside_the_buffer_are_clamped(ep):
     b.forward(ep)
     torch.cuda.synchronize()
     assert (b.o["y"] == 7.0).all() and ep.ep_device_error() == 0
+
+
+def test_saved_halves_in_bfloat16_storage(ep):
+    """g and u may be bfloat16 tensors, as storage: the bits are the same."""
+    b, c = (Block(ep, [5, 70], 136, 72) for _ in range(2))
+    for k in ("g", "u"):
+        c.o[k] = torch.empty_like(c.o["h"])
+    for t in (b, c):
+        t.forward(ep)
+        t.backward(ep)
+    for k in b.o:
+        assert torch.equal(b.o[k].view(torch.int16), c.o[k].view(torch.int16)), k
 
 
 def test_no_rows(ep):
