@@ -213,6 +213,9 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
         for (int r = 0; r < 4; ++r) mine[(i * 8 + 2 * t + r % 2) * kStreamRows + r0 + r / 2 * 8] = acc[i][r];
 }
 
+// The line of `p` into L1.
+__device__ __forceinline__ void ask_for_line(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory"); }
 
 template <bool GATED, int G>
@@ -259,44 +262,56 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
     const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
 
     if (warp == kStreamWarps) {
-        // ---- producer
-        if (elect_one()) {
-            uint32_t it = 0;
-            bool ok = true, ready = false;
-            for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
-                const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
-                const int first = min(max(p.expert_offset[e], 0), p.S);
-                const int rows = min(p.expert_offset[e + 1], p.S) - first;
-                const int64_t fills = (int64_t)((rows + kStreamTokens - 1) / kStreamTokens) * kb;
-                int b = 0;
-                for (int64_t f = 0; f < fills; ++f, ++it) {
+        // ---- producer. Besides the weights it asks for the lines of x and of the scales that the stage's
+        // consumers will read, three stages ahead of them: fetched by each warp for itself they cost an L2
+        // latency a stage.
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
+            const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
+            const int first = min(max(p.expert_offset[e], 0), p.S);
+            const int rows = min(p.expert_offset[e + 1], p.S) - first;
+            for (int done = 0; ok && done < rows; done += kStreamTokens)
+                for (int b = 0; b < kb; ++b, ++it) {
                     const int s = it % kStreamStages;
-                    if (it >= kStreamStages && !ready &&
-                        !mbar_poll_limited(&empty[s], (it / kStreamStages - 1) & 1, &failed)) {
-                        ok = false;
-                        break;
+                    if (it >= kStreamStages) {
+                        if (lane == 0) ok = mbar_poll_limited(&empty[s], (it / kStreamStages - 1) & 1, &failed);
+                        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                        if (!ok) break;
                     }
-                    ready = it + 1 >= kStreamStages &&
-                            mbar_test(&empty[(it + 1) % kStreamStages], ((it + 1) / kStreamStages - 1) & 1);
-                    mbar_arrive_expect_tx(&full[s], kStreamStageBytes);
-                    unsigned char *to = stages + s * kStreamStageBytes;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[s], kStreamStageBytes);
+                        unsigned char *to = stages + s * kStreamStageBytes;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int at = (2 * b + h) * (G == 0 ? 64 : 128);  // the map's elements: bf16, or bytes of nibbles
-                        tma_load_3d<1>(to + h * kStreamBox, &p.w[0], at, n0, e, smem_u32(&full[s]));
-                        if (GATED)
-                            tma_load_3d<1>(to + h * kStreamBox + kStreamBox / 2, &p.w[1], at, n0, e, smem_u32(&full[s]));
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = (2 * b + h) * (G == 0 ? 64 : 128);  // the map's elements: bf16, or bytes of nibbles
+                            tma_load_3d<1>(to + h * kStreamBox, &p.w[0], at, n0, e, smem_u32(&full[s]));
+                            if (GATED)
+                                tma_load_3d<1>(to + h * kStreamBox + kStreamBox / 2, &p.w[1], at, n0, e, smem_u32(&full[s]));
+                        }
                     }
-                    if (++b == kb) b = 0;
+                    __syncwarp();
+                    constexpr int kLines = Sh::kStageK / 64;
+                    for (int i = lane; i < min(rows - done, kStreamTokens) * kLines; i += 32) {
+                        const int k = b * Sh::kStageK + i % kLines * 64;
+                        if (k < p.K) ask_for_line(p.x + (size_t)(first + done + i / kLines) * p.K + k);
+                    }
+                    if (G > 0 && b == 0) {
+                        const size_t row_bytes = (size_t)((p.K + 127) / 128) * (256 / (G > 0 ? G : 1));
+                        for (int i = lane; i < kStreamRows; i += 32) {
+                            const int n = min(n0 + (GATED ? i % kOut : i), p.N - 1);
+                            const char *row = reinterpret_cast<const char *>(p.scale[GATED && i >= kOut]) + ((size_t)e * p.N + n) * row_bytes;
+                            for (size_t off = 0; off < row_bytes; off += 128) ask_for_line(row + off);
+                        }
+                    }
                 }
-            }
-            if (failed)  // no copy may be under way when the CTA ends
-                for (int i = 0; i < kStreamStages; ++i)
-                    if (it > (uint32_t)i) {
-                        int never = 0;
-                        mbar_wait_limited(&full[i], ((it - 1 - i) / kStreamStages) & 1, &never);
-                    }
         }
+        if (failed && lane == 0)  // no copy may be under way when the CTA ends
+            for (int i = 0; i < kStreamStages; ++i)
+                if (it > (uint32_t)i) {
+                    int never = 0;
+                    mbar_wait_limited(&full[i], ((it - 1 - i) / kStreamStages) & 1, &never);
+                }
         __syncwarp();
     } else {
         // ---- consumers. After a failure they go on without waiting: every warp reaches the barriers.
