@@ -3,9 +3,11 @@
 // y[s, n] = sum_k x[s, k] w[e, n, k], e the expert that owns row s, and the gated block's first half
 // silu(g) u from two such products. For single tokens the weights are the traffic (N K values of
 // every expert that has rows, against 2 rows N K operations), so what counts is to keep enough of
-// them on their way: one producer thread per CTA fetches stages of 128 weight rows x 256 bytes by TMA
-// into a ring of four (128 KB, so 19 MB on the GPU; HBM needs about 10 MB under way), on across work
-// items. Sixteen warps consume a stage: warp (m, half) takes 16 weight rows and half of the stage's k.
+// them on their way: a producer warp fetches stages of 64 weight rows x 256 bytes by TMA into a ring of
+// four, on across work items. Eight warps consume a stage: warp (m, half) takes 16 weight rows and half
+// of the stage's k. Two CTAs share an SM (128 KB of stages, 19 MB on the GPU; HBM needs about 10 MB under
+// way; a fifth stage took L1 from the activations and cost 5%): all warps of one wait for the same stage,
+// and what each then does before its products is latency, which the other CTA's products fill.
 //
 // The product is the matrix instruction m16n8k16 with the weights as its 16 rows and 8 rows of x as
 // its columns. Which k a lane's register stands for is free as long as both operands agree, so a
@@ -13,8 +15,13 @@
 //
 // Weights are bf16, or 4 bits with one bf16 scale for G consecutive k. There a nibble v becomes the
 // bf16 value 128 + v by setting the bits 0x4300 over it (bf16 has 7 bits of fraction, so at 128 its
-// step is 1): one logic operation for two nibbles; minus 136 gives v - 8, exactly. Products with
-// bf16 activations are exact in fp32; a group is summed in fp32 and scaled once as a whole.
+// step is 1): one logic operation for two nibbles. What is over, 136, comes off in one of two ways. For
+// up to 8 rows of x it is taken off the sums: sum (128 + v) x - 136 sum x = sum (v - 8) x, with sum x
+// from the same instruction and a matrix of ones; the sums are about 30 times what is left of them,
+// which costs 5 of fp32's 24 bits where the result keeps 8. For more rows it is taken off the values,
+// exactly. Shifts, logic and the bf16 subtraction all take two cycles a quarter of an SM, 22 for a word
+// of 8 nibbles with it and 14 without; the products with ones take 8 for each eight rows of x. Either
+// way products with bf16 activations are exact in fp32; a group is summed in fp32 and scaled as a whole.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,16 +32,18 @@
 
 namespace ep {
 
-constexpr int kStreamWarps = 16;                      // consumers
+constexpr int kStreamWarps = 8;                        // consumers
 constexpr int kStreamThreads = (kStreamWarps + 1) * 32;
-constexpr int kStreamRows = 128;                      // weight rows of a work item (gated: 64 of either projection)
-constexpr int kStreamBox = kStreamRows * 128;         // bytes of 128 bytes of every row: a stage has two
+constexpr int kStreamCtas = 2;                         // on an SM
+constexpr int kStreamRows = 64;                        // weight rows of a work item (gated: 32 of either projection)
+constexpr int kStreamBox = kStreamRows * 128;          // bytes of 128 bytes of every row: a stage has two
 constexpr int kStreamStageBytes = 2 * kStreamBox;
 constexpr int kStreamStages = 4;
-constexpr int kStreamTokens = 16;                     // rows of x that one pass over the weights serves
+constexpr int kStreamTokens = 16;                      // rows of x that one pass over the weights serves
+constexpr int kStreamRed = 2 * kStreamTokens * kStreamRows;  // floats of a pass's sums
 
 struct StreamParams {
-    CUtensorMap w[2];         // [E][N][bytes of a row], boxes of 128 bytes x 64 or 128 rows, swizzled
+    CUtensorMap w[2];         // [E][N][bytes of a row], boxes of 128 bytes x 32 or 64 rows, swizzled
     const ep_bf16 *scale[2];  // 4-bit weights: [E][N][Kp / G]
     const ep_bf16 *x;
     const int32_t *expert_offset;
@@ -43,14 +52,18 @@ struct StreamParams {
     int32_t *error;
 };
 
+// Nibbles i and i + 4 of a word: as the bf16 values 128 + v, or v - 8.
+template <bool OFF>
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
     uint32_t v;
     // (word >> 4 i) & 0x000F000F | 0x43004300
     asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)));
+    if (!OFF) return v;
     const __nv_bfloat162 m = __float2bfloat162_rn(136.0f);
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), m);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -66,9 +79,9 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i ==
 template <int G>
 struct StreamShape {
     static constexpr int kStageK = G == 0 ? 128 : 512;
-    static constexpr int kWarpK = kStageK / 2;     // k of a stage that one warp takes
-    static constexpr int kPartK = kWarpK / 2;      // taken at a time: 64 bytes of a weight row
-    static constexpr int kVecs = kPartK / 32;      // 16-byte words of x for it
+    static constexpr int kWarpK = kStageK / 2;                  // k of a stage that one warp takes
+    static constexpr int kPartK = kWarpK / 2;                   // taken at a time: 64 bytes of a weight row
+    static constexpr int kVecs = kPartK / 32;                   // 16-byte words of x for it
 };
 
 // The scales of 128 k of a row, from k `off` on: one bf16 (G = 128), two or four of them.
@@ -84,12 +97,32 @@ __device__ __forceinline__ uint2 load_scales(const ep_bf16 *row, int off) {
         return make_uint2(0, 0);
 }
 
+// An expert that has rows.
+struct StreamExpert {
+    int e, first, rows;
+};
+// The work items of one CTA, item blockIdx.x + i gridDim.x for i = 0, 1, ...: each a block of output
+// columns of an expert. Stepped through without a division, which every warp would wait for.
+struct StreamItems {
+    const StreamExpert *experts;  // those that have rows, in shared memory
+    int count, blocks;
+    int index, block;
+    __device__ StreamItems(const StreamExpert *x, int n, int b)
+        : experts(x), count(n), blocks(b), index((int)(blockIdx.x / (unsigned)b)), block((int)(blockIdx.x % (unsigned)b)) {}
+    __device__ bool any() const { return index < count; }
+    __device__ void next() {
+        block += gridDim.x;
+        while (block >= blocks && index < count) block -= blocks, ++index;
+    }
+};
+
 // What one consumer warp does with the work items' stages.
 struct StreamWarp {
     unsigned char *stages;
     uint64_t *full, *empty;
     volatile int *failed;
     uint32_t it;
+    bool ready;  // stage `it` has been seen to be there
     int lane, m, half;
 };
 
@@ -110,8 +143,8 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
         const size_t row_groups = (size_t)((p.K + 127) / 128) * (128 / G);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int n = n0 + (GATED ? r0 % 64 : r0) + 8 * h;  // past the last: that one, not stored
-            sc[h] = p.scale[GATED && w.m >= 4] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.half * (Sh::kWarpK / G);
+            const int n = n0 + (GATED ? r0 % (kStreamRows / 2) : r0) + 8 * h;  // past the last: that one, not stored
+            sc[h] = p.scale[GATED && w.m >= kStreamRows / 32] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.half * (Sh::kWarpK / G);
         }
     }
     const ep_bf16 *x[NT];
@@ -138,74 +171,95 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
 #pragma unroll
         for (int h = 0; h < 2; ++h) a.scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc[h], off);
     };
-    const auto fetch_any = [&](int b, int part, Ahead &a) {
-        if ((b + 1) * Sh::kStageK <= p.K)
-            fetch(std::false_type{}, b, part, a);
-        else
-            fetch(std::true_type{}, b, part, a);
-    };
     const auto scale_of = [](const uint2 &v, int i) {
         return __uint_as_float(((i / 2 ? v.y : v.x) >> (16 * (i % 2))) << 16);
     };
 
     float acc[NT][4] = {};
-    const auto multiply = [&](const Ahead &a, const uint4 &q0, const uint4 &q1) {
+    // PARTS parts at once, their chains of dependent products side by side
+    const auto multiply = [&](auto parts, const Ahead *a, const uint4 (*q)[2]) {
+        constexpr int P = decltype(parts)::value;
         if constexpr (G == 0) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                mma_16816(acc[i], q0.x, q1.x, q0.y, q1.y, a.x[i][0].x, a.x[i][0].y);
-                mma_16816(acc[i], q0.z, q1.z, q0.w, q1.w, a.x[i][0].z, a.x[i][0].w);
-            }
+            for (int h = 0; h < P; ++h)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    mma_16816(acc[i], q[h][0].x, q[h][1].x, q[h][0].y, q[h][1].y, a[h].x[i][0].x, a[h].x[i][0].y);
+                    mma_16816(acc[i], q[h][0].z, q[h][1].z, q[h][0].w, q[h][1].w, a[h].x[i][0].z, a[h].x[i][0].w);
+                }
         } else {
-            float part[NT][4] = {};
+            constexpr bool kOff = NT > 1;  // 136 is taken off the values, not off the sums
+            float sum[P][NT][4] = {}, xs[P][4] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w0 = word_of(q0, j), w1 = word_of(q1, j);
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    const uint32_t a0 = w4_pair(w0, 2 * step), a1 = w4_pair(w1, 2 * step);
-                    const uint32_t a2 = w4_pair(w0, 2 * step + 1), a3 = w4_pair(w1, 2 * step + 1);
+                for (int h = 0; h < P; ++h) {
+                    const Ahead &b = a[h];
+                    const uint32_t w0 = word_of(q[h][0], j), w1 = word_of(q[h][1], j);
+                    if constexpr (!kOff) {
+                        mma_16816(xs[h], kOnes, kOnes, kOnes, kOnes, b.x[0][j].x, b.x[0][j].y);
+                        mma_16816(xs[h], kOnes, kOnes, kOnes, kOnes, b.x[0][j].z, b.x[0][j].w);
+                    }
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        mma_16816(part[i], a0, a1, a2, a3, step ? a.x[i][j].z : a.x[i][j].x, step ? a.x[i][j].w : a.x[i][j].y);
+                    for (int step = 0; step < 2; ++step) {
+                        const uint32_t a0 = w4_pair<kOff>(w0, 2 * step), a1 = w4_pair<kOff>(w1, 2 * step);
+                        const uint32_t a2 = w4_pair<kOff>(w0, 2 * step + 1), a3 = w4_pair<kOff>(w1, 2 * step + 1);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            mma_16816(sum[h][i], a0, a1, a2, a3, step ? b.x[i][j].z : b.x[i][j].x,
+                                      step ? b.x[i][j].w : b.x[i][j].y);
+                    }
+                    if ((32 * (j + 1)) % G == 0) {
+                        const float f[2] = {scale_of(b.scale[0], 32 * j / G), scale_of(b.scale[1], 32 * j / G)};
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = kOff ? sum[h][i][r] : fmaf(-136.0f, xs[h][r % 2], sum[h][i][r]);
+                                acc[i][r] = fmaf(f[r / 2], v, acc[i][r]);
+                                sum[h][i][r] = 0.0f;
+                            }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) xs[h][r] = 0.0f;
+                    }
                 }
-                if ((32 * (j + 1)) % G == 0) {
-                    const float f[2] = {scale_of(a.scale[0], 32 * j / G), scale_of(a.scale[1], 32 * j / G)};
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            acc[i][r] = fmaf(f[r / 2], part[i][r], acc[i][r]);
-                            part[i][r] = 0.0f;
-                        }
-                }
-            }
         }
     };
     const int u0 = t ^ (r0 & 7), u1 = (4 + t) ^ (r0 & 7);  // the two parts' words of the row
-    // one row of tokens leaves registers for a stage's first part ahead of it; the second is fetched
-    // ahead of the wait
-    constexpr bool kDeep = NT == 1;
-    Ahead a0, a1;
-    if (kDeep) fetch_any(0, 0, a0);
-    for (int b = 0; b < kb; ++b, ++w.it) {
+    // A stage, without a branch from the wait on: loads and products of both parts can move past each other.
+    const auto stage = [&](auto check, int b) {
         const uint32_t s = w.it % kStreamStages;
+        Ahead a[2];
+        fetch(check, b, 0, a[0]);
+        if constexpr (NT == 1) fetch(check, b, 1, a[1]);  // the registers allow it
+        if (!w.ready) {
+            if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
+            __syncwarp();  // the barrier's completion was seen by one lane; the others' reads are ordered behind it
+        }
         const uint4 *from = at + s * (kStreamStageBytes / 16);
-        fetch_any(b, kDeep ? 1 : 0, kDeep ? a1 : a0);
-        if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
-        __syncwarp();
-        // the barrier's completion was seen by one lane; the others' reads are ordered behind it here
-        const uint4 q00 = from[u0], q01 = from[u0 + 64], q10 = from[u1], q11 = from[u1 + 64];
+        const uint4 q[2][2] = {{from[u0], from[u0 + 64]}, {from[u1], from[u1 + 64]}};
         __syncwarp();
         if (w.lane == 0) mbar_arrive(&w.empty[s]);
-        multiply(a0, q00, q01);
-        if (!kDeep) fetch_any(b, 1, a1);
+        ++w.it;
+        // every lane asks whether the next stage is there: the answer's latency is behind the products
+        const bool there = mbar_test(&w.full[w.it % kStreamStages], (w.it / kStreamStages) & 1);
+        if constexpr (NT == 1) {
+            multiply(std::integral_constant<int, 2>{}, a, q);
+        } else {
+            multiply(std::integral_constant<int, 1>{}, a, q);
+            asm volatile("" ::: "memory");  // not earlier: the registers are the first part's
+            fetch(check, b, 1, a[0]);
+            multiply(std::integral_constant<int, 1>{}, a, q + 1);
+        }
+        w.ready = __all_sync(0xFFFFFFFFu, there);
 #pragma unroll
         for (int i = 0; i < NT; ++i) x[i] += Sh::kStageK;
         if constexpr (G > 0) sc[0] += Sh::kStageK / G, sc[1] += Sh::kStageK / G;
-        if (kDeep && b + 1 < kb) fetch_any(b + 1, 0, a0);
-        multiply(a1, q10, q11);
-    }
+    };
+    const int whole = p.K / Sh::kStageK;
+#pragma unroll 1
+    for (int b = 0; b < whole; ++b) stage(std::false_type{}, b);
+    if (whole < kb) stage(std::true_type{}, whole);
     float *mine = red + (size_t)w.half * kStreamTokens * kStreamRows;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -216,10 +270,12 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
 // The line of `p` into L1.
 __device__ __forceinline__ void ask_for_line(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory"); }
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory");
+}
 
 template <bool GATED, int G>
-__global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const __grid_constant__ StreamParams p) {
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_kernel(const __grid_constant__ StreamParams p) {
     using Sh = StreamShape<G>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kStreamStages], empty[kStreamStages];
@@ -228,8 +284,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
     unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     // two buffers [half][token][row]: one takes a pass's sums while the other is still read
     float *red = reinterpret_cast<float *>(stages + kStreamStages * kStreamStageBytes);
-    constexpr int kRed = 2 * kStreamTokens * kStreamRows;
-    int *hit = reinterpret_cast<int *>(red + 2 * kRed);  // experts that have rows
+    StreamExpert *hit = reinterpret_cast<StreamExpert *>(red + 2 * kStreamRed);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStreamStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kStreamWarps);
@@ -244,13 +299,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
         int n = 0;
         for (int base = 0; base < p.E; base += 32) {
             const int e = base + lane;
-            bool has = false;
+            int first = 0, rows = 0;
             if (e < p.E) {
-                const int first = min(max(p.expert_offset[e], 0), p.S);
-                has = min(p.expert_offset[e + 1], p.S) > first;
+                first = min(max(p.expert_offset[e], 0), p.S);
+                rows = min(p.expert_offset[e + 1], p.S) - first;
             }
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
-            if (has) hit[n + __popc(m & ((1u << lane) - 1))] = e;
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, rows > 0);
+            if (rows > 0) hit[n + __popc(m & ((1u << lane) - 1))] = StreamExpert{e, first, rows};
             n += __popc(m);
         }
         if (lane == 0) hits = n;
@@ -258,7 +313,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
     __syncthreads();
     constexpr int kOut = GATED ? kStreamRows / 2 : kStreamRows;  // output columns of a work item
     const int blocks = (p.N + kOut - 1) / kOut;
-    const int64_t items = (int64_t)hits * blocks;
+    StreamItems items(hit, hits, blocks);
     const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
 
     if (warp == kStreamWarps) {
@@ -267,10 +322,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
         // latency a stage.
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
-            const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
-            const int first = min(max(p.expert_offset[e], 0), p.S);
-            const int rows = min(p.expert_offset[e + 1], p.S) - first;
+        for (; ok && items.any(); items.next()) {
+            const auto [e, first, rows] = hit[items.index];
+            const int n0 = items.block * kOut;
             for (int done = 0; ok && done < rows; done += kStreamTokens)
                 for (int b = 0; b < kb; ++b, ++it) {
                     const int s = it % kStreamStages;
@@ -316,11 +370,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
     } else {
         // ---- consumers. After a failure they go on without waiting: every warp reaches the barriers.
         float *const red_begin = red;
-        StreamWarp w{stages, full, empty, &failed, 0, lane, warp / 2, warp % 2};
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-            const int e = hit[item / blocks], n0 = (int)(item % blocks) * kOut;
-            const int first = min(max(p.expert_offset[e], 0), p.S);
-            const int rows = min(p.expert_offset[e + 1], p.S) - first;
+        StreamWarp w{stages, full, empty, &failed, 0, false, lane, warp / 2, warp % 2};
+        for (; items.any(); items.next()) {
+            const auto [e, first, rows] = hit[items.index];
+            const int n0 = items.block * kOut;
             for (int done = 0; done < rows; done += kStreamTokens) {
                 const int tokens = min(rows - done, kStreamTokens);
                 const int64_t x0 = (int64_t)first + done;
@@ -339,7 +392,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
                     if (n0 + n < p.N)
                         reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)(x0 + token) * p.N + n0 + n] = __float2bfloat16_rn(v);
                 }
-                red = red == red_begin ? red_begin + kRed : red_begin;
+                red = red == red_begin ? red_begin + kStreamRed : red_begin;
             }
         }
     }
@@ -349,6 +402,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) expert_stream_kernel(const 
 
 template <bool GATED, int G>
 cudaError_t launch_stream(StreamParams &p, const void *w0, const void *w1, cudaStream_t s) {
+    using Sh = StreamShape<G>;
     auto kernel = expert_stream_kernel<GATED, G>;
     cudaError_t e = expert_error_word(&p.error);
     if (e != cudaSuccess) return e;
@@ -357,15 +411,15 @@ cudaError_t launch_stream(StreamParams &p, const void *w0, const void *w1, cudaS
     constexpr int kBytes = G == 0 ? 2 : 1;
     if (!make_map(&p.w[0], w0, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
     if (GATED && !make_map(&p.w[1], w1, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + 4 * kStreamTokens * kStreamRows * sizeof(float) +
-                        (size_t)p.E * sizeof(int);
+    const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + 2 * kStreamRed * sizeof(float) +
+                        (size_t)p.E * sizeof(StreamExpert);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     constexpr int kOut = GATED ? kStreamRows / 2 : kStreamRows;
     const int64_t most = (int64_t)(p.E < p.S ? p.E : p.S) * ((p.N + kOut - 1) / kOut);
     const int sms = current_device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    return launch_dependent(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(kStreamThreads), smem, s, p);
+    return launch_dependent(kernel, dim3((unsigned)(most < kStreamCtas * sms ? most : kStreamCtas * sms)), dim3(kStreamThreads), smem, s, p);
 }
 
 }  // namespace ep
