@@ -12,10 +12,9 @@ namespace ep {
 // by elements, 128 bytes wide and swizzled over 128 bytes. What lies outside reads as zero.
 bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by);
 
-// mbarrier.try_wait puts the thread to sleep until the phase completes, for kWaitSliceNs at most.
-// (Polled without that hint, by the epilogue's warps above all, the waits slowed the whole CTA: a
-// block of 8 rows took 91 us.) A wait that is not satisfied after kWaitSlices of them, about two
-// seconds, gives up; no wait of a kernel that works comes near it.
+// A wait gives up after about two seconds; no wait of a kernel that works comes near that, the
+// longest one spans a single tile's main loop. mbarrier.try_wait puts the thread to sleep until the
+// phase completes, for kWaitSliceNs at most: for waits that are long. One thread waits for its warp.
 constexpr uint32_t kWaitSliceNs = 2000000;
 constexpr int kWaitSlices = 1000;
 constexpr int64_t kPollLimitCycles = 4000000000ll;  // the same for a thread that polls
