@@ -143,7 +143,7 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: 
     # the usual case in one expression: a call of the path checks up to sixteen tensors, and at a
     # few microseconds each the steps below would cost more than its kernels
     if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape)
-            and t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice()):
+            and t.is_contiguous() and t.get_device() == torch.cuda.current_device()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -165,7 +165,7 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: 
 def _stream(stream):
     if stream is None:
         if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     elif stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream: on {stream.device}, but the current device is cuda:{torch.cuda.current_device()}")

@@ -194,7 +194,7 @@ class GradList:
         self.n = len(grads)
         self.records = (EpGradTensor * max(self.n, 1))()
         table = np.frombuffer(self.records, dtype=_GRAD_RECORD)[:self.n]
-        device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2  # -1: the CPU
+        device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # -1: the CPU
         if all(type(g) is torch.Tensor and g.dtype in _GRAD_TYPES and o.dtype is g.dtype and g.shape == o.shape
                and g.get_device() == device and o.get_device() == device and g.is_contiguous() and o.is_contiguous()
                for g, o in zip(grads, out)):
