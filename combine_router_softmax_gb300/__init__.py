@@ -136,14 +136,16 @@ def _check(status: int, what: str):
         raise EpError(status, what)
 
 
-def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: str):
-    """Device pointer of a contiguous CUDA tensor of the expected dtype/shape (None -> NULL)."""
+def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: str, device: int | None = None):
+    """Device pointer of a contiguous CUDA tensor of the expected dtype/shape (None -> NULL).
+
+    ``device``: the current device, where the caller has asked for it already (-1: none yet)."""
     if t is None:
         return None
     # the usual case in one expression: a call of the path checks up to sixteen tensors, and at a
     # few microseconds each the steps below would cost more than its kernels
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape)
-            and t.is_contiguous() and t.get_device() == torch.cuda.current_device()):
+    if (type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()
+            and t.is_cuda and t.get_device() == (torch.cuda.current_device() if device is None else device)):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -160,6 +162,11 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: 
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _device() -> int:
+    """The current device; -1 before CUDA is in use (no tensor is on one then)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
 
 
 def _stream(stream):

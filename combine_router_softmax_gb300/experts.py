@@ -12,7 +12,7 @@ import ctypes
 import numpy as np
 import torch
 
-from . import EpConfig, _check, _lib, _ptr, _stream
+from . import EpConfig, _check, _device, _lib, _ptr, _stream
 
 EXPORTS = ("ep_expert_ffn", "ep_expert_ffn_backward", "ep_w4_sizes", "ep_w4_pack", "ep_w4_linear", "ep_expert_ffn_w4",
            "ep_combine_backward", "ep_route_backward", "ep_grad_workspace_size", "ep_grad_norm", "ep_grad_clip")
@@ -64,13 +64,13 @@ def _declare() -> None:
 _declare()
 
 
-def _bf16(t, shape, name):
-    return _ptr(t, torch.bfloat16, shape, name)
+def _bf16(t, shape, name, device=None):
+    return _ptr(t, torch.bfloat16, shape, name, device)
 
 
-def _half(t, shape, name):
+def _half(t, shape, name, device=None):
     """Memory for 16-bit values: a float16 tensor, or a bfloat16 one of which nobody reads the values."""
-    return _ptr(t, torch.bfloat16 if t is not None and t.dtype is torch.bfloat16 else torch.float16, shape, name)
+    return _ptr(t, torch.bfloat16 if t is not None and t.dtype is torch.bfloat16 else torch.float16, shape, name, device)
 
 
 def ep_expert_ffn(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, h, y, g=None, u=None,
@@ -81,11 +81,12 @@ def ep_expert_ffn(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, h
     int32 [E + 1]. g and u (float16 [rows, I], both or neither) are what ep_expert_ffn_backward needs besides h;
     they are written as halves, into bfloat16 tensors too, which are then storage only."""
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
-    _check(_lib.ep_expert_ffn(ctypes.byref(cfg), _bf16(rows, (S, H), "rows"),
-                              _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
-                              _bf16(w_gate, (E, I, H), "w_gate"), _bf16(w_up, (E, I, H), "w_up"),
-                              _bf16(w_down, (E, H, I), "w_down"), _half(g, (S, I), "g"), _half(u, (S, I), "u"),
-                              _bf16(h, (S, I), "h"), _bf16(y, (S, H), "y"), _stream(stream)), "ep_expert_ffn")
+    dev = _device()
+    _check(_lib.ep_expert_ffn(ctypes.byref(cfg), _bf16(rows, (S, H), "rows", dev),
+                              _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset", dev),
+                              _bf16(w_gate, (E, I, H), "w_gate", dev), _bf16(w_up, (E, I, H), "w_up", dev),
+                              _bf16(w_down, (E, H, I), "w_down", dev), _half(g, (S, I), "g", dev), _half(u, (S, I), "u", dev),
+                              _bf16(h, (S, I), "h", dev), _bf16(y, (S, H), "y", dev), _stream(stream)), "ep_expert_ffn")
 
 
 def ep_expert_ffn_backward(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, g, u, h, d_y, d_g, d_u,
@@ -93,13 +94,14 @@ def ep_expert_ffn_backward(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, 
     """Gradients of ep_expert_ffn for d_y, the gradient of y. d_g and d_u bf16 [rows, I] are written on the
     way; d_rows and the weights' gradients (overwritten) are written where they are given."""
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
+    dev = _device()
     _check(_lib.ep_expert_ffn_backward(
-        ctypes.byref(cfg), _bf16(rows, (S, H), "rows"), _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
-        _bf16(w_gate, (E, I, H), "w_gate"), _bf16(w_up, (E, I, H), "w_up"), _bf16(w_down, (E, H, I), "w_down"),
-        _half(g, (S, I), "g"), _half(u, (S, I), "u"), _bf16(h, (S, I), "h"), _bf16(d_y, (S, H), "d_y"),
-        _bf16(d_g, (S, I), "d_g"), _bf16(d_u, (S, I), "d_u"), _bf16(d_rows, (S, H), "d_rows"),
-        _bf16(d_w_gate, (E, I, H), "d_w_gate"), _bf16(d_w_up, (E, I, H), "d_w_up"),
-        _bf16(d_w_down, (E, H, I), "d_w_down"), _stream(stream)), "ep_expert_ffn_backward")
+        ctypes.byref(cfg), _bf16(rows, (S, H), "rows", dev), _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset", dev),
+        _bf16(w_gate, (E, I, H), "w_gate", dev), _bf16(w_up, (E, I, H), "w_up", dev), _bf16(w_down, (E, H, I), "w_down", dev),
+        _half(g, (S, I), "g", dev), _half(u, (S, I), "u", dev), _bf16(h, (S, I), "h", dev), _bf16(d_y, (S, H), "d_y", dev),
+        _bf16(d_g, (S, I), "d_g", dev), _bf16(d_u, (S, I), "d_u", dev), _bf16(d_rows, (S, H), "d_rows", dev),
+        _bf16(d_w_gate, (E, I, H), "d_w_gate", dev), _bf16(d_w_up, (E, I, H), "d_w_up", dev),
+        _bf16(d_w_down, (E, H, I), "d_w_down", dev), _stream(stream)), "ep_expert_ffn_backward")
 
 
 def ep_w4_sizes(cfg: EpW4Config) -> tuple[int, int]:
@@ -109,11 +111,11 @@ def ep_w4_sizes(cfg: EpW4Config) -> tuple[int, int]:
     return q.value, s.value
 
 
-def _packed(cfg: EpW4Config, q, scale, name):
+def _packed(cfg: EpW4Config, q, scale, name, device=None):
     """Pointers of a packed weight: q uint8 [E, N, Kp / 2], scale bf16 [E, N, Kp / group]."""
     Kp = (cfg.K + 127) // 128 * 128
-    return (_ptr(q, torch.uint8, (cfg.E, cfg.N, Kp // 2), "q" + name),
-            _bf16(scale, (cfg.E, cfg.N, Kp // max(cfg.group, 1)), "scale" + name))
+    return (_ptr(q, torch.uint8, (cfg.E, cfg.N, Kp // 2), "q" + name, device),
+            _bf16(scale, (cfg.E, cfg.N, Kp // max(cfg.group, 1)), "scale" + name, device))
 
 
 def ep_w4_pack(cfg: EpW4Config, w, q, scale, stream=None) -> None:
@@ -124,9 +126,10 @@ def ep_w4_pack(cfg: EpW4Config, w, q, scale, stream=None) -> None:
 
 def ep_w4_linear(cfg: EpW4Config, x, expert_offset, q, scale, y, stream=None) -> None:
     """y[s] = W[e(s)] x[s] with packed 4-bit weights; x bf16 [rows, K], y bf16 [rows, N]."""
-    _check(_lib.ep_w4_linear(ctypes.byref(cfg), _bf16(x, (cfg.rows, cfg.K), "x"),
-                             _ptr(expert_offset, torch.int32, (cfg.E + 1,), "expert_offset"),
-                             *_packed(cfg, q, scale, ""), _bf16(y, (cfg.rows, cfg.N), "y"), _stream(stream)),
+    dev = _device()
+    _check(_lib.ep_w4_linear(ctypes.byref(cfg), _bf16(x, (cfg.rows, cfg.K), "x", dev),
+                             _ptr(expert_offset, torch.int32, (cfg.E + 1,), "expert_offset", dev),
+                             *_packed(cfg, q, scale, "", dev), _bf16(y, (cfg.rows, cfg.N), "y", dev), _stream(stream)),
            "ep_w4_linear")
 
 
@@ -136,31 +139,34 @@ def ep_expert_ffn_w4(cfg: EpFfnConfig, group: int, rows, expert_offset, q_gate, 
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
     wide = EpW4Config.make(N=I, K=H, E=E, group=group)
     down = EpW4Config.make(N=H, K=I, E=E, group=group)
-    _check(_lib.ep_expert_ffn_w4(ctypes.byref(cfg), ctypes.c_int32(group), _bf16(rows, (S, H), "rows"),
-                                 _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset"),
-                                 *_packed(wide, q_gate, s_gate, "_gate"), *_packed(wide, q_up, s_up, "_up"),
-                                 *_packed(down, q_down, s_down, "_down"), _bf16(h, (S, I), "h"),
-                                 _bf16(y, (S, H), "y"), _stream(stream)), "ep_expert_ffn_w4")
+    dev = _device()
+    _check(_lib.ep_expert_ffn_w4(ctypes.byref(cfg), ctypes.c_int32(group), _bf16(rows, (S, H), "rows", dev),
+                                 _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset", dev),
+                                 *_packed(wide, q_gate, s_gate, "_gate", dev), *_packed(wide, q_up, s_up, "_up", dev),
+                                 *_packed(down, q_down, s_down, "_down", dev), _bf16(h, (S, I), "h", dev),
+                                 _bf16(y, (S, H), "y", dev), _stream(stream)), "ep_expert_ffn_w4")
 
 
 def ep_combine_backward(cfg: EpConfig, d_out, y, slot, topk_w, d_y, d_topk_w, stream=None) -> None:
     """d_out bf16 [T, H], y bf16 [T*k, H] -> d_y bf16 [T*k, H] (slot order), d_topk_w fp32 [T, k]."""
     T, H, k = cfg.T, cfg.H, cfg.k
-    _check(_lib.ep_combine_backward(ctypes.byref(cfg), _bf16(d_out, (T, H), "d_out"), _bf16(y, (T * k, H), "y"),
-                                    _ptr(slot, torch.int32, (T, k), "slot"),
-                                    _ptr(topk_w, torch.float32, (T, k), "topk_w"), _bf16(d_y, (T * k, H), "d_y"),
-                                    _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(stream)),
+    dev = _device()
+    _check(_lib.ep_combine_backward(ctypes.byref(cfg), _bf16(d_out, (T, H), "d_out", dev), _bf16(y, (T * k, H), "y", dev),
+                                    _ptr(slot, torch.int32, (T, k), "slot", dev),
+                                    _ptr(topk_w, torch.float32, (T, k), "topk_w", dev), _bf16(d_y, (T * k, H), "d_y", dev),
+                                    _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w", dev), _stream(stream)),
            "ep_combine_backward")
 
 
 def ep_route_backward(cfg: EpConfig, logits, topk_idx, topk_w, d_topk_w, d_logits, stream=None) -> None:
     """d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]; logits may be None where cfg.renormalize is 1."""
     T, E, k = cfg.T, cfg.E, cfg.k
-    _check(_lib.ep_route_backward(ctypes.byref(cfg), _ptr(logits, torch.float32, (T, E), "logits"),
-                                  _ptr(topk_idx, torch.int32, (T, k), "topk_idx"),
-                                  _ptr(topk_w, torch.float32, (T, k), "topk_w"),
-                                  _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"),
-                                  _ptr(d_logits, torch.float32, (T, E), "d_logits"), _stream(stream)),
+    dev = _device()
+    _check(_lib.ep_route_backward(ctypes.byref(cfg), _ptr(logits, torch.float32, (T, E), "logits", dev),
+                                  _ptr(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+                                  _ptr(topk_w, torch.float32, (T, k), "topk_w", dev),
+                                  _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w", dev),
+                                  _ptr(d_logits, torch.float32, (T, E), "d_logits", dev), _stream(stream)),
            "ep_route_backward")
 
 
