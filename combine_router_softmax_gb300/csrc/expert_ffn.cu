@@ -129,7 +129,7 @@ cudaError_t run_rows(GemmParams &p, const RowProduct &r, cudaStream_t s) {
         if (r.a[i] && !rows_map(p, i, r.a[i], p.K)) return cudaErrorInvalidValue;
         if (!r.b[i]) continue;
         // weights [E, N, K], or [E, K, N] where the product contracts their rows
-        constexpr int kBoxN = OP == ExpertOp::kGateUp ? NB / 2 : Sh::kBRows;
+        constexpr int kBoxN = OP == ExpertOp::kGateUp ? Sh::kGate : Sh::kBRows;
         const bool ok = Sh::kBMn ? make_map(&p.b[i], r.b[i], 2, p.N[0], p.K, p.E, 64, kGemmBK)
                                  : make_map(&p.b[i], r.b[i], 2, p.K, p.N[0], p.E, kGemmBK, kBoxN);
         if (!ok) return cudaErrorInvalidValue;

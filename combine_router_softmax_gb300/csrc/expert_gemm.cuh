@@ -20,9 +20,8 @@
 // results. Every wait has a time limit (kErrExpertWait).
 //
 // What bounds it. With many rows the tensor pipe: 8 experts x 1024 rows, 4096 to 2048 and
-// back, forward 247 us = 1671 TFLOP/s, DGateUp 1262, DRows 1711, DWeight 1620 (8 KB stages of
-// one k a row, and 64 KB written for every 16 stages); 16 experts of uneven size lose the empty
-// half of their last tiles. As single CTAs the same forward took 270 us or more: 128 x 256 tiles
+// back, forward 246 us = 1676 TFLOP/s, DGateUp 1277, DRows 1741, DWeight 1614 (64 KB written for
+// every 16 stages); 16 experts of uneven size lose what their last tiles do not fill. As single CTAs the same forward took 270 us or more: 128 x 256 tiles
 // move 48 KB into shared memory and read 48 KB out for 512 cycles of MMA, 192 bytes a cycle
 // where there are 128; a pair's 256 x 256 halves what each SM moves. With few rows an expert the
 // weights' stream: 512 rows over 64 experts of 7168 / 2048 in 826 us = 6.8 TB/s.
@@ -63,6 +62,7 @@ struct GemmShape {
     static constexpr bool kBMn = OP == ExpertOp::kDGateUp || OP == ExpertOp::kDRows || kDW;
     static constexpr int kOutN = OP == ExpertOp::kGateUp ? NB / 2 : NB;  // output columns of a tile
     static constexpr int kCols = kOutN < 64 ? kOutN : 64;  // columns the epilogue takes at a time
+    static constexpr int kGate = kCols;                    // GateUp: B is so many rows of Wg, as many of Wu, and so on
     static constexpr int kBRows = NB / CG;                               // B rows a CTA holds
     static constexpr int kABytes = kGemmBM * 128;
     static constexpr int kBBytes = kBRows * 128;
@@ -210,8 +210,17 @@ struct Walk {
 // Rows of A that are fetched for a CTA with `valid` rows left: one box of 128, or as many of
 // 16 as hold them. The MMA computes all 128 rows; what lies in the others reaches only
 // result rows that are not stored.
-__device__ __forceinline__ int a_rows_fetched(int valid) {
+__device__ __forceinline__ int a_rows_fetched(int valid, int most) {
+    valid = min(valid, most);
     return valid <= 0 ? 0 : valid > 96 ? kGemmBM : (valid + 15) / 16 * 16;
+}
+
+// A CTA pair's last tile of an expert, when 128 rows or fewer are left: half the MMA (M = 128), 64 rows
+// a CTA. Its accumulator lies in half the columns: lanes 0 to 63 hold the rows' first half of the N
+// columns, lanes 64 to 127 the second.
+template <ExpertOp OP, int CG>
+__device__ __forceinline__ bool half_tile(const Tile &t) {
+    return CG == 2 && OP != ExpertOp::kDWeight && t.valid <= kGemmBM;
 }
 
 // DWeight: a stage whose rows go past the expert's end also holds rows of the next one, which
@@ -302,12 +311,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
-                const int fetched = Sh::kDW ? 0 : a_rows_fetched(t.valid - (int)rank * kGemmBM);
+                const int most = half_tile<OP, CG>(t) ? kGemmBM / 2 : kGemmBM;  // rows of a CTA
+                const int fetched = Sh::kDW ? 0 : a_rows_fetched(t.valid - (int)rank * most, most);
                 uint32_t bytes = Sh::kBBytes * CG;
                 if constexpr (Sh::kDW)
                     bytes += Sh::kABytes * CG;
                 else
-                    for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * kGemmBM) * 128;
+                    for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * most, most) * 128;
                 for (int b = 0; b < kb; ++b, ++it) {
                     const int s = it % kStages;
                     if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], (it / kStages - 1) & 1, &failed)) {
@@ -331,19 +341,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     } else {
                         const int half = OP == ExpertOp::kDRows && b >= kb / 2 ? 1 : 0;
                         const int k = (half ? b - kb / 2 : b) * kGemmBK;
-                        const int row = t.m0 + (int)rank * kGemmBM;
+                        const int row = t.m0 + (int)rank * most;
                         if (fetched == kGemmBM)
                             tma_load_2d<CG>(sa, &p.a[half], k, row, bar);
                         else
                             for (int i = 0; i < fetched; i += 16)
                                 tma_load_2d<CG>(sa + i * 128, &p.a16[half], k, row + i, bar);
                         if constexpr (OP == ExpertOp::kGateUp) {
-                            if constexpr (CG == 2)
-                                tma_load_3d<CG>(sb, &p.b[rank], k, t.n0, t.e, bar);
-                            else {
-                                tma_load_3d<CG>(sb, &p.b[0], k, t.n0, t.e, bar);
-                                tma_load_3d<CG>(sb + Sh::kBBytes / 2, &p.b[1], k, t.n0, t.e, bar);
-                            }
+#pragma unroll
+                            for (int i = 0; i < Sh::kBRows / Sh::kGate; ++i)
+                                tma_load_3d<CG>(sb + i * Sh::kGate * 128, &p.b[i % 2], k,
+                                                t.n0 + (int)rank * (Sh::kBRows / 2) + i / 2 * Sh::kGate, t.e, bar);
                         } else if constexpr (!Sh::kBMn) {
                             tma_load_3d<CG>(sb, &p.b[0], k, t.n0 + (int)rank * Sh::kBRows, t.e, bar);
                         } else {
@@ -371,7 +379,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
     } else if (warp == 1) {
         // ---- MMA issuer (CG = 2: of the pair's first CTA)
         if (rank == 0) {
-            constexpr uint32_t idesc = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
+            constexpr uint32_t idesc_whole = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
+            constexpr uint32_t idesc_half = mma_idesc(kGemmBM, NB, Sh::kAMn, Sh::kBMn);
             uint32_t it = 0, acc_it = 0, relayed = 0;
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
@@ -379,6 +388,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 if (kb == 0) continue;
                 const uint32_t slot = acc_it & 1;
                 const uint32_t d = tmem + slot * NB;
+                const uint32_t idesc = half_tile<OP, CG>(t) ? idesc_half : idesc_whole;
                 // the stage's MMAs; one thread
                 const auto issue = [&](uint32_t s, int steps, int b) {
                     const uint32_t sa = smem_u32(stages + s * Sh::kStageBytes);
@@ -443,7 +453,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
     } else {
         // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread
         const int quarter = warp % 4;
-        const int r0 = (int)rank * kGemmBM + quarter * 32;  // the warp's first row within the tile
         unsigned char *slab = slabs + quarter * kSlabBytes;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         uint32_t acc_it = 0;
@@ -457,11 +466,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 ++acc_it;
                 tmem_fence_after();
             }
+            // the warp's first row within the tile; its columns of the accumulator
+            const bool half = half_tile<OP, CG>(t);
+            const int r0 = half ? (int)rank * (kGemmBM / 2) + quarter % 2 * 32 : (int)rank * kGemmBM + quarter * 32;
+            const int c_begin = half ? quarter / 2 * (Sh::kOutN / 2) : 0, c_end = half ? c_begin + Sh::kOutN / 2 : Sh::kOutN;
             const int rows = min(t.valid - r0, 32);  // of this warp's 32 that count
-            const uint32_t src = tmem + lanes + slot * NB;
+            // where the tile's column 0 would be for this warp
+            const uint32_t src = tmem + lanes + slot * NB - (half ? quarter / 2 * (NB / 2) : 0);
             const int N = p.N[t.problem];
             const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r0 : (size_t)t.m0 + r0;
-            for (int c = 0; rows > 0 && c < Sh::kOutN && t.n0 + c < N; c += Sh::kCols) {
+            for (int c = c_begin; rows > 0 && c < c_end && t.n0 + c < N; c += Sh::kCols) {
                 const int n = t.n0 + c;
                 if constexpr (OP == ExpertOp::kDGateUp) {
                     uint4 gq[8], uq[8];
@@ -477,14 +491,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     slab_get(slab, lane, 1, u[1]);
                     __syncwarp();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int part = 0; part < 2; ++part) {
                         uint32_t v[32], o[16];
-                        tmem_load_32(src + c + 32 * half, v);
+                        tmem_load_32(src + c + 32 * part, v);
                         tmem_wait_ld(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float dg[2], du[2];
-                            const float2 g2 = half_values(g[half][i]), u2 = half_values(u[half][i]);
+                            const float2 g2 = half_values(g[part][i]), u2 = half_values(u[part][i]);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const float dh = __uint_as_float(v[2 * i + k]);
@@ -494,9 +508,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                                 dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
                             }
                             o[i] = bf16_pair(dg[0], dg[1]);
-                            u[half][i] = bf16_pair(du[0], du[1]);
+                            u[part][i] = bf16_pair(du[0], du[1]);
                         }
-                        slab_put(slab, lane, half, o);
+                        slab_put(slab, lane, part, o);
                     }
                     slab_store<Sh::kCols>(slab, lane, p.out[0] + row * N, N, n, rows);
                     slab_put(slab, lane, 0, u[0]);
@@ -506,10 +520,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     // what: 0 h, 1 g, 2 u; each takes its columns from TMEM anew
                     for (int what = 0; what < (p.g ? 3 : 1); ++what) {
 #pragma unroll
-                        for (int half = 0; half < Sh::kCols / 32; ++half) {
+                        for (int part = 0; part < Sh::kCols / 32; ++part) {
                             uint32_t v[32], w[32], o[16];
-                            tmem_load_32(src + c + 32 * half, v);
-                            tmem_load_32(src + Sh::kOutN + c + 32 * half, w);
+                            tmem_load_32(src + 2 * c + 32 * part, v);
+                            tmem_load_32(src + 2 * c + Sh::kGate + 32 * part, w);
                             tmem_wait_ld(v);
                             tmem_wait_ld(w);
 #pragma unroll
@@ -520,23 +534,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                                        : what == 1 ? half_pair(g0, g1)
                                                    : half_pair(u0, u1);
                             }
-                            slab_put(slab, lane, half, o);
+                            slab_put(slab, lane, part, o);
                         }
                         ep_bf16 *out = what == 0 ? p.out[0] : what == 1 ? p.g : p.u;
                         slab_store<Sh::kCols>(slab, lane, out + row * N, N, n, rows);
                     }
                 } else {
 #pragma unroll
-                    for (int half = 0; half < Sh::kCols / 32; ++half) {
+                    for (int part = 0; part < Sh::kCols / 32; ++part) {
                         uint32_t v[32], o[16];
                         if (!none) {
-                            tmem_load_32(src + c + 32 * half, v);
+                            tmem_load_32(src + c + 32 * part, v);
                             tmem_wait_ld(v);
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        slab_put(slab, lane, half, o);
+                        slab_put(slab, lane, part, o);
                     }
                     slab_store<Sh::kCols>(slab, lane, p.out[t.problem] + row * N, N, n, rows);
                 }

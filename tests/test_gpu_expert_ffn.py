@@ -88,6 +88,7 @@ CASES = [
     ([0, 0, 300], 1000, 360, 0, 0),               # leading experts without rows
     ([700, 0, 11], 2056, 136, 7, 130),            # long contraction, one wide and one narrow expert
     ([2] * 200, 128, 64, 0, 0),                   # more experts than SMs
+    ([513, 576, 577, 639, 640, 641], 1536, 1544, 0, 1),  # CTA pairs: last tiles of 1 to 129 rows
 ]
 
 
