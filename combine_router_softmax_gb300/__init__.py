@@ -166,13 +166,13 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple | None, name: 
 
 def _device() -> int:
     """The current device; -1 before CUDA is in use (no tensor is on one then)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
 def _stream(stream):
     if stream is None:
         if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     elif stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream: on {stream.device}, but the current device is cuda:{torch.cuda.current_device()}")

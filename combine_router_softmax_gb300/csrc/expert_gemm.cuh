@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
         // ---- producer: one lane fetches the stages of every tile in turn
         if (elect_one()) {
             uint32_t it = 0, relayed = 0, ever = 0;
+            uint32_t s = 0, phase = 0;  // it % kStages, it / kStages % 2: kept by counting, a stage is few instructions
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
@@ -319,12 +320,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 else
                     for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * most, most) * 128;
                 for (int b = 0; b < kb; ++b, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], (it / kStages - 1) & 1, &failed)) {
+                    if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], phase ^ 1, &failed)) {
                         ok = false;
                         break;
                     }
-                    ready = it + 1 >= kStages && mbar_test(&empty[(it + 1) % kStages], ((it + 1) / kStages - 1) & 1);
+                    const uint32_t next = s + 1 == kStages ? 0 : s + 1, next_phase = next == 0 ? phase ^ 1 : phase;
+                    ready = it + 1 >= kStages && mbar_test(&empty[next], next_phase ^ 1);
                     const bool relay = kRelay && t.rows - b * kGemmBK < kGemmBK;
                     if (rank == 0 || relay) mbar_arrive_expect_tx(&full[s], relay ? bytes / 2 : bytes);
                     if (relay) relayed ^= 1u << s, ever |= 1u << s;
@@ -361,6 +362,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                                                 t.e, bar);
                         }
                     }
+                    s = next;
+                    phase = next_phase;
                 }
             }
             // no copy may be under way when the CTA ends: after a failure nobody else waits for them
@@ -381,7 +384,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
         if (rank == 0) {
             constexpr uint32_t idesc_whole = mma_idesc(kGemmBM * CG, NB, Sh::kAMn, Sh::kBMn);
             constexpr uint32_t idesc_half = mma_idesc(kGemmBM, NB, Sh::kAMn, Sh::kBMn);
-            uint32_t it = 0, acc_it = 0, relayed = 0;
+            const uint64_t da_first = smem_desc(smem_u32(stages), Sh::kAMn ? 8192 : 16);
+            const uint64_t db_first = smem_desc(smem_u32(stages) + Sh::kABytes, Sh::kBMn ? 8192 : 16);
+            uint32_t s = 0, phase = 0, acc_it = 0, relayed = 0;
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
@@ -391,9 +396,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 const uint32_t idesc = half_tile<OP, CG>(t) ? idesc_half : idesc_whole;
                 // the stage's MMAs; one thread
                 const auto issue = [&](uint32_t s, int steps, int b) {
-                    const uint32_t sa = smem_u32(stages + s * Sh::kStageBytes);
-                    const uint64_t da = smem_desc(sa, Sh::kAMn ? 8192 : 16);
-                    const uint64_t db = smem_desc(sa + Sh::kABytes, Sh::kBMn ? 8192 : 16);
+                    const uint64_t da = da_first + s * (Sh::kStageBytes / 16), db = db_first + s * (Sh::kStageBytes / 16);
                     for (int k = 0; k < steps; ++k)
                         mma_bf16<CG>(d, da + k * (Sh::kAMn ? 128 : 2), db + k * (Sh::kBMn ? 128 : 2), idesc, b + k > 0);
                     mma_commit<CG>(&empty[s]);
@@ -403,20 +406,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 if (elect_one()) {
                     if (acc_it >= 2) ok = mbar_poll_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed);
                     tmem_fence_after();
+                    uint32_t at = s, parity = phase;
                     for (int b = 0; ok && b < whole; ++b) {
-                        const uint32_t i = it + b, s = i % kStages;
-                        ok = ready || mbar_poll_limited(&full[s], (i / kStages) & 1, &failed);
-                        ready = mbar_test(&full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
-                        if (ok) issue(s, kGemmBK / 16, b);
+                        ok = ready || mbar_poll_limited(&full[at], parity, &failed);
+                        const uint32_t next = at + 1 == kStages ? 0 : at + 1;
+                        if (next == 0) parity ^= 1;
+                        ready = mbar_test(&full[next], parity);
+                        if (ok) issue(at, kGemmBK / 16, b);
+                        at = next;
                     }
                 }
                 __syncwarp();
+                phase ^= (s + whole) / kStages % 2;
+                s = (s + whole) % kStages;
                 if constexpr (Sh::kDW)
                     if (whole < kb) {
-                        const uint32_t s = (it + whole) % kStages;
                         ready = false;
                         // every lane waits: each is to see the copies that it zeroes a part of
-                        ok = !failed && mbar_wait_limited(&full[s], ((it + whole) / kStages) & 1, &failed);
+                        ok = !failed && mbar_wait_limited(&full[s], phase, &failed);
                         const int steps = zero_rows_past_end<Sh>(stages + s * Sh::kStageBytes, t.rows - whole * kGemmBK, lane);
                         if (kRelay && ok) {
                             ok = mbar_wait_limited<true>(&other[s], relayed >> s & 1, &failed);
@@ -424,9 +431,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                         }
                         if (elect_one() && ok) issue(s, steps, whole);
                         __syncwarp();
+                        if (++s == kStages) s = 0, phase ^= 1;
                     }
                 ok = !failed;
-                it += kb;
                 ++acc_it;
             }
             if (failed) {  // MMAs may still read the stages and write TMEM
