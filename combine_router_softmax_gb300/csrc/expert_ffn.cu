@@ -53,7 +53,8 @@ namespace {
 
 // A operand of a row product: rows x k.
 bool rows_map(GemmParams &p, int i, const ep_bf16 *base, int64_t k) {
-    return make_map(&p.a[i], base, 2, k, p.S, 0, kGemmBK, kGemmBM) && make_map(&p.a16[i], base, 2, k, p.S, 0, kGemmBK, 16);
+    return make_map(&p.a[i], base, 2, k, p.S, 0, kGemmBK, 128) && make_map(&p.a64[i], base, 2, k, p.S, 0, kGemmBK, 64) &&
+           make_map(&p.a16[i], base, 2, k, p.S, 0, kGemmBK, 16);
 }
 
 template <ExpertOp OP, int CG, int NB>

@@ -42,7 +42,7 @@ constexpr int kSlabBytes = 32 * 128;
 
 struct GemmParams {
     CUtensorMap a[3];    // K-major: box 64 k x 128 rows; MN-major: box 64 m x 64 k
-    CUtensorMap a16[2];  // K-major: box 64 k x 16 rows, for tiles with few rows
+    CUtensorMap a64[2], a16[2];  // K-major: boxes of 64 and 16 rows, for tiles with few rows
     CUtensorMap b[3];
     const int32_t *expert_offset;
     int32_t E, S;
@@ -207,12 +207,13 @@ struct Walk {
     }
 };
 
-// Rows of A that are fetched for a CTA with `valid` rows left: one box of 128, or as many of
-// 16 as hold them. The MMA computes all 128 rows; what lies in the others reaches only
-// result rows that are not stored.
+// Rows of A that are fetched for a CTA with `valid` rows left, of `most`: one box of 128 or 64, or one or
+// two of 16. A copy costs its thread about 60 cycles whatever its size, so more than 32 rows are one box
+// (prefill with uneven experts 892 -> 868 us). The MMA computes all rows; what lies in the others reaches
+// only result rows that are not stored.
 __device__ __forceinline__ int a_rows_fetched(int valid, int most) {
     valid = min(valid, most);
-    return valid <= 0 ? 0 : valid > 96 ? kGemmBM : (valid + 15) / 16 * 16;
+    return valid <= 0 ? 0 : valid > 64 ? 128 : valid > 32 ? 64 : (valid + 15) / 16 * 16;
 }
 
 // A CTA pair's last tile of an expert, when 128 rows or fewer are left: half the MMA (M = 128), 64 rows
@@ -343,8 +344,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                         const int half = OP == ExpertOp::kDRows && b >= kb / 2 ? 1 : 0;
                         const int k = (half ? b - kb / 2 : b) * kGemmBK;
                         const int row = t.m0 + (int)rank * most;
-                        if (fetched == kGemmBM)
+                        if (fetched == 128)
                             tma_load_2d<CG>(sa, &p.a[half], k, row, bar);
+                        else if (fetched == 64)
+                            tma_load_2d<CG>(sa, &p.a64[half], k, row, bar);
                         else
                             for (int i = 0; i < fetched; i += 16)
                                 tma_load_2d<CG>(sa + i * 128, &p.a16[half], k, row + i, bar);

@@ -8,6 +8,10 @@
  * row-major, nothing allocated, arguments checked on the host before anything
  * is enqueued, status codes, work asynchronous on `stream`.
  *
+ * The kernels here are launched as programmatic dependents, as ep_combine is
+ * (ep.h): each waits for the kernel before it on the stream before it touches
+ * memory.
+ *
  * Rows lie grouped by expert, as ep_layout and ep_dispatch leave them: expert e
  * owns rows [expert_offset[e], expert_offset[e + 1]) of the row buffers, with
  * expert_offset (int32 [E + 1], device) non-decreasing and within [0, rows].
@@ -51,6 +55,8 @@ typedef struct ep_ffn_config {
  *          finer than bf16; beyond 65504 they are infinite (h and y are not)
  * h      : bf16 [rows, I] output
  * y      : bf16 [rows, H] output
+ * With and without g and u, and with few or many rows, other kernels may run,
+ * whose sums go in another order; the same call repeats bit by bit.
  * All 16-byte aligned. rows = 0 enqueues nothing. Outputs must not overlap
  * inputs. A CTA that gives up a bounded wait sets ep_device_error bit 4 (16).
  */
