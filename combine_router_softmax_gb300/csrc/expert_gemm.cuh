@@ -16,7 +16,7 @@
 //
 // One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
 // holding half of either operand): warp 0 feeds a ring of shared-memory stages by TMA, warp
-// 1 issues the MMAs into one of two accumulators, warps 2 to 5 turn the other one into
+// 1 issues the MMAs into one of two accumulators, warps 2 to 9 turn the other one into
 // results. Every wait has a time limit (kErrExpertWait).
 //
 // What bounds it. With many rows the tensor pipe: 8 experts x 1024 rows, 4096 to 2048 and
@@ -35,10 +35,11 @@ namespace ep {
 
 enum class ExpertOp { kGateUp, kDown, kDGateUp, kDRows, kDWeight };
 
-constexpr int kGemmThreads = 192;
+constexpr int kGemmThreads = 320;
+constexpr int kEpilogueWarps = 8;
 constexpr int kGemmBK = 64;   // contraction per stage: 128 bytes of bf16, one swizzled row
 constexpr int kGemmBM = 128;  // rows of a CTA's tile: the TMEM lanes
-constexpr int kSlabBytes = 32 * 128;
+constexpr int kSlabBytes = 32 * 64;
 
 struct GemmParams {
     CUtensorMap a[3];    // K-major: box 64 k x 128 rows; MN-major: box 64 m x 64 k
@@ -61,15 +62,14 @@ struct GemmShape {
     static constexpr bool kAMn = kDW;
     static constexpr bool kBMn = OP == ExpertOp::kDGateUp || OP == ExpertOp::kDRows || kDW;
     static constexpr int kOutN = OP == ExpertOp::kGateUp ? NB / 2 : NB;  // output columns of a tile
-    static constexpr int kCols = kOutN < 64 ? kOutN : 64;  // columns the epilogue takes at a time
-    static constexpr int kGate = kCols;                    // GateUp: B is so many rows of Wg, as many of Wu, and so on
-    static constexpr int kBRows = NB / CG;                               // B rows a CTA holds
+    static constexpr int kGate = kOutN < 64 ? kOutN : 64;  // GateUp: B is so many rows of Wg, as many of Wu, and so on
+    static constexpr int kBRows = NB / CG;                 // B rows a CTA holds
     static constexpr int kABytes = kGemmBM * 128;
     static constexpr int kBBytes = kBRows * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = 196608 / kStageBytes;
     static constexpr int kTmemCols = 2 * NB;
-    static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + 4 * kSlabBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
+    static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + kEpilogueWarps * kSlabBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -85,57 +85,53 @@ __device__ __forceinline__ float2 half_values(uint32_t v) { return __half22float
 // exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-// An epilogue warp's results lie one row to a thread, 64 columns at a time; they pass through a slab
-// of shared memory (32 rows of 128 bytes, 16-byte words swizzled by the row) so that global memory
-// is written, and read, in whole 128-byte lines: 8 threads to a row. Stores straight from the
+// An epilogue warp's results lie one row to a thread, 32 columns at a time; they pass through a slab
+// of shared memory (32 rows of 64 bytes, 16-byte words swizzled by the row) so that global memory
+// is written, and read, 64 bytes of a row at a time: 4 threads to a row. Stores straight from the
 // registers touch 32 rows at once, 16 bytes of each, and took longer than the main loop of a short
 // contraction.
+constexpr int kCols = 32;
+__device__ __forceinline__ int slab_at(int row, int word) { return row * 64 + ((word ^ (row / 2 % 4)) * 16); }
 
-// 32 values of this thread's row, columns 32 half ..: into the slab.
-__device__ __forceinline__ void slab_put(unsigned char *slab, int lane, int half, const uint32_t (&v)[16]) {
+// 32 values of this thread's row into the slab.
+__device__ __forceinline__ void slab_put(unsigned char *slab, int lane, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(slab + lane * 128 + (((half * 4 + i) ^ (lane & 7)) * 16)) =
-            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        *reinterpret_cast<uint4 *>(slab + slab_at(lane, i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-__device__ __forceinline__ void slab_get(const unsigned char *slab, int lane, int half, uint32_t (&v)[16]) {
+__device__ __forceinline__ void slab_get(const unsigned char *slab, int lane, uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(slab + lane * 128 + (((half * 4 + i) ^ (lane & 7)) * 16));
+        const uint4 q = *reinterpret_cast<const uint4 *>(slab + slab_at(lane, i));
         v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
 }
-// The slab's first `rows` rows to columns [n, n + COLS) of N, N % 8 == 0, of the rows from `base` on.
-template <int COLS>
+// The slab's first `rows` rows to columns [n, n + 32) of N, N % 8 == 0, of the rows from `base` on.
 __device__ __forceinline__ void slab_store(const unsigned char *slab, int lane, ep_bf16 *base, int N, int n, int rows) {
     __syncwarp();
-    const int c = lane % 8;
+    const int c = lane % 4;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int r = 4 * j + lane / 8;
-        if (r < rows && 8 * c < COLS && n + 8 * c < N)
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + lane / 4;
+        if (r < rows && n + 8 * c < N)
             st_v4(reinterpret_cast<uint4 *>(base + (size_t)r * N + n + 8 * c),
-                  *reinterpret_cast<const uint4 *>(slab + r * 128 + ((c ^ (r & 7)) * 16)));
+                  *reinterpret_cast<const uint4 *>(slab + slab_at(r, c)));
     }
     __syncwarp();
 }
-// The other way round (64 columns), as loads that are put into the slab once they are there (slab_fill).
-__device__ __forceinline__ void slab_load(uint4 (&q)[8], int lane, const ep_bf16 *base, int N, int n, int rows) {
-    const int c = lane % 8;
+// The other way round, as loads that are put into the slab once they are there (slab_fill).
+__device__ __forceinline__ void slab_load(uint4 (&q)[4], int lane, const uint16_t *base, int N, int n, int rows) {
+    const int c = lane % 4;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int r = 4 * j + lane / 8;
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + lane / 4;
         q[j] = r < rows && n + 8 * c < N ? *reinterpret_cast<const uint4 *>(base + (size_t)r * N + n + 8 * c)
                                          : make_uint4(0, 0, 0, 0);
     }
 }
-__device__ __forceinline__ void slab_fill(unsigned char *slab, int lane, const uint4 (&q)[8]) {
-    const int c = lane % 8;
+__device__ __forceinline__ void slab_fill(unsigned char *slab, int lane, const uint4 (&q)[4]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int r = 4 * j + lane / 8;
-        *reinterpret_cast<uint4 *>(slab + r * 128 + ((c ^ (r & 7)) * 16)) = q[j];
-    }
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(slab + slab_at(8 * j + lane / 4, lane % 4)) = q[j];
     __syncwarp();
 }
 
@@ -255,7 +251,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
 
     unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     unsigned char *slabs = stages + kStages * Sh::kStageBytes;
-    int64_t *prefix = reinterpret_cast<int64_t *>(slabs + 4 * kSlabBytes);
+    int64_t *prefix = reinterpret_cast<int64_t *>(slabs + kEpilogueWarps * kSlabBytes);
     int *lo = reinterpret_cast<int *>(prefix + p.E + 1), *count = lo + p.E;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -263,7 +259,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
 
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1), mbar_init(&other[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4 * CG);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], kEpilogueWarps * CG);
         mbar_init(&drained, 1);
         failed = 0;
         fence_mbar_init();
@@ -461,14 +457,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
             }
         }
     } else {
-        // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread
-        const int quarter = warp % 4;
-        unsigned char *slab = slabs + quarter * kSlabBytes;
+        // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread,
+        // and two warps take the same rows' columns in turns of 32
+        const int quarter = warp % 4, turn = (warp - 2) / 4;
+        unsigned char *slab = slabs + (warp - 2) * kSlabBytes;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         uint32_t acc_it = 0;
         while (walk.next(t)) {
             const bool none = walk.blocks(t) == 0;
             const uint32_t slot = acc_it & 1;
+            // the warp's first row within the tile; its columns of the tile
+            const bool half = half_tile<OP, CG>(t);
+            const int r0 = half ? (int)rank * (kGemmBM / 2) + quarter % 2 * 32 : (int)rank * kGemmBM + quarter * 32;
+            const int c_first = half ? quarter / 2 * (Sh::kOutN / 2) : 0;
+            const int N = p.N[t.problem];
+            const int c_end = min(half ? c_first + Sh::kOutN / 2 : Sh::kOutN, N - t.n0);
+            const int rows = min(t.valid - r0, 32);  // of this warp's 32 that count
+            // where the tile's column 0 would be for this warp
+            const uint32_t src = tmem + lanes + slot * NB - (half ? quarter / 2 * (NB / 2) : 0);
+            const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r0 : (size_t)t.m0 + r0;
+            int c = c_first + turn * kCols;
+            // DGateUp: g and u are asked for a turn ahead, the first before the accumulator is there
+            uint4 gq[4], uq[4];
+            const auto ask = [&](int c) {
+                if (OP != ExpertOp::kDGateUp || rows <= 0 || c >= c_end) return;
+                slab_load(gq, lane, p.g + row * N, N, t.n0 + c, rows);
+                slab_load(uq, lane, p.u + row * N, N, t.n0 + c, rows);
+            };
+            ask(c);
             if (!none) {
                 bool ok = true;
                 if (lane == 0) ok = mbar_wait_limited(&acc_full[slot], (acc_it / 2) & 1, &failed);
@@ -476,93 +492,74 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 ++acc_it;
                 tmem_fence_after();
             }
-            // the warp's first row within the tile; its columns of the accumulator
-            const bool half = half_tile<OP, CG>(t);
-            const int r0 = half ? (int)rank * (kGemmBM / 2) + quarter % 2 * 32 : (int)rank * kGemmBM + quarter * 32;
-            const int c_begin = half ? quarter / 2 * (Sh::kOutN / 2) : 0, c_end = half ? c_begin + Sh::kOutN / 2 : Sh::kOutN;
-            const int rows = min(t.valid - r0, 32);  // of this warp's 32 that count
-            // where the tile's column 0 would be for this warp
-            const uint32_t src = tmem + lanes + slot * NB - (half ? quarter / 2 * (NB / 2) : 0);
-            const int N = p.N[t.problem];
-            const size_t row = Sh::kDW ? (size_t)t.e * p.M[t.problem] + t.m0 + r0 : (size_t)t.m0 + r0;
-            for (int c = c_begin; rows > 0 && c < c_end && t.n0 + c < N; c += Sh::kCols) {
+            for (; rows > 0 && c < c_end; c += 2 * kCols) {
                 const int n = t.n0 + c;
+                uint32_t v[32], o[16];
                 if constexpr (OP == ExpertOp::kDGateUp) {
-                    uint4 gq[8], uq[8];
-                    slab_load(gq, lane, p.g + row * N, N, n, rows);
-                    slab_load(uq, lane, p.u + row * N, N, n, rows);
-                    uint32_t g[2][16], u[2][16];
+                    uint32_t g[16], u[16];
                     slab_fill(slab, lane, gq);
-                    slab_get(slab, lane, 0, g[0]);
-                    slab_get(slab, lane, 1, g[1]);
+                    slab_get(slab, lane, g);
                     __syncwarp();
                     slab_fill(slab, lane, uq);
-                    slab_get(slab, lane, 0, u[0]);
-                    slab_get(slab, lane, 1, u[1]);
+                    slab_get(slab, lane, u);
                     __syncwarp();
+                    ask(c + 2 * kCols);
+                    tmem_load_32(src + c, v);
+                    tmem_wait_ld(v);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        uint32_t v[32], o[16];
-                        tmem_load_32(src + c + 32 * part, v);
-                        tmem_wait_ld(v);
+                    for (int i = 0; i < 16; ++i) {
+                        float dg[2], du[2];
+                        const float2 g2 = half_values(g[i]), u2 = half_values(u[i]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float dg[2], du[2];
-                            const float2 g2 = half_values(g[part][i]), u2 = half_values(u[part][i]);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float dh = __uint_as_float(v[2 * i + k]);
-                                const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
-                                const float s = sigmoid(gg);
-                                du[k] = dh * gg * s;
-                                dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
-                            }
-                            o[i] = bf16_pair(dg[0], dg[1]);
-                            u[part][i] = bf16_pair(du[0], du[1]);
+                        for (int k = 0; k < 2; ++k) {
+                            const float dh = __uint_as_float(v[2 * i + k]);
+                            const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
+                            const float s = sigmoid(gg);
+                            du[k] = dh * gg * s;
+                            dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
                         }
-                        slab_put(slab, lane, part, o);
+                        o[i] = bf16_pair(dg[0], dg[1]);
+                        u[i] = bf16_pair(du[0], du[1]);
                     }
-                    slab_store<Sh::kCols>(slab, lane, p.out[0] + row * N, N, n, rows);
-                    slab_put(slab, lane, 0, u[0]);
-                    slab_put(slab, lane, 1, u[1]);
-                    slab_store<Sh::kCols>(slab, lane, p.out[1] + row * N, N, n, rows);
+                    slab_put(slab, lane, o);
+                    slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
+                    slab_put(slab, lane, u);
+                    slab_store(slab, lane, p.out[1] + row * N, N, n, rows);
                 } else if constexpr (OP == ExpertOp::kGateUp) {
-                    // what: 0 h, 1 g, 2 u; each takes its columns from TMEM anew
-                    for (int what = 0; what < (p.g ? 3 : 1); ++what) {
+                    uint32_t w[32];
+                    const uint32_t at = src + c / Sh::kGate * (2 * Sh::kGate) + c % Sh::kGate;
+                    tmem_load_32(at, v);
+                    tmem_load_32(at + Sh::kGate, w);
+                    tmem_wait_ld(v);
+                    tmem_wait_ld(w);
 #pragma unroll
-                        for (int part = 0; part < Sh::kCols / 32; ++part) {
-                            uint32_t v[32], w[32], o[16];
-                            tmem_load_32(src + 2 * c + 32 * part, v);
-                            tmem_load_32(src + 2 * c + Sh::kGate + 32 * part, w);
-                            tmem_wait_ld(v);
-                            tmem_wait_ld(w);
+                    for (int i = 0; i < 16; ++i) {
+                        const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
+                        o[i] = bf16_pair(g0 * sigmoid(g0) * __uint_as_float(w[2 * i]),
+                                         g1 * sigmoid(g1) * __uint_as_float(w[2 * i + 1]));
+                    }
+                    slab_put(slab, lane, o);
+                    slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
+                    if (p.g) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float g0 = __uint_as_float(v[2 * i]), g1 = __uint_as_float(v[2 * i + 1]);
-                                const float u0 = __uint_as_float(w[2 * i]), u1 = __uint_as_float(w[2 * i + 1]);
-                                o[i] = what == 0   ? bf16_pair(g0 * sigmoid(g0) * u0, g1 * sigmoid(g1) * u1)
-                                       : what == 1 ? half_pair(g0, g1)
-                                                   : half_pair(u0, u1);
-                            }
-                            slab_put(slab, lane, part, o);
-                        }
-                        ep_bf16 *out = what == 0 ? p.out[0] : what == 1 ? p.g : p.u;
-                        slab_store<Sh::kCols>(slab, lane, out + row * N, N, n, rows);
+                        for (int i = 0; i < 16; ++i) o[i] = half_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        slab_put(slab, lane, o);
+                        slab_store(slab, lane, p.g + row * N, N, n, rows);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = half_pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+                        slab_put(slab, lane, o);
+                        slab_store(slab, lane, p.u + row * N, N, n, rows);
                     }
                 } else {
-#pragma unroll
-                    for (int part = 0; part < Sh::kCols / 32; ++part) {
-                        uint32_t v[32], o[16];
-                        if (!none) {
-                            tmem_load_32(src + c + 32 * part, v);
-                            tmem_wait_ld(v);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        slab_put(slab, lane, part, o);
+                    if (!none) {
+                        tmem_load_32(src + c, v);
+                        tmem_wait_ld(v);
                     }
-                    slab_store<Sh::kCols>(slab, lane, p.out[t.problem] + row * N, N, n, rows);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = none ? 0u : bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    slab_put(slab, lane, o);
+                    slab_store(slab, lane, p.out[t.problem] + row * N, N, n, rows);
                 }
             }
             if (!none) {
