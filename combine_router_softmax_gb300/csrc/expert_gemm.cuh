@@ -35,8 +35,9 @@ namespace ep {
 
 enum class ExpertOp { kGateUp, kDown, kDGateUp, kDRows, kDWeight };
 
-constexpr int kGemmThreads = 320;
 constexpr int kEpilogueWarps = 8;
+constexpr int kProducers = 2;
+constexpr int kGemmThreads = 32 * (1 + kEpilogueWarps + kProducers);
 constexpr int kGemmBK = 64;   // contraction per stage: 128 bytes of bf16, one swizzled row
 constexpr int kGemmBM = 128;  // rows of a CTA's tile: the TMEM lanes
 constexpr int kSlabBytes = 32 * 64;
@@ -68,6 +69,7 @@ struct GemmShape {
     static constexpr int kBBytes = kBRows * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = 196608 / kStageBytes;
+    static_assert(kStages % kProducers == 0 && kStages < 32, "a stage has one producer, and a bit");
     static constexpr int kTmemCols = 2 * NB;
     static constexpr size_t smem_bytes(int E) { return 1024 + (size_t)kStages * kStageBytes + kEpilogueWarps * kSlabBytes + (size_t)(E + 1) * 8 + (size_t)E * 8; }
 };
@@ -319,11 +321,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
     Walk<OP, CG, NB> walk(p, lo, count, prefix);
     Tile t;
 
-    if (warp == 0) {
-        // ---- producer: one lane fetches the stages of every tile in turn
+    if (warp == 0 || warp > 1 + kEpilogueWarps) {
+        // ---- producers: one lane each, which take the stages in turn
         if (elect_one()) {
-            uint32_t it = 0, relayed = 0, ever = 0;
-            uint32_t s = 0, phase = 0;  // it % kStages, it / kStages % 2: kept by counting, a stage is few instructions
+            const uint32_t mine = warp == 0 ? 0 : warp - 1 - kEpilogueWarps;
+            uint32_t it = mine, relayed = 0, ever = 0;
+            uint32_t s = mine, phase = 0;  // it % kStages, it / kStages % 2: kept by counting, a stage is few instructions
+            int b = mine;                  // of the tile
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
@@ -334,13 +338,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     bytes += Sh::kABytes * CG;
                 else
                     for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * most, most) * 128;
-                for (int b = 0; b < kb; ++b, ++it) {
+                for (; b < kb; b += kProducers, it += kProducers) {
                     if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], phase ^ 1, &failed)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t next = s + 1 == kStages ? 0 : s + 1, next_phase = next == 0 ? phase ^ 1 : phase;
-                    ready = it + 1 >= kStages && mbar_test(&empty[next], next_phase ^ 1);
+                    const bool wraps = s + kProducers >= kStages;
+                    const uint32_t next = s + kProducers - (wraps ? kStages : 0), next_phase = wraps ? phase ^ 1 : phase;
+                    ready = it + kProducers >= kStages && mbar_test(&empty[next], next_phase ^ 1);
                     const bool relay = kRelay && t.rows - b * kGemmBK < kGemmBK;
                     if (rank == 0 || relay) mbar_arrive_expect_tx(&full[s], relay ? bytes / 2 : bytes);
                     if (relay) relayed ^= 1u << s, ever |= 1u << s;
@@ -382,10 +387,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     s = next;
                     phase = next_phase;
                 }
+                b -= kb;
             }
             // no copy may be under way when the CTA ends: after a failure nobody else waits for them
             if (failed) {
-                for (int i = 0; i < kStages; ++i) {
+                for (int i = mine; i < kStages; i += kProducers) {
                     int never = 0;
                     if (rank == 0 && it > (uint32_t)i) {
                         const uint32_t last = (it - 1 - i) / kStages;  // how often stage i was filled again
