@@ -15,16 +15,20 @@
 // gradients are 0.0024 off in norm with it, 0.0031 with bf16); beyond 65504 it has infinity.
 //
 // One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
-// holding half of either operand): warp 0 feeds a ring of shared-memory stages by TMA, warp
-// 1 issues the MMAs into one of two accumulators, warps 2 to 9 turn the other one into
+// holding half of either operand): two producer warps feed a ring of shared-memory stages by TMA, in
+// turn, warp 1 issues the MMAs into one of two accumulators, warps 2 to 9 turn the other one into
 // results. Every wait has a time limit (kErrExpertWait).
 //
-// What bounds it. With many rows the tensor pipe: 8 experts x 1024 rows, 4096 to 2048 and
-// back, forward 246 us = 1676 TFLOP/s, DGateUp 1277, DRows 1741, DWeight 1614 (64 KB written for
-// every 16 stages); 16 experts of uneven size lose what their last tiles do not fill. As single CTAs the same forward took 270 us or more: 128 x 256 tiles
+// What bounds it. With many rows the tensor pipe: 16 experts x 1024 rows, 4096 to 2048 and back,
+// forward 466 us = 1771 TFLOP/s, DGateUp 1572, DRows 1844, DWeight 1728 (64 KB written for
+// every 16 stages) of a library product's 2040 in the same burst; experts of uneven size lose what their
+// last tiles do not fill. As single CTAs the forward is 10% slower: 128 x 256 tiles
 // move 48 KB into shared memory and read 48 KB out for 512 cycles of MMA, 192 bytes a cycle
 // where there are 128; a pair's 256 x 256 halves what each SM moves. With few rows an expert the
-// weights' stream: 512 rows over 64 experts of 7168 / 2048 in 826 us = 6.8 TB/s.
+// weights' stream: 512 rows over 64 experts of 7168 / 2048 in 809 us = 7.0 TB/s. Between the two, what
+// a stage costs the threads that serve it: one producer took 520 cycles a stage whatever its copies, as
+// many as the MMAs of a pair's stage (two: 16384 rows, 4096 to 2048, all gradients 1670 -> 1607 us), the
+// issuer takes 330 (470 without its loop unrolled).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -338,6 +342,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     bytes += Sh::kABytes * CG;
                 else
                     for (int r = 0; r < CG; ++r) bytes += a_rows_fetched(t.valid - r * most, most) * 128;
+#pragma unroll 2
                 for (; b < kb; b += kProducers, it += kProducers) {
                     if (it >= kStages && !ready && !mbar_poll_limited(&empty[s], phase ^ 1, &failed)) {
                         ok = false;
@@ -430,6 +435,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     if (acc_it >= 2) ok = mbar_poll_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed);
                     tmem_fence_after();
                     uint32_t at = s, parity = phase;
+#pragma unroll 4
                     for (int b = 0; ok && b < whole; ++b) {
                         ok = ready || mbar_poll_limited(&full[at], parity, &failed);
                         const uint32_t next = at + 1 == kStages ? 0 : at + 1;
