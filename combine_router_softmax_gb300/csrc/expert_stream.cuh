@@ -40,7 +40,9 @@ constexpr int kStreamBox = kStreamRows * 128;          // bytes of 128 bytes of 
 constexpr int kStreamStageBytes = 2 * kStreamBox;
 constexpr int kStreamStages = 4;
 constexpr int kStreamTokens = 16;                      // rows of x that one pass over the weights serves
-constexpr int kStreamRed = 2 * kStreamTokens * kStreamRows;  // floats of a pass's sums
+constexpr int kStreamParts = 4;                        // of a stage's k, one to a warp
+constexpr int kStreamRedRow = kStreamRows + 4;         // floats of a token's sums: the four tokens of a store meet different banks
+constexpr int kStreamRed = kStreamParts * kStreamTokens * kStreamRedRow;  // of a pass's
 
 struct StreamParams {
     CUtensorMap w[2];         // [E][N][bytes of a row], boxes of 128 bytes x 32 or 64 rows, swizzled
@@ -74,25 +76,24 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// G = 0: bf16 weights, 128 k a stage; else 4-bit weights, 512 k a stage. The stage's first 128 bytes
-// of the rows are one half's, the second 128 the other's.
+// G = 0: bf16 weights, 128 k a stage; else 4-bit weights, 512 k a stage. A part is 64 bytes of every
+// weight row of the stage.
 template <int G>
 struct StreamShape {
     static constexpr int kStageK = G == 0 ? 128 : 512;
-    static constexpr int kWarpK = kStageK / 2;                  // k of a stage that one warp takes
-    static constexpr int kPartK = kWarpK / 2;                   // taken at a time: 64 bytes of a weight row
-    static constexpr int kVecs = kPartK / 32;                   // 16-byte words of x for it
+    static constexpr int kPartK = kStageK / kStreamParts;
+    static constexpr int kVecs = kPartK / 32;  // 16-byte words of a row of x for it
 };
 
-// The scales of 128 k of a row, from k `off` on: one bf16 (G = 128), two or four of them.
+// The scales of 128 k of a row: one bf16 (G = 128), two or four of them.
 template <int G>
-__device__ __forceinline__ uint2 load_scales(const ep_bf16 *row, int off) {
+__device__ __forceinline__ uint2 load_scales(const ep_bf16 *row) {
     if constexpr (G == 128)
-        return make_uint2(row[off / 128], 0);
+        return make_uint2(*row, 0);
     else if constexpr (G == 64)
-        return make_uint2(*reinterpret_cast<const uint32_t *>(row + off / 64), 0);
+        return make_uint2(*reinterpret_cast<const uint32_t *>(row), 0);
     else if constexpr (G == 32)
-        return *reinterpret_cast<const uint2 *>(row + off / 32);
+        return *reinterpret_cast<const uint2 *>(row);
     else
         return make_uint2(0, 0);
 }
@@ -123,156 +124,139 @@ struct StreamWarp {
     volatile int *failed;
     uint32_t it;
     bool ready;  // stage `it` has been seen to be there
-    int lane, m, half;
+    int lane, pair, part;  // 32 weight rows, a quarter of a stage's k
 };
 
-// One pass over an item's stages for up to NT * 8 rows of x (`tokens` of them exist); red[half]
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory");
+}
+
+// One pass over an item's stages for up to NT * 8 rows of x (`tokens` of them exist); red[part]
 // [token][row] gets the warp's sums.
 template <bool GATED, int G, int NT>
 __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w, int e, int n0, int64_t x0, int tokens,
                                             float *red) {
     using Sh = StreamShape<G>;
     const int g = w.lane / 4, t = w.lane % 4;
-    // weight rows of the fragment's rows g and g + 8: with g's order changed so that the eight lanes of
-    // one shared-memory phase, two rows, meet different banks of the swizzled stage
-    const int r0 = w.m * 16 + (g >> 1) + 4 * (g & 1);
-    const uint4 *at = reinterpret_cast<const uint4 *>(w.stages + w.half * kStreamBox + r0 * 128);
-    // scales of the two rows, activations of this lane's row: at the warp's part of the present stage
-    const ep_bf16 *sc[2] = {nullptr, nullptr};
+    // weight rows of the first fragment's rows g and g + 8 (the second's are 16 more): with g's order
+    // changed so that the eight lanes of one shared-memory phase, two rows, meet different banks of the
+    // swizzled stage
+    const int r0 = w.pair * 32 + (g >> 1) + 4 * (g & 1);
+    const uint4 *at = reinterpret_cast<const uint4 *>(w.stages + w.part / 2 * kStreamBox + r0 * 128) +
+                      ((w.part % 2 * 4 + t) ^ (r0 & 7));
+    // scales of the four rows, activations of this lane's row: at the warp's part of the present stage
+    const ep_bf16 *sc[4] = {};
     if constexpr (G > 0) {
         const size_t row_groups = (size_t)((p.K + 127) / 128) * (128 / G);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
             const int n = n0 + (GATED ? r0 % (kStreamRows / 2) : r0) + 8 * h;  // past the last: that one, not stored
-            sc[h] = p.scale[GATED && w.m >= kStreamRows / 32] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.half * (Sh::kWarpK / G);
+            sc[h] = p.scale[GATED && w.pair] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.part * (Sh::kPartK / G);
         }
     }
     const ep_bf16 *x[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)  // past the last row: the first again; its sums are not stored
-        x[i] = p.x + (size_t)(x0 + (i * 8 + g < tokens ? i * 8 + g : 0)) * p.K + w.half * Sh::kWarpK + 8 * t;
+        x[i] = p.x + (size_t)(x0 + (i * 8 + g < tokens ? i * 8 + g : 0)) * p.K + w.part * Sh::kPartK + 8 * t;
     const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
 
-    // the activations and scales (G = 128: one a row; 64: two, 32: four, in 4 or 8 bytes) of one part;
-    // CHECK: of a stage that goes past K
-    struct Ahead {
-        uint4 x[NT][Sh::kVecs];
-        uint2 scale[2];
-    };
-    const auto fetch = [&](auto check, int b, int part, Ahead &a) {
-        const int off = part * Sh::kPartK;
-        const int left = p.K - b * Sh::kStageK - w.half * Sh::kWarpK - off;  // k from the part's first on
+    float acc[2][NT][4] = {};
+    // A stage, without a branch from the wait on. CHECK: it goes past K.
+    const auto stage = [&](auto check, int b) {
+        const uint32_t s = w.it % kStreamStages;
+        uint4 v[NT][Sh::kVecs];
+        uint2 scale[4];
+        const int left = p.K - b * Sh::kStageK - w.part * Sh::kPartK;  // k from the part's first on
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < Sh::kVecs; ++j)
-                a.x[i][j] = !check || 32 * j + 8 * t < left ? *reinterpret_cast<const uint4 *>(x[i] + off + 32 * j)
-                                                            : make_uint4(0, 0, 0, 0);
+                v[i][j] = !check || 32 * j + 8 * t < left ? *reinterpret_cast<const uint4 *>(x[i] + 32 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a.scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc[h], off);
-    };
-    const auto scale_of = [](const uint2 &v, int i) {
-        return __uint_as_float(((i / 2 ? v.y : v.x) >> (16 * (i % 2))) << 16);
-    };
-
-    float acc[NT][4] = {};
-    // PARTS parts at once, their chains of dependent products side by side
-    const auto multiply = [&](auto parts, const Ahead *a, const uint4 (*q)[2]) {
-        constexpr int P = decltype(parts)::value;
+        for (int h = 0; h < 4; ++h) scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc[h]);
+        if (!w.ready) {
+            if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
+            __syncwarp();  // the barrier's completion was seen by one lane; the others' reads are ordered behind it
+        }
+        const uint4 *from = at + s * (kStreamStageBytes / 16);
+        const uint4 q[2][2] = {{from[0], from[64]}, {from[128], from[192]}};
+        __syncwarp();
+        if (w.lane == 0) mbar_arrive(&w.empty[s]);
+        ++w.it;
+        // every lane asks whether the next stage is there: the answer's latency is behind the products
+        const bool there = mbar_test(&w.full[w.it % kStreamStages], (w.it / kStreamStages) & 1);
         if constexpr (G == 0) {
 #pragma unroll
-            for (int h = 0; h < P; ++h)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    mma_16816(acc[i], q[h][0].x, q[h][1].x, q[h][0].y, q[h][1].y, a[h].x[i][0].x, a[h].x[i][0].y);
-                    mma_16816(acc[i], q[h][0].z, q[h][1].z, q[h][0].w, q[h][1].w, a[h].x[i][0].z, a[h].x[i][0].w);
+                    mma_16816(acc[m][i], q[m][0].x, q[m][1].x, q[m][0].y, q[m][1].y, v[i][0].x, v[i][0].y);
+                    mma_16816(acc[m][i], q[m][0].z, q[m][1].z, q[m][0].w, q[m][1].w, v[i][0].z, v[i][0].w);
                 }
         } else {
             constexpr bool kOff = NT > 1;  // 136 is taken off the values, not off the sums
-            float sum[P][NT][4] = {}, xs[P][4] = {};
+            float sum[2][NT][4] = {}, xs[4] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (!kOff) {
+                    mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].x, v[0][j].y);
+                    mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].z, v[0][j].w);
+                }
 #pragma unroll
-                for (int h = 0; h < P; ++h) {
-                    const Ahead &b = a[h];
-                    const uint32_t w0 = word_of(q[h][0], j), w1 = word_of(q[h][1], j);
-                    if constexpr (!kOff) {
-                        mma_16816(xs[h], kOnes, kOnes, kOnes, kOnes, b.x[0][j].x, b.x[0][j].y);
-                        mma_16816(xs[h], kOnes, kOnes, kOnes, kOnes, b.x[0][j].z, b.x[0][j].w);
-                    }
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t w0 = word_of(q[m][0], j), w1 = word_of(q[m][1], j);
 #pragma unroll
                     for (int step = 0; step < 2; ++step) {
                         const uint32_t a0 = w4_pair<kOff>(w0, 2 * step), a1 = w4_pair<kOff>(w1, 2 * step);
                         const uint32_t a2 = w4_pair<kOff>(w0, 2 * step + 1), a3 = w4_pair<kOff>(w1, 2 * step + 1);
 #pragma unroll
                         for (int i = 0; i < NT; ++i)
-                            mma_16816(sum[h][i], a0, a1, a2, a3, step ? b.x[i][j].z : b.x[i][j].x,
-                                      step ? b.x[i][j].w : b.x[i][j].y);
-                    }
-                    if ((32 * (j + 1)) % G == 0) {
-                        const float f[2] = {scale_of(b.scale[0], 32 * j / G), scale_of(b.scale[1], 32 * j / G)};
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float v = kOff ? sum[h][i][r] : fmaf(-136.0f, xs[h][r % 2], sum[h][i][r]);
-                                acc[i][r] = fmaf(f[r / 2], v, acc[i][r]);
-                                sum[h][i][r] = 0.0f;
-                            }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) xs[h][r] = 0.0f;
+                            mma_16816(sum[m][i], a0, a1, a2, a3, step ? v[i][j].z : v[i][j].x, step ? v[i][j].w : v[i][j].y);
                     }
                 }
-        }
-    };
-    const int u0 = t ^ (r0 & 7), u1 = (4 + t) ^ (r0 & 7);  // the two parts' words of the row
-    // A stage, without a branch from the wait on: loads and products of both parts can move past each other.
-    const auto stage = [&](auto check, int b) {
-        const uint32_t s = w.it % kStreamStages;
-        Ahead a[2];
-        fetch(check, b, 0, a[0]);
-        if constexpr (NT == 1) fetch(check, b, 1, a[1]);  // the registers allow it
-        if (!w.ready) {
-            if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
-            __syncwarp();  // the barrier's completion was seen by one lane; the others' reads are ordered behind it
-        }
-        const uint4 *from = at + s * (kStreamStageBytes / 16);
-        const uint4 q[2][2] = {{from[u0], from[u0 + 64]}, {from[u1], from[u1 + 64]}};
-        __syncwarp();
-        if (w.lane == 0) mbar_arrive(&w.empty[s]);
-        ++w.it;
-        // every lane asks whether the next stage is there: the answer's latency is behind the products
-        const bool there = mbar_test(&w.full[w.it % kStreamStages], (w.it / kStreamStages) & 1);
-        if constexpr (NT == 1) {
-            multiply(std::integral_constant<int, 2>{}, a, q);
-        } else {
-            multiply(std::integral_constant<int, 1>{}, a, q);
-            asm volatile("" ::: "memory");  // not earlier: the registers are the first part's
-            fetch(check, b, 1, a[0]);
-            multiply(std::integral_constant<int, 1>{}, a, q + 1);
+                if ((32 * (j + 1)) % G == 0) {
+                    const int part = 32 * j / G;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint2 of = scale[2 * m + r / 2];
+                            const float f = __uint_as_float(((part / 2 ? of.y : of.x) >> (16 * (part % 2))) << 16);
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                const float d = kOff ? sum[m][i][r] : fmaf(-136.0f, xs[r % 2], sum[m][i][r]);
+                                acc[m][i][r] = fmaf(f, d, acc[m][i][r]);
+                                sum[m][i][r] = 0.0f;
+                            }
+                        }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) xs[r] = 0.0f;
+                }
+            }
         }
         w.ready = __all_sync(0xFFFFFFFFu, there);
 #pragma unroll
         for (int i = 0; i < NT; ++i) x[i] += Sh::kStageK;
-        if constexpr (G > 0) sc[0] += Sh::kStageK / G, sc[1] += Sh::kStageK / G;
+        if constexpr (G > 0)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) sc[h] += Sh::kStageK / G;
     };
     const int whole = p.K / Sh::kStageK;
 #pragma unroll 1
     for (int b = 0; b < whole; ++b) stage(std::false_type{}, b);
     if (whole < kb) stage(std::true_type{}, whole);
-    float *mine = red + (size_t)w.half * kStreamTokens * kStreamRows;
+    float *mine = red + (size_t)w.part * kStreamTokens * kStreamRedRow;
+    consumers_sync();  // the sums before these have been read
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mine[(i * 8 + 2 * t + r % 2) * kStreamRows + r0 + r / 2 * 8] = acc[i][r];
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mine[(i * 8 + 2 * t + r % 2) * kStreamRedRow + m * 16 + r0 + r / 2 * 8] = acc[m][i][r];
 }
 
 // The line of `p` into L1.
 __device__ __forceinline__ void ask_for_line(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
-
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kStreamWarps * 32) : "memory");
-}
 
 template <bool GATED, int G>
 __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_kernel(const __grid_constant__ StreamParams p) {
@@ -282,9 +266,9 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
     __shared__ int hits;
     __shared__ volatile int failed;
     unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    // two buffers [half][token][row]: one takes a pass's sums while the other is still read
+    // [part][token][row]
     float *red = reinterpret_cast<float *>(stages + kStreamStages * kStreamStageBytes);
-    StreamExpert *hit = reinterpret_cast<StreamExpert *>(red + 2 * kStreamRed);
+    StreamExpert *hit = reinterpret_cast<StreamExpert *>(red + kStreamRed);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStreamStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kStreamWarps);
@@ -369,8 +353,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
         __syncwarp();
     } else {
         // ---- consumers. After a failure they go on without waiting: every warp reaches the barriers.
-        float *const red_begin = red;
-        StreamWarp w{stages, full, empty, &failed, 0, false, lane, warp / 2, warp % 2};
+        StreamWarp w{stages, full, empty, &failed, 0, false, lane, warp / kStreamParts, warp % kStreamParts};
         for (; items.any(); items.next()) {
             const auto [e, first, rows] = hit[items.index];
             const int n0 = items.block * kOut;
@@ -382,17 +365,19 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
                 else
                     stream_pass<GATED, G, 2>(p, w, e, n0, x0, tokens, red);
                 consumers_sync();
-                const float *sums = red;
                 for (int i = threadIdx.x; i < tokens * kOut; i += kStreamWarps * 32) {
                     const int token = i / kOut, n = i % kOut;
-                    const float *r = sums + token * kStreamRows + n;
-                    constexpr int kHalf = kStreamTokens * kStreamRows;
-                    float v = r[0] + r[kHalf];
-                    if constexpr (GATED) v = __fdividef(v, 1.0f + __expf(-v)) * (r[kOut] + r[kHalf + kOut]);
+                    const auto sum = [&](int n) {
+                        float v = 0.0f;
+#pragma unroll
+                        for (int part = 0; part < kStreamParts; ++part) v += red[(part * kStreamTokens + token) * kStreamRedRow + n];
+                        return v;
+                    };
+                    float v = sum(n);
+                    if constexpr (GATED) v = __fdividef(v, 1.0f + __expf(-v)) * sum(kOut + n);
                     if (n0 + n < p.N)
                         reinterpret_cast<__nv_bfloat16 *>(p.y)[(size_t)(x0 + token) * p.N + n0 + n] = __float2bfloat16_rn(v);
                 }
-                red = red == red_begin ? red_begin + kStreamRed : red_begin;
             }
         }
     }
@@ -411,7 +396,7 @@ cudaError_t launch_stream(StreamParams &p, const void *w0, const void *w1, cudaS
     constexpr int kBytes = G == 0 ? 2 : 1;
     if (!make_map(&p.w[0], w0, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
     if (GATED && !make_map(&p.w[1], w1, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + 2 * kStreamRed * sizeof(float) +
+    const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + kStreamRed * sizeof(float) +
                         (size_t)p.E * sizeof(StreamExpert);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
