@@ -145,14 +145,14 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
     const uint4 *at = reinterpret_cast<const uint4 *>(w.stages + w.part / 2 * kStreamBox + r0 * 128) +
                       ((w.part % 2 * 4 + t) ^ (r0 & 7));
     // scales of the four rows, activations of this lane's row: at the warp's part of the present stage
-    const ep_bf16 *sc[4] = {};
+    const ep_bf16 *sc = nullptr;
+    int sc_row[4] = {};
     if constexpr (G > 0) {
         const size_t row_groups = (size_t)((p.K + 127) / 128) * (128 / G);
+        const int n = min(n0 + (GATED ? r0 % (kStreamRows / 2) : r0), p.N - 1);  // past the last: that one, not stored
+        sc = p.scale[GATED && w.pair] + ((size_t)e * p.N + n) * row_groups + w.part * (Sh::kPartK / G);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int n = n0 + (GATED ? r0 % (kStreamRows / 2) : r0) + 8 * h;  // past the last: that one, not stored
-            sc[h] = p.scale[GATED && w.pair] + ((size_t)e * p.N + min(n, p.N - 1)) * row_groups + w.part * (Sh::kPartK / G);
-        }
+        for (int h = 1; h < 4; ++h) sc_row[h] = min(8 * h, p.N - 1 - n) * (int)row_groups;
     }
     const ep_bf16 *x[NT];
 #pragma unroll
@@ -173,7 +173,7 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
             for (int j = 0; j < Sh::kVecs; ++j)
                 v[i][j] = !check || 32 * j + 8 * t < left ? *reinterpret_cast<const uint4 *>(x[i] + 32 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc[h]);
+        for (int h = 0; h < 4; ++h) scale[h] = check && left <= 0 ? make_uint2(0, 0) : load_scales<G>(sc + sc_row[h]);
         if (!w.ready) {
             if (w.lane == 0 && !*w.failed) mbar_poll_limited(&w.full[s], (w.it / kStreamStages) & 1, w.failed);
             __syncwarp();  // the barrier's completion was seen by one lane; the others' reads are ordered behind it
@@ -194,52 +194,54 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
                     mma_16816(acc[m][i], q[m][0].z, q[m][1].z, q[m][0].w, q[m][1].w, v[i][0].z, v[i][0].w);
                 }
         } else {
-            constexpr bool kOff = NT > 1;  // 136 is taken off the values, not off the sums
-            float sum[2][NT][4] = {}, xs[4] = {};
+            constexpr bool kOff = NT > 1;       // 136 is taken off the values, not off the sums
+            constexpr int M = NT > 1 ? 1 : 2;   // fragments at a time: two chains of dependent products either way
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (!kOff) {
-                    mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].x, v[0][j].y);
-                    mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].z, v[0][j].w);
-                }
+            for (int m0 = 0; m0 < 2; m0 += M) {
+                float sum[M][NT][4] = {}, xs[4] = {};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t w0 = word_of(q[m][0], j), w1 = word_of(q[m][1], j);
-#pragma unroll
-                    for (int step = 0; step < 2; ++step) {
-                        const uint32_t a0 = w4_pair<kOff>(w0, 2 * step), a1 = w4_pair<kOff>(w1, 2 * step);
-                        const uint32_t a2 = w4_pair<kOff>(w0, 2 * step + 1), a3 = w4_pair<kOff>(w1, 2 * step + 1);
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            mma_16816(sum[m][i], a0, a1, a2, a3, step ? v[i][j].z : v[i][j].x, step ? v[i][j].w : v[i][j].y);
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (!kOff) {
+                        mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].x, v[0][j].y);
+                        mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].z, v[0][j].w);
                     }
-                }
-                if ((32 * (j + 1)) % G == 0) {
-                    const int part = 32 * j / G;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < M; ++m) {
+                        const uint32_t w0 = word_of(q[m0 + m][0], j), w1 = word_of(q[m0 + m][1], j);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const uint2 of = scale[2 * m + r / 2];
-                            const float f = __uint_as_float(((part / 2 ? of.y : of.x) >> (16 * (part % 2))) << 16);
+                        for (int step = 0; step < 2; ++step) {
+                            const uint32_t a0 = w4_pair<kOff>(w0, 2 * step), a1 = w4_pair<kOff>(w1, 2 * step);
+                            const uint32_t a2 = w4_pair<kOff>(w0, 2 * step + 1), a3 = w4_pair<kOff>(w1, 2 * step + 1);
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                const float d = kOff ? sum[m][i][r] : fmaf(-136.0f, xs[r % 2], sum[m][i][r]);
-                                acc[m][i][r] = fmaf(f, d, acc[m][i][r]);
-                                sum[m][i][r] = 0.0f;
-                            }
+                            for (int i = 0; i < NT; ++i)
+                                mma_16816(sum[m][i], a0, a1, a2, a3, step ? v[i][j].z : v[i][j].x, step ? v[i][j].w : v[i][j].y);
                         }
+                    }
+                    if ((32 * (j + 1)) % G == 0) {
+                        const int part = 32 * j / G;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) xs[r] = 0.0f;
+                        for (int m = 0; m < M; ++m)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint2 of = scale[2 * (m0 + m) + r / 2];
+                                const float f = __uint_as_float(((part / 2 ? of.y : of.x) >> (16 * (part % 2))) << 16);
+#pragma unroll
+                                for (int i = 0; i < NT; ++i) {
+                                    const float d = kOff ? sum[m][i][r] : fmaf(-136.0f, xs[r % 2], sum[m][i][r]);
+                                    acc[m0 + m][i][r] = fmaf(f, d, acc[m0 + m][i][r]);
+                                    sum[m][i][r] = 0.0f;
+                                }
+                            }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) xs[r] = 0.0f;
+                    }
                 }
             }
         }
         w.ready = __all_sync(0xFFFFFFFFu, there);
 #pragma unroll
         for (int i = 0; i < NT; ++i) x[i] += Sh::kStageK;
-        if constexpr (G > 0)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) sc[h] += Sh::kStageK / G;
+        if constexpr (G > 0) sc += Sh::kStageK / G;
     };
     const int whole = p.K / Sh::kStageK;
 #pragma unroll 1
