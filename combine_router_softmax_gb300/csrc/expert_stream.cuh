@@ -4,10 +4,17 @@
 // silu(g) u from two such products. For single tokens the weights are the traffic (N K values of
 // every expert that has rows, against 2 rows N K operations), so what counts is to keep enough of
 // them on their way: a producer warp fetches stages of 64 weight rows x 256 bytes by TMA into a ring of
-// four, on across work items. Eight warps consume a stage: warp (m, half) takes 16 weight rows and half
-// of the stage's k. Two CTAs share an SM (128 KB of stages, 19 MB on the GPU; HBM needs about 10 MB under
+// four, on across work items. Eight warps consume a stage: each takes 32 weight rows and a quarter of
+// the stage's k. Two CTAs share an SM (128 KB of stages, 19 MB on the GPU; HBM needs about 10 MB under
 // way; a fifth stage took L1 from the activations and cost 5%): all warps of one wait for the same stage,
 // and what each then does before its products is latency, which the other CTA's products fill.
+//
+// bf16 weights run at HBM's rate (8 rows over 32 experts of 4096 / 1024 in 33 us, 5.4 TB/s with both
+// launches). 4-bit weights need more of L1: a load of activations by a warp touches eight rows, eight
+// lines for 512 bytes, and with 16 weight rows and half the k a warp they kept L1 81% busy. With twice the
+// rows they are loaded half as often: 8 rows over 64 experts of 7168 / 2048 55 -> 50 us, 512 rows of
+// 4096 / 1024 163 -> 133, of which 23 are one fragment at a time for more than 8 rows (both at once need
+// 48 registers more than the 96 a thread can have, with 18 warps on four quarters of an SM).
 //
 // The product is the matrix instruction m16n8k16 with the weights as its 16 rows and 8 rows of x as
 // its columns. Which k a lane's register stands for is free as long as both operands agree, so a
@@ -194,8 +201,8 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
                     mma_16816(acc[m][i], q[m][0].z, q[m][1].z, q[m][0].w, q[m][1].w, v[i][0].z, v[i][0].w);
                 }
         } else {
-            constexpr bool kOff = NT > 1;       // 136 is taken off the values, not off the sums
-            constexpr int M = NT > 1 ? 1 : 2;   // fragments at a time: two chains of dependent products either way
+            constexpr bool kOff = NT > 1;      // 136 is taken off the values, not off the sums
+            constexpr int M = NT > 1 ? 1 : 2;  // fragments at a time: two chains of dependent products either way
 #pragma unroll
             for (int m0 = 0; m0 < 2; m0 += M) {
                 float sum[M][NT][4] = {}, xs[4] = {};
