@@ -100,10 +100,10 @@ int64_t row_tiles(const GemmParams &p, int bm) { return p.S / bm + (p.E < p.S ? 
 
 // Which tile a product takes: the narrowest whose tiles are all resident at once, as a narrower one
 // gives each SM less and ends sooner (8 experts x 128 rows, 2048 to 1024 and back, forward: 64 wide
-// 35 us, 128 wide 30, 256 wide 37; at half the experts 21, 22, 30; at twice the rows 57, 42, 37). With
+// 31 us, 128 wide 27, 256 wide 33; at half the experts 17, 18, 26; at twice the experts 56, 47, 48). With
 // more tiles than SMs, 256 wide, and by CTA pairs of 256 rows where an expert has more than
 // `pair_rows`: a pair halves what each SM reads of the weights (16 experts, 2048 to 1024 and back,
-// forward: 200 rows each 63 us single, 59 pairs; 512 rows 106 and 90).
+// forward: 200 rows each 60 us single, 57 pairs; 512 rows 100 and 86).
 enum class TileShape { k64, k128, k256, kPair };
 template <typename Tiles>
 TileShape choose(const GemmParams &p, int pair_rows, Tiles tiles) {
@@ -234,8 +234,8 @@ cudaError_t launch_expert_ffn_backward(const ep_ffn_config &c, const ep_bf16 *ro
     }
     if (p.problems == 0) return cudaSuccess;
     // the epilogue is a large part of these tiles: between 64 and 256 wide there is nothing to gain, and
-    // pairs, which share it less evenly, pay later (2048 x 1024, 16 experts: 256 rows each 64 us single,
-    // 87 pairs; 512 rows 98 and 92)
+    // pairs, which share it less evenly, pay later (2048 x 1024, 16 experts: 256 rows each 65 us single,
+    // 91 pairs; 512 rows 101 and 97)
     switch (choose(p, 3 * kGemmBM, [&](int width) { return weight_tiles(p, kGemmBM, width < 128 ? 64 : 256); })) {
         case TileShape::k64: return launch<ExpertOp::kDWeight, 1, 64>(p, weight_tiles(p, kGemmBM, 64), s);
         case TileShape::kPair: return launch<ExpertOp::kDWeight, 2, 256>(p, weight_tiles(p, 2 * kGemmBM, 256), s);
