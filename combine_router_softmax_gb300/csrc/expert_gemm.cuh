@@ -446,26 +446,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     }
                 }
                 __syncwarp();
+                ok = !warp_failed(&failed);
                 phase ^= (s + whole) / kStages % 2;
                 s = (s + whole) % kStages;
                 if constexpr (Sh::kDW)
                     if (whole < kb) {
                         ready = false;
                         // every lane waits: each is to see the copies that it zeroes a part of
-                        ok = !failed && mbar_wait_limited(&full[s], phase, &failed);
+                        ok = ok && mbar_wait_warp(&full[s], phase, &failed);
                         const int steps = zero_rows_past_end<Sh>(stages + s * Sh::kStageBytes, t.rows - whole * kGemmBK, lane);
                         if (kRelay && ok) {
-                            ok = mbar_wait_limited<true>(&other[s], relayed >> s & 1, &failed);
+                            ok = mbar_wait_warp<true>(&other[s], relayed >> s & 1, &failed);
                             relayed ^= 1u << s;
                         }
                         if (elect_one() && ok) issue(s, steps, whole);
                         __syncwarp();
                         if (++s == kStages) s = 0, phase ^= 1;
                     }
-                ok = !failed;
                 ++acc_it;
             }
-            if (failed) {  // MMAs may still read the stages and write TMEM
+            if (warp_failed(&failed)) {  // MMAs may still read the stages and write TMEM
                 if (elect_one()) mma_commit<CG>(&drained);
                 __syncwarp();
                 int never = 0;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 it += kb;
                 if (t.rows % kGemmBK == 0) continue;
                 const int s = (it - 1) % kStages;
-                if (!mbar_wait_limited(&full[s], relayed >> s & 1, &failed)) break;
+                if (!mbar_wait_warp(&full[s], relayed >> s & 1, &failed)) break;
                 relayed ^= 1u << s;
                 zero_rows_past_end<Sh>(stages + s * Sh::kStageBytes, t.rows - (kb - 1) * kGemmBK, lane);
                 if (lane == 0) mbar_arrive_cluster(cluster_smem_u32(&other[s], 0));

@@ -1,0 +1,61 @@
+// What the expert kernels' bounded waits rest on, run alone: warps whose lanes have to agree on a failure, and
+// a barrier that nothing arrives at, waited for until the limit. Built and called by test_expert_waits.py.
+#include "tcgen05.cuh"
+
+namespace {
+
+// Warp 1 sets and clears the flag all the time; warp 0 counts the readings on which its lanes differ. Both
+// loops are counted.
+__global__ void agreement_kernel(int rounds, int *differ, int *seen_set) {
+    __shared__ volatile int failed;
+    if (threadIdx.x == 0) failed = 0;
+    __syncthreads();
+    int bad = 0, set = 0;
+    for (int i = 0; i < rounds; ++i) {
+        if (threadIdx.x / 32 == 1) {
+            failed = i & 1;
+        } else {
+            const unsigned votes = __ballot_sync(0xFFFFFFFFu, ep::warp_failed(&failed));
+            bad += votes != 0 && votes != 0xFFFFFFFFu;
+            set += votes != 0;
+        }
+    }
+    if (threadIdx.x == 0) *differ = bad, *seen_set = set;
+}
+
+// results: [0] lanes whose wait succeeded, [1] the flag after it, [2] whether a poll that starts after the
+// failure succeeds, [3] lanes that succeed on a phase that is complete.
+__global__ void give_up_kernel(int *results, int *error) {
+    __shared__ uint64_t never, done;
+    __shared__ volatile int failed;
+    if (threadIdx.x == 0) {
+        ep::mbar_init(&never, 1);
+        ep::mbar_init(&done, 1);
+        failed = 0;
+        ep::fence_mbar_init();
+        ep::mbar_arrive(&done);
+    }
+    __syncwarp();
+    const bool complete = ep::mbar_wait_warp(&done, 0, &failed);
+    const unsigned d = __ballot_sync(0xFFFFFFFFu, complete);
+    const bool ok = ep::mbar_wait_warp(&never, 0, &failed);
+    const unsigned v = __ballot_sync(0xFFFFFFFFu, ok);
+    if (threadIdx.x == 0) {
+        results[0] = __popc(v);
+        results[1] = failed;
+        results[2] = ep::mbar_poll_limited(&never, 0, &failed);
+        results[3] = __popc(d);
+        if (failed) atomicOr(error, ep::kErrExpertWait);
+    }
+}
+
+}  // namespace
+
+extern "C" int run_agreement(int rounds, int *differ, int *seen_set) {
+    agreement_kernel<<<1, 64>>>(rounds, differ, seen_set);
+    return (int)cudaDeviceSynchronize();
+}
+extern "C" int run_give_up(int *results, int *error) {
+    give_up_kernel<<<1, 32>>>(results, error);
+    return (int)cudaDeviceSynchronize();
+}

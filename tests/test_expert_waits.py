@@ -1,0 +1,54 @@
+"""The bounded waits of the expert kernels (tcgen05.cuh): a warp's lanes agree on a failure, a wait for what never
+comes ends, and ep_device_error reports it."""
+from __future__ import annotations
+
+import ctypes
+import subprocess
+
+import pytest
+import torch
+
+from gpu_harness import require_cuda
+
+
+@pytest.fixture(scope="module")
+def waits(tmp_path_factory):
+    import __graft_entry__
+
+    b = __graft_entry__._cuda_build_module()
+    lib = tmp_path_factory.mktemp("waits") / "expert_waits.so"
+    cmd = [b.nvcc_path(), *b.ARCH, "-O3", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared",
+           f"-I{b.ROOT / 'include'}", f"-I{b.CSRC}", str(b.ROOT / "tests" / "expert_waits.cu"), "-o", str(lib)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return lib
+
+
+def test_helpers_build(waits):
+    assert ctypes.CDLL(str(waits)).run_agreement
+
+
+@pytest.mark.gpu
+def test_a_warp_agrees_on_a_failure(waits):
+    require_cuda()
+    out = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    f = ctypes.CDLL(str(waits)).run_agreement
+    assert f(100000, ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(out.data_ptr() + 4)) == 0
+    differ, seen = out.tolist()
+    assert differ == 0 and 0 < seen < 100000
+
+
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_reported(waits):
+    require_cuda()
+    import combine_router_softmax_gb300 as ep
+
+    assert ep.ep_device_error() == 0
+    word = ctypes.c_void_p()
+    symbol = getattr(ep._lib, "_ZN2ep17expert_error_wordEPPi")  # ep::expert_error_word
+    assert symbol(ctypes.byref(word)) == 0
+    out = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    assert ctypes.CDLL(str(waits)).run_give_up(ctypes.c_void_p(out.data_ptr()), word) == 0
+    assert out.tolist() == [0, 1, 0, 32]
+    assert ep.ep_device_error() == 16  # an expert product gave up
+    assert ep.ep_device_error() == 0   # read and cleared
