@@ -324,12 +324,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
 
     Walk<OP, CG, NB> walk(p, lo, count, prefix);
     Tile t;
+    // what a producer has under way (it: the next fill of its thread; kRelay's uses of the second CTA's `full`)
+    bool produces = false;
+    uint32_t it = 0, relayed = 0, ever = 0;
 
     if (warp == 0 || warp > 1 + kEpilogueWarps) {
         // ---- producers: one lane each, which take the stages in turn
         if (elect_one()) {
             const uint32_t mine = warp == 0 ? 0 : warp - 1 - kEpilogueWarps;
-            uint32_t it = mine, relayed = 0, ever = 0;
+            produces = true;
+            it = mine;
             uint32_t s = mine, phase = 0;  // it % kStages, it / kStages % 2: kept by counting, a stage is few instructions
             int b = mine;                  // of the tile
             bool ok = true, ready = false;
@@ -394,17 +398,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                 }
                 b -= kb;
             }
-            // no copy may be under way when the CTA ends: after a failure nobody else waits for them
-            if (failed) {
-                for (int i = mine; i < kStages; i += kProducers) {
-                    int never = 0;
-                    if (rank == 0 && it > (uint32_t)i) {
-                        const uint32_t last = (it - 1 - i) / kStages;  // how often stage i was filled again
-                        mbar_wait_limited(&full[i], last & 1, &never);
-                    }
-                    if (rank == 1 && (ever >> i & 1)) mbar_wait_limited(&full[i], (relayed >> i & 1) ^ 1, &never);
-                }
-            }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -414,7 +407,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
             constexpr uint32_t idesc_half = mma_idesc(kGemmBM, NB, Sh::kAMn, Sh::kBMn);
             const uint64_t da_first = smem_desc(smem_u32(stages), Sh::kAMn ? 8192 : 16);
             const uint64_t db_first = smem_desc(smem_u32(stages) + Sh::kABytes, Sh::kBMn ? 8192 : 16);
-            uint32_t s = 0, phase = 0, acc_it = 0, relayed = 0;
+            uint32_t s = 0, phase = 0, acc_it = 0;
             bool ok = true, ready = false;
             while (ok && walk.next(t)) {
                 const int kb = walk.blocks(t);
@@ -465,15 +458,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     }
                 ++acc_it;
             }
-            if (warp_failed(&failed)) {  // MMAs may still read the stages and write TMEM
-                if (elect_one()) mma_commit<CG>(&drained);
-                __syncwarp();
-                int never = 0;
-                mbar_wait_limited(&drained, 0, &never);
-            }
         } else if (kRelay) {
             // the pair's second CTA: its part of the stages that go past an expert's end
-            uint32_t it = 0, relayed = 0;
             while (walk.next(t)) {
                 const int kb = walk.blocks(t);
                 it += kb;
@@ -606,8 +592,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
     }
 
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();  // no arrival may reach a CTA that has ended
-    if (threadIdx.x == 0 && failed) atomicOr(p.error, kErrExpertWait);
+    if constexpr (CG == 2) {
+        // a CTA that gave up tells the other one, whose memory its copies and MMAs may use
+        if (threadIdx.x == 0 && failed) st_cluster(cluster_smem_u32(const_cast<int *>(&failed), rank ^ 1), 1);
+        cluster_sync();  // no arrival may reach a CTA that has ended
+    }
+    // After a failure nobody has waited for what is under way, and it may have come after its warp had
+    // finished: from here on no role adds to it or sets `failed`. Nothing may be left when a CTA ends.
+    if (failed) {
+        if (produces) {
+            const uint32_t mine = warp == 0 ? 0 : warp - 1 - kEpilogueWarps;
+            int gave_up = 0;
+            if (rank == 0) {
+                wait_for_fills(full, it, mine, kProducers, kStages);
+            } else {
+                for (int i = mine; kRelay && i < kStages; i += kProducers)
+                    if (ever >> i & 1) mbar_wait_limited(&full[i], (relayed >> i & 1) ^ 1, &gave_up);
+                // copies for which the first CTA's barrier was not armed any more
+                for (int i = 0; i < 100; ++i) __nanosleep(10000);
+            }
+        } else if (warp == 1 && rank == 0) {  // MMAs read the stages and write TMEM
+            if (elect_one()) mma_commit<CG>(&drained);
+            __syncwarp();
+            int gave_up = 0;
+            mbar_wait_limited(&drained, 0, &gave_up);
+        }
+        __syncthreads();
+        if constexpr (CG == 2) cluster_sync();
+        if (threadIdx.x == 0) atomicOr(p.error, kErrExpertWait);
+    }
     if (warp == 1) tmem_free<CG>(tmem, Sh::kTmemCols);
 }
 

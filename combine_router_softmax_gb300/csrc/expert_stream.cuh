@@ -308,12 +308,12 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
     const int blocks = (p.N + kOut - 1) / kOut;
     StreamItems items(hit, hits, blocks);
     const int kb = (p.K + Sh::kStageK - 1) / Sh::kStageK;
+    uint32_t it = 0;  // the producer's next stage
 
     if (warp == kStreamWarps) {
         // ---- producer. Besides the weights it asks for the lines of x and of the scales that the stage's
         // consumers will read, three stages ahead of them: fetched by each warp for itself they cost an L2
         // latency a stage.
-        uint32_t it = 0;
         bool ok = true;
         for (; ok && items.any(); items.next()) {
             const auto [e, first, rows] = hit[items.index];
@@ -353,12 +353,6 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
                     }
                 }
         }
-        if (failed && lane == 0)  // no copy may be under way when the CTA ends
-            for (int i = 0; i < kStreamStages; ++i)
-                if (it > (uint32_t)i) {
-                    int never = 0;
-                    mbar_wait_limited(&full[i], ((it - 1 - i) / kStreamStages) & 1, &never);
-                }
         __syncwarp();
     } else {
         // ---- consumers. After a failure they go on without waiting: every warp reaches the barriers.
@@ -391,7 +385,12 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) expert_stream_ker
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0 && failed) atomicOr(p.error, kErrExpertWait);
+    // No copy may be under way when the CTA ends. A consumer may have given up after the producer had
+    // finished; from here on nobody sets `failed`.
+    if (failed && threadIdx.x == kStreamWarps * 32) {
+        wait_for_fills(full, it, 0, 1, kStreamStages);
+        atomicOr(p.error, kErrExpertWait);
+    }
 }
 
 template <bool GATED, int G>

@@ -109,6 +109,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, v
     return __all_sync(0xFFFFFFFFu, mbar_wait_limited<CLUSTER>(bar, parity, failed)) != 0;
 }
 
+// Waits until the copies of a producer have landed: of the fills first, first + step, ... below `it`, the last
+// one of each of the `stages` stages, whose barriers are `full`. One time limit for all of them. By one thread,
+// after a failure, once nobody else uses the barriers.
+__device__ __forceinline__ bool wait_for_fills(uint64_t *full, uint32_t it, uint32_t first, uint32_t step, uint32_t stages) {
+    int gave_up = 0;
+    for (uint32_t i = first; i < stages; i += step)
+        if (it > i) mbar_wait_limited(&full[i], (it - 1 - i) / stages & 1, &gave_up);
+    return gave_up == 0;
+}
+
 // True in one lane of the warp, all of which are active. The compiler knows of this predicate that
 // one lane alone passes: the instructions below take uniform operands, and behind an ordinary
 // `lane == 0` each of them becomes a loop over the active lanes.
@@ -127,6 +137,10 @@ __device__ __forceinline__ uint32_t cluster_smem_u32(const void *p, uint32_t ran
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
+}
+// Sets the int at `addr`, a shared::cluster address.
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_cta_rank() {
     uint32_t r;

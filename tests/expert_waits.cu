@@ -49,8 +49,25 @@ __global__ void give_up_kernel(int *results, int *error) {
     }
 }
 
+// A ring of four stages after `fills` fills, all of which have landed, or all but the last one:
+// results[late] = whether the wait says that all of them have.
+__global__ void fills_kernel(int fills, int *results) {
+    __shared__ uint64_t full[4];
+    for (int late = 0; late < 2; ++late) {
+        for (int i = 0; i < 4; ++i) ep::mbar_init(&full[i], 1);
+        ep::fence_mbar_init();
+        for (int i = 0; i < fills - late; ++i) ep::mbar_arrive(&full[i % 4]);
+        results[late] = ep::wait_for_fills(full, fills, 0, 2, 4) + 2 * ep::wait_for_fills(full, fills, 1, 2, 4);
+        for (int i = 0; i < 4; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(ep::smem_u32(&full[i])) : "memory");
+    }
+}
+
 }  // namespace
 
+extern "C" int run_fills(int fills, int *results) {
+    fills_kernel<<<1, 1>>>(fills, results);
+    return (int)cudaDeviceSynchronize();
+}
 extern "C" int run_agreement(int rounds, int *differ, int *seen_set) {
     agreement_kernel<<<1, 64>>>(rounds, differ, seen_set);
     return (int)cudaDeviceSynchronize();

@@ -39,6 +39,18 @@ def test_a_warp_agrees_on_a_failure(waits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fills", [1, 2, 4, 6, 9])
+def test_copies_under_way_are_waited_for(waits, fills):
+    """Two producers take a ring's fills in turn: each waits for its own, and says so when the last one does not
+    come in time."""
+    require_cuda()
+    out = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    assert ctypes.CDLL(str(waits)).run_fills(fills, ctypes.c_void_p(out.data_ptr())) == 0
+    late = (fills - 1) % 2  # the producer of the last fill
+    assert out.tolist() == [3, 3 - (1 << late)]
+
+
+@pytest.mark.gpu
 def test_a_wait_that_runs_out_is_reported(waits):
     require_cuda()
     import combine_router_softmax_gb300 as ep
