@@ -12,7 +12,9 @@
 // Operands are bf16, sums fp32 (in TMEM), results are rounded to bf16 once. h, dg and du are
 // rounded to bf16 where they become operands of the next product. g and u are no operands: they are
 // kept for the backward pass in fp16, which rounds eight times finer in the same 16 bits (the weights'
-// gradients are 0.0024 off in norm with it, 0.0031 with bf16); beyond 65504 it has infinity.
+// gradients are 0.0024 off in norm with it, 0.0031 with bf16) from 6e-5 on. What lies beyond 65504 is kept
+// as 65504, where silu and its derivative are at their limits; as infinity it would make NaN of a gradient
+// of 0 (s = 0 times g).
 //
 // One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
 // holding half of either operand): two producer warps feed a ring of shared-memory stages by TMA, in
@@ -86,6 +88,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+// A finite value within the halves' range; infinities and NaN as they are.
+__device__ __forceinline__ float half_range(float v) {
+    return fabsf(v) < INFINITY ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v;
 }
 __device__ __forceinline__ float2 half_values(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 // exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
@@ -531,8 +537,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                             const float dh = __uint_as_float(v[2 * i + k]);
                             const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
                             const float s = sigmoid(gg);
-                            du[k] = dh * gg * s;
-                            dg[k] = dh * uu * s * (1.0f + gg * (1.0f - s));
+                            // s first: it may be 0 where dh g or dh u overflows
+                            du[k] = dh * (gg * s);
+                            dg[k] = dh * (uu * (s * (1.0f + gg * (1.0f - s))));
                         }
                         o[i] = bf16_pair(dg[0], dg[1]);
                         u[i] = bf16_pair(du[0], du[1]);
@@ -558,11 +565,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
                     if (p.g) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = half_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        for (int i = 0; i < 16; ++i) o[i] = half_pair(half_range(__uint_as_float(v[2 * i])), half_range(__uint_as_float(v[2 * i + 1])));
                         slab_put(slab, lane, o);
                         slab_store(slab, lane, p.g + row * N, N, n, rows);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = half_pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+                        for (int i = 0; i < 16; ++i) o[i] = half_pair(half_range(__uint_as_float(w[2 * i])), half_range(__uint_as_float(w[2 * i + 1])));
                         slab_put(slab, lane, o);
                         slab_store(slab, lane, p.u + row * N, N, n, rows);
                     }
