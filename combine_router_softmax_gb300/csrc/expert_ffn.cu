@@ -90,6 +90,7 @@ GemmParams base_params(const ep_ffn_config &c, const int32_t *expert_offset) {
     p.expert_offset = expert_offset;
     p.E = c.E;
     p.S = c.rows;
+    p.saved_bf16 = c.saved_bf16;
     return p;
 }
 

@@ -12,9 +12,9 @@
 // Operands are bf16, sums fp32 (in TMEM), results are rounded to bf16 once. h, dg and du are
 // rounded to bf16 where they become operands of the next product. g and u are no operands: they are
 // kept for the backward pass in fp16, which rounds eight times finer in the same 16 bits (the weights'
-// gradients are 0.0024 off in norm with it, 0.0031 with bf16) from 6e-5 on. What lies beyond 65504 is kept
-// as 65504, where silu and its derivative are at their limits; as infinity it would make NaN of a gradient
-// of 0 (s = 0 times g).
+// gradients are 0.0024 off in norm with it, 0.0031 with bf16) from 6e-5 on, or in bf16, whose range is fp32's.
+// What is finite and lies beyond the type's largest value is kept as that (65504: silu and its derivative
+// are at their limits there); as infinity it would make NaN of a gradient of 0 (s = 0 times g).
 //
 // One persistent CTA per SM (CG = 2: one CTA pair per two SMs, a tile of 256 rows, each CTA
 // holding half of either operand): two producer warps feed a ring of shared-memory stages by TMA, in
@@ -59,7 +59,8 @@ struct GemmParams {
     int32_t N[3];      // output columns of each problem (row products: N[0])
     int32_t problems;  // DWeight: how many of the three are wanted
     ep_bf16 *out[3];   // GateUp: h; DGateUp: dg, du; DWeight: the gradients [E, M, N]
-    uint16_t *g, *u;   // fp16. GateUp: written when not null; DGateUp: read
+    uint16_t *g, *u;   // GateUp: written when not null; DGateUp: read
+    int32_t saved_bf16;  // their type: 0 fp16, 1 bf16
     int32_t *error;
 };
 
@@ -89,13 +90,61 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// A finite value within the halves' range; infinities and NaN as they are.
-__device__ __forceinline__ float half_range(float v) {
-    return fabsf(v) < INFINITY ? fminf(fmaxf(v, -65504.0f), 65504.0f) : v;
-}
-__device__ __forceinline__ float2 half_values(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 // exp(-x) overflows to infinity for x below -88: the quotient is then 0, the limit.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 32 sums as they are kept for the backward pass. Beyond the type's largest value, which hardly ever occurs,
+// a finite one is kept as that; infinities and NaN stay.
+__device__ __forceinline__ void saved_pairs(const uint32_t (&v)[32], uint32_t (&o)[16], bool bf16) {
+    const float top = bf16 ? 3.38953139e38f : 65504.0f;
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(__uint_as_float(v[i])));
+    if (most > top) {
+        const auto within = [&](uint32_t bits) {
+            const float x = __uint_as_float(bits);
+            return fabsf(x) < INFINITY ? fminf(fmaxf(x, -top), top) : x;
+        };
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float lo = within(v[2 * i]), hi = within(v[2 * i + 1]);
+            o[i] = bf16 ? bf16_pair(lo, hi) : half_pair(lo, hi);
+        }
+    } else if (bf16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = half_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ float2 saved_values(uint32_t v) {
+    if constexpr (BF16)
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+// d_g and d_u of a row's 32 columns from d_h; u's place takes d_u.
+template <bool BF16>
+__device__ __forceinline__ void gate_gradients(const uint32_t (&dh)[32], const uint32_t (&g)[16], uint32_t (&u)[16],
+                                               uint32_t (&d_g)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float dg[2], du[2];
+        const float2 g2 = saved_values<BF16>(g[i]), u2 = saved_values<BF16>(u[i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float d = __uint_as_float(dh[2 * i + k]);
+            const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
+            const float s = sigmoid(gg);
+            // s first: it may be 0 where dh g or dh u overflows
+            du[k] = d * (gg * s);
+            dg[k] = d * (uu * (s * (1.0f + gg * (1.0f - s))));
+        }
+        d_g[i] = bf16_pair(dg[0], dg[1]);
+        u[i] = bf16_pair(du[0], du[1]);
+    }
+}
 
 // An epilogue warp's results lie one row to a thread, 32 columns at a time; they pass through a slab
 // of shared memory (32 rows of 64 bytes, 16-byte words swizzled by the row) so that global memory
@@ -528,22 +577,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     ask(c + 2 * kCols);
                     tmem_load_32(src + c, v);
                     tmem_wait_ld(v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float dg[2], du[2];
-                        const float2 g2 = half_values(g[i]), u2 = half_values(u[i]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float dh = __uint_as_float(v[2 * i + k]);
-                            const float gg = k ? g2.y : g2.x, uu = k ? u2.y : u2.x;
-                            const float s = sigmoid(gg);
-                            // s first: it may be 0 where dh g or dh u overflows
-                            du[k] = dh * (gg * s);
-                            dg[k] = dh * (uu * (s * (1.0f + gg * (1.0f - s))));
-                        }
-                        o[i] = bf16_pair(dg[0], dg[1]);
-                        u[i] = bf16_pair(du[0], du[1]);
-                    }
+                    if (p.saved_bf16)
+                        gate_gradients<true>(v, g, u, o);
+                    else
+                        gate_gradients<false>(v, g, u, o);
                     slab_put(slab, lane, o);
                     slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
                     slab_put(slab, lane, u);
@@ -564,12 +601,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     slab_put(slab, lane, o);
                     slab_store(slab, lane, p.out[0] + row * N, N, n, rows);
                     if (p.g) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = half_pair(half_range(__uint_as_float(v[2 * i])), half_range(__uint_as_float(v[2 * i + 1])));
+                        saved_pairs(v, o, p.saved_bf16);
                         slab_put(slab, lane, o);
                         slab_store(slab, lane, p.g + row * N, N, n, rows);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = half_pair(half_range(__uint_as_float(w[2 * i])), half_range(__uint_as_float(w[2 * i + 1])));
+                        saved_pairs(w, o, p.saved_bf16);
                         slab_put(slab, lane, o);
                         slab_store(slab, lane, p.u + row * N, N, n, rows);
                     }

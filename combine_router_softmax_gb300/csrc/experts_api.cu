@@ -17,6 +17,7 @@ ep_status from_cuda(cudaError_t e) { return e == cudaSuccess ? EP_OK : EP_ERR_CU
 ep_status check_ffn(const ep_ffn_config *c) {
     if (!c) return EP_ERR_INVALID_ARG;
     if (c->rows < 0 || c->H <= 0 || c->I <= 0 || c->E <= 0) return EP_ERR_INVALID_ARG;
+    if (c->saved_bf16 != 0 && c->saved_bf16 != 1) return EP_ERR_INVALID_ARG;
     if (c->H % 8 != 0 || c->I % 8 != 0 || c->E > ep::kMaxE) return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }

@@ -20,12 +20,15 @@ __all__ = [*EXPORTS, "EpFfnConfig", "EpW4Config", "EpGradTensor", "GradList"]
 
 
 class EpFfnConfig(ctypes.Structure):
-    """``ep_ffn_config`` of include/ep_experts.h."""
-    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "H", "I", "E")]
+    """``ep_ffn_config`` of include/ep_experts.h.
+
+    ``saved_bf16``: what ep_expert_ffn keeps for the backward pass (g and u) is float16 (0), finer for values
+    between 6.1e-5 and 65504, or bfloat16 (1), for values of any size."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "H", "I", "E", "saved_bf16")]
 
     @classmethod
-    def make(cls, *, rows, H, I, E) -> "EpFfnConfig":
-        return cls(rows, H, I, E)
+    def make(cls, *, rows, H, I, E, saved_bf16=0) -> "EpFfnConfig":
+        return cls(rows, H, I, E, saved_bf16)
 
 
 class EpW4Config(ctypes.Structure):
@@ -68,9 +71,11 @@ def _bf16(t, shape, name, device=None):
     return _ptr(t, torch.bfloat16, shape, name, device)
 
 
-def _half(t, shape, name, device=None):
-    """Memory for 16-bit values: a float16 tensor, or a bfloat16 one of which nobody reads the values."""
-    return _ptr(t, torch.bfloat16 if t is not None and t.dtype is torch.bfloat16 else torch.float16, shape, name, device)
+def _saved(cfg, t, shape, name, device=None):
+    """g or u: a bfloat16 tensor where cfg.saved_bf16 is 1; else a float16 one, or a bfloat16 one as mere memory for
+    the halves, of which nobody reads the values."""
+    bf16 = cfg.saved_bf16 == 1 or t is not None and t.dtype is torch.bfloat16
+    return _ptr(t, torch.bfloat16 if bf16 else torch.float16, shape, name, device)
 
 
 def ep_expert_ffn(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, h, y, g=None, u=None,
@@ -78,27 +83,29 @@ def ep_expert_ffn(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, h
     """y = (silu(rows Wg^T) * (rows Wu^T)) Wd^T with each row's own expert; h is the product before Wd.
 
     rows, y bf16 [rows, H]; h bf16 [rows, I]; w_gate, w_up bf16 [E, I, H]; w_down bf16 [E, H, I]; expert_offset
-    int32 [E + 1]. g and u (float16 [rows, I], both or neither) are what ep_expert_ffn_backward needs besides h;
-    they are written as halves, into bfloat16 tensors too, which are then storage only."""
+    int32 [E + 1]. g and u ([rows, I], both or neither) are what ep_expert_ffn_backward needs besides h: bfloat16
+    where cfg.saved_bf16 is 1, else float16. Without it they are written as halves into bfloat16 tensors too, which
+    are then storage only: their values mean nothing."""
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
     dev = _device()
     _check(_lib.ep_expert_ffn(ctypes.byref(cfg), _bf16(rows, (S, H), "rows", dev),
                               _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset", dev),
                               _bf16(w_gate, (E, I, H), "w_gate", dev), _bf16(w_up, (E, I, H), "w_up", dev),
-                              _bf16(w_down, (E, H, I), "w_down", dev), _half(g, (S, I), "g", dev), _half(u, (S, I), "u", dev),
+                              _bf16(w_down, (E, H, I), "w_down", dev), _saved(cfg, g, (S, I), "g", dev), _saved(cfg, u, (S, I), "u", dev),
                               _bf16(h, (S, I), "h", dev), _bf16(y, (S, H), "y", dev), _stream(stream)), "ep_expert_ffn")
 
 
 def ep_expert_ffn_backward(cfg: EpFfnConfig, rows, expert_offset, w_gate, w_up, w_down, g, u, h, d_y, d_g, d_u,
                            d_rows=None, d_w_gate=None, d_w_up=None, d_w_down=None, stream=None) -> None:
-    """Gradients of ep_expert_ffn for d_y, the gradient of y. d_g and d_u bf16 [rows, I] are written on the
-    way; d_rows and the weights' gradients (overwritten) are written where they are given."""
+    """Gradients of ep_expert_ffn for d_y, the gradient of y, from the g, u and h that it wrote with the same cfg. d_g
+    and d_u bf16 [rows, I] are written on the way; d_rows and the weights' gradients (overwritten) are written
+    where they are given."""
     S, H, I, E = cfg.rows, cfg.H, cfg.I, cfg.E
     dev = _device()
     _check(_lib.ep_expert_ffn_backward(
         ctypes.byref(cfg), _bf16(rows, (S, H), "rows", dev), _ptr(expert_offset, torch.int32, (E + 1,), "expert_offset", dev),
         _bf16(w_gate, (E, I, H), "w_gate", dev), _bf16(w_up, (E, I, H), "w_up", dev), _bf16(w_down, (E, H, I), "w_down", dev),
-        _half(g, (S, I), "g", dev), _half(u, (S, I), "u", dev), _bf16(h, (S, I), "h", dev), _bf16(d_y, (S, H), "d_y", dev),
+        _saved(cfg, g, (S, I), "g", dev), _saved(cfg, u, (S, I), "u", dev), _bf16(h, (S, I), "h", dev), _bf16(d_y, (S, H), "d_y", dev),
         _bf16(d_g, (S, I), "d_g", dev), _bf16(d_u, (S, I), "d_u", dev), _bf16(d_rows, (S, H), "d_rows", dev),
         _bf16(d_w_gate, (E, I, H), "d_w_gate", dev), _bf16(d_w_up, (E, I, H), "d_w_up", dev),
         _bf16(d_w_down, (E, H, I), "d_w_down", dev), _stream(stream)), "ep_expert_ffn_backward")

@@ -85,7 +85,40 @@ def test_halves_beyond_their_range(ep, counts, H, I):
     check(o, bounds, ref.U11, HALF_MAX)
 
 
-def test_an_infinite_row_stays_infinite(ep):
+@pytest.mark.parametrize("counts,H,I", [([40], 64, 64), ([5, 300], 264, 136)])
+@pytest.mark.parametrize("x_scale", [1e-12, 1e-6, 1.0, 1e5, 1e15])
+def test_bfloat16_at_any_scale(ep, counts, H, I, x_scale):
+    """Kept as bf16, g and u of any size give gradients within the roundings' bounds."""
+    o, bounds = run(ep, counts, H, I, x_scale, seed=I, dtype=BF16, saved_bf16=1)
+    check(o, bounds, ref.U16, math.inf)
+
+
+def test_bfloat16_at_the_end_of_fp32(ep):
+    """Sums between the largest bf16 and the largest fp32 value stay finite, and silu is at its limits."""
+    n = 64
+    x = torch.zeros((3, n), dtype=BF16, device="cuda")
+    x[0, 0], x[1, 0], x[2, 0] = 2.0**127, -2.0**127, 1.0
+    x[:, 1] = x[:, 0]
+    x[0, 2], x[1, 2] = 1.0, -1.0
+    w = torch.zeros((1, n, n), dtype=BF16, device="cuda")
+    w[0, :, 0], w[0, :, 1] = 2 - 2.0**-7, 2.0**-8  # x0 (w0 + w1) = 2^127 (2 - 2^-8): bf16 would round it up
+    up, down = torch.zeros_like(w), torch.zeros_like(w)
+    up[0, :, 2], down[0] = 1.0, 1.0
+    g, u, h, d_g, d_u = (torch.full((3, n), 7.0, dtype=BF16, device="cuda") for _ in range(5))
+    y, d_y = torch.zeros((3, n), dtype=BF16, device="cuda"), torch.ones((3, n), dtype=BF16, device="cuda")
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    cfg = ep.EpFfnConfig.make(rows=3, H=n, I=n, E=1, saved_bf16=1)
+    ep.ep_expert_ffn(cfg, x, off, w, up, down, h, y, g=g, u=u)
+    ep.ep_expert_ffn_backward(cfg, x, off, w, up, down, g, u, h, d_y, d_g, d_u)
+    top = torch.finfo(BF16).max
+    assert (g[0] == top).all() and (g[1] == -top).all()
+    assert (u[0] == 1).all() and (u[1] == -1).all()
+    # dh = 64: d_g = dh u silu'(g) with silu' = 1 and 0, d_u = dh silu(g), which is infinite and 0
+    assert (d_g[0] == 64).all() and (d_g[1] == 0).all() and (d_u[1] == 0).all()
+
+
+@pytest.mark.parametrize("kept", [F16, BF16])
+def test_an_infinite_row_stays_infinite(ep, kept):
     """What the forward pass cannot represent is not made finite: a row with an infinity has no gradient."""
     gen = torch.Generator(device="cuda").manual_seed(0)
     x = torch.randn((9, 64), generator=gen, device="cuda").to(BF16)
@@ -93,9 +126,9 @@ def test_an_infinite_row_stays_infinite(ep):
     x[6, 3] = float("nan")
     w = [(torch.randn((1, 64, 64), generator=gen, device="cuda") / 8).to(BF16) for _ in range(3)]
     h, y = (torch.empty((9, 64), dtype=BF16, device="cuda") for _ in range(2))
-    g, u = (torch.empty((9, 64), dtype=F16, device="cuda") for _ in range(2))
+    g, u = (torch.empty((9, 64), dtype=kept, device="cuda") for _ in range(2))
     off = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
-    ep.ep_expert_ffn(ep.EpFfnConfig.make(rows=9, H=64, I=64, E=1), x, off, *w, h, y, g=g, u=u)
+    ep.ep_expert_ffn(ep.EpFfnConfig.make(rows=9, H=64, I=64, E=1, saved_bf16=int(kept is BF16)), x, off, *w, h, y, g=g, u=u)
     for t in (g, u):
         assert torch.isinf(t[4]).all() and torch.isnan(t[6]).all()
         assert torch.isfinite(t[[0, 1, 2, 3, 5, 7, 8]]).all()
