@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                     if (b == kb - 1) mma_commit<CG>(&acc_full[slot]);
                 };
                 const int whole = Sh::kDW ? t.rows / kGemmBK : kb;  // stages without a row past the expert's end
+                bool issued = false;
                 if (elect_one()) {
                     if (acc_it >= 2) ok = mbar_poll_limited<CG == 2>(&acc_empty[slot], (acc_it / 2 - 1) & 1, &failed);
                     tmem_fence_after();
@@ -492,9 +493,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) expert_gemm_kernel(const __gr
                         if (ok) issue(at, kGemmBK / 16, b);
                         at = next;
                     }
+                    issued = ok;
                 }
-                __syncwarp();
-                ok = !warp_failed(&failed);
+                // that thread's waits count for all: lanes that each read `failed` could part here, and the
+                // next elect.sync would wait for the missing ones without a limit
+                ok = __any_sync(0xFFFFFFFFu, issued);
                 phase ^= (s + whole) / kStages % 2;
                 s = (s + whole) % kStages;
                 if constexpr (Sh::kDW)

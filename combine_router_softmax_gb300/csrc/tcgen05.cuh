@@ -95,15 +95,10 @@ __device__ __forceinline__ bool mbar_poll_limited(uint64_t *bar, uint32_t parity
     }
 }
 
-// A warp's lanes read `failed` at different times, and another warp may set it in between: lanes that went
-// by their own readings could part, and the next instruction that needs all of them would wait without
-// a limit. Lane 0's reading counts for all.
-__device__ __forceinline__ bool warp_failed(volatile int *failed) {
-    return __shfl_sync(0xFFFFFFFFu, *failed, 0) != 0;
-}
-
 // mbar_wait_limited by every lane of a warp, each of which is to see what the phase brings: true in
-// all of them or in none.
+// all of them or in none. A warp's lanes read `failed` at different times, and another warp may set it in
+// between: lanes that went by their own readings could part, and the next instruction that needs all of
+// them would wait without a limit.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *failed) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_limited<CLUSTER>(bar, parity, failed)) != 0;

@@ -4,23 +4,34 @@
 
 namespace {
 
-// Warp 1 sets and clears the flag all the time; warp 0 counts the readings on which its lanes differ. Both
-// loops are counted.
-__global__ void agreement_kernel(int rounds, int *differ, int *seen_set) {
+// Warp 0 waits for a phase, lane by lane; warp 1 says that it has failed, and completes the phase, at about
+// the time that the waits look at either: whatever comes first, the lanes have one answer. results[0] rounds on
+// which they differ, [1] rounds that succeed, [2] rounds that fail.
+__global__ void agreement_kernel(int rounds, int *results) {
+    __shared__ uint64_t bar;
     __shared__ volatile int failed;
-    if (threadIdx.x == 0) failed = 0;
-    __syncthreads();
-    int bad = 0, set = 0;
+    int differ = 0, good = 0, bad = 0;
     for (int i = 0; i < rounds; ++i) {
-        if (threadIdx.x / 32 == 1) {
-            failed = i & 1;
-        } else {
-            const unsigned votes = __ballot_sync(0xFFFFFFFFu, ep::warp_failed(&failed));
-            bad += votes != 0 && votes != 0xFFFFFFFFu;
-            set += votes != 0;
+        if (threadIdx.x == 0) {
+            ep::mbar_init(&bar, 1);
+            failed = 0;
+            ep::fence_mbar_init();
         }
+        __syncthreads();
+        if (threadIdx.x / 32 == 0) {
+            const unsigned votes = __ballot_sync(0xFFFFFFFFu, ep::mbar_wait_warp(&bar, 0, &failed));
+            differ += votes != 0 && votes != 0xFFFFFFFFu;
+            good += votes == 0xFFFFFFFFu;
+            bad += votes == 0;
+        } else if (threadIdx.x == 32) {
+            if (i & 1) failed = 1;
+            __nanosleep(i % 64 * 50);
+            if (i % 4 != 1) ep::mbar_arrive(&bar);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(ep::smem_u32(&bar)) : "memory");
     }
-    if (threadIdx.x == 0) *differ = bad, *seen_set = set;
+    if (threadIdx.x == 0) results[0] = differ, results[1] = good, results[2] = bad;
 }
 
 // results: [0] lanes whose wait succeeded, [1] the flag after it, [2] whether a poll that starts after the
@@ -68,8 +79,8 @@ extern "C" int run_fills(int fills, int *results) {
     fills_kernel<<<1, 1>>>(fills, results);
     return (int)cudaDeviceSynchronize();
 }
-extern "C" int run_agreement(int rounds, int *differ, int *seen_set) {
-    agreement_kernel<<<1, 64>>>(rounds, differ, seen_set);
+extern "C" int run_agreement(int rounds, int *results) {
+    agreement_kernel<<<1, 64>>>(rounds, results);
     return (int)cudaDeviceSynchronize();
 }
 extern "C" int run_give_up(int *results, int *error) {
