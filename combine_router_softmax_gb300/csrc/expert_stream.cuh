@@ -22,13 +22,12 @@
 //
 // Weights are bf16, or 4 bits with one bf16 scale for G consecutive k. There a nibble v becomes the
 // bf16 value 128 + v by setting the bits 0x4300 over it (bf16 has 7 bits of fraction, so at 128 its
-// step is 1): one logic operation for two nibbles. What is over, 136, comes off in one of two ways. For
-// up to 8 rows of x it is taken off the sums: sum (128 + v) x - 136 sum x = sum (v - 8) x, with sum x
-// from the same instruction and a matrix of ones; the sums are about 30 times what is left of them,
-// which costs 5 of fp32's 24 bits where the result keeps 8. For more rows it is taken off the values,
-// exactly. Shifts, logic and the bf16 subtraction all take two cycles a quarter of an SM, 22 for a word
-// of 8 nibbles with it and 14 without; the products with ones take 8 for each eight rows of x. Either
-// way products with bf16 activations are exact in fp32; a group is summed in fp32 and scaled as a whole.
+// step is 1): one logic operation for two nibbles. What is over, 136, is taken off the values, exactly. Taken
+// off the sums, sum (128 + v) x - 136 sum x, it would save the subtraction (shifts, logic and subtraction take
+// two cycles a quarter of an SM each: 22 for a word of 8 nibbles, 14 without it) but leave the rounding of
+// 136 x behind, which an activation some hundred times the others' size makes larger than bf16's, and NaN of
+// an infinite one. Products with bf16 activations are exact in fp32; a group is summed in fp32 and
+// scaled as a whole.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,18 +60,15 @@ struct StreamParams {
     int32_t *error;
 };
 
-// Nibbles i and i + 4 of a word: as the bf16 values 128 + v, or v - 8.
-template <bool OFF>
+// Nibbles i and i + 4 of a word as the bf16 values v - 8.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
     uint32_t v;
-    // (word >> 4 i) & 0x000F000F | 0x43004300
+    // 128 + v: (word >> 4 i) & 0x000F000F | 0x43004300
     asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)));
-    if (!OFF) return v;
     const __nv_bfloat162 m = __float2bfloat162_rn(136.0f);
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), m);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -201,24 +197,19 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
                     mma_16816(acc[m][i], q[m][0].z, q[m][1].z, q[m][0].w, q[m][1].w, v[i][0].z, v[i][0].w);
                 }
         } else {
-            constexpr bool kOff = NT > 1;      // 136 is taken off the values, not off the sums
             constexpr int M = NT > 1 ? 1 : 2;  // fragments at a time: two chains of dependent products either way
 #pragma unroll
             for (int m0 = 0; m0 < 2; m0 += M) {
-                float sum[M][NT][4] = {}, xs[4] = {};
+                float sum[M][NT][4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if constexpr (!kOff) {
-                        mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].x, v[0][j].y);
-                        mma_16816(xs, kOnes, kOnes, kOnes, kOnes, v[0][j].z, v[0][j].w);
-                    }
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         const uint32_t w0 = word_of(q[m0 + m][0], j), w1 = word_of(q[m0 + m][1], j);
 #pragma unroll
                         for (int step = 0; step < 2; ++step) {
-                            const uint32_t a0 = w4_pair<kOff>(w0, 2 * step), a1 = w4_pair<kOff>(w1, 2 * step);
-                            const uint32_t a2 = w4_pair<kOff>(w0, 2 * step + 1), a3 = w4_pair<kOff>(w1, 2 * step + 1);
+                            const uint32_t a0 = w4_pair(w0, 2 * step), a1 = w4_pair(w1, 2 * step);
+                            const uint32_t a2 = w4_pair(w0, 2 * step + 1), a3 = w4_pair(w1, 2 * step + 1);
 #pragma unroll
                             for (int i = 0; i < NT; ++i)
                                 mma_16816(sum[m][i], a0, a1, a2, a3, step ? v[i][j].z : v[i][j].x, step ? v[i][j].w : v[i][j].y);
@@ -234,13 +225,10 @@ __device__ __forceinline__ void stream_pass(const StreamParams &p, StreamWarp &w
                                 const float f = __uint_as_float(((part / 2 ? of.y : of.x) >> (16 * (part % 2))) << 16);
 #pragma unroll
                                 for (int i = 0; i < NT; ++i) {
-                                    const float d = kOff ? sum[m][i][r] : fmaf(-136.0f, xs[r % 2], sum[m][i][r]);
-                                    acc[m0 + m][i][r] = fmaf(f, d, acc[m0 + m][i][r]);
+                                    acc[m0 + m][i][r] = fmaf(f, sum[m][i][r], acc[m0 + m][i][r]);
                                     sum[m][i][r] = 0.0f;
                                 }
                             }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) xs[r] = 0.0f;
                     }
                 }
             }

@@ -135,11 +135,14 @@ ep_status ep_w4_pack(const ep_w4_config *cfg, const ep_bf16 *w, uint8_t *q, ep_b
 
 /*
  * ep_w4_linear -- y[s, n] = sum_k x[s, k] w[e, n, k], e the expert that owns
- * row s, w the packed weight's values. The products are exact, sums fp32, y is
- * rounded to bf16 once. Right for any number of rows; made for few: the weights
- * are read once for every 16 rows of an expert.
+ * row s, w the packed weight's values. The products x (q - 8) are exact; they are
+ * summed in fp32 over a group, times its scale, then over the groups; y is rounded
+ * to bf16 once. An infinite x times a weight has the weight's sign, and is NaN
+ * where q = 8. Right for any number of rows; made for few: the weights are read
+ * once for every 16 rows of an expert.
  *
- * x : const bf16 [rows, K], 16-byte aligned       y : bf16 [rows, N] output
+ * x : const bf16 [rows, K], 16-byte aligned
+ * y : bf16 [rows, N] output, 16-byte aligned
  */
 ep_status ep_w4_linear(const ep_w4_config *cfg, const ep_bf16 *x, const int32_t *expert_offset, const uint8_t *q,
                        const ep_bf16 *scale, ep_bf16 *y, cudaStream_t stream);
