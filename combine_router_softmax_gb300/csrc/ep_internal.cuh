@@ -351,6 +351,6 @@ cudaError_t launch_route_backward(const ep_config &c, const float *logits, const
 // Gradient norm and clipping (grad_clip.cu); scale false: the norm alone.
 size_t grad_workspace_bytes(int32_t n);
 cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm,
-                             float *partial, cudaStream_t s);
+                             double *partial, cudaStream_t s);
 
 }  // namespace ep

@@ -159,7 +159,7 @@ ep_status ep_grad_norm(const ep_grad_tensor *tensors, int32_t n, float *norm, vo
                        cudaStream_t stream) {
     const ep_status st = check_grads(tensors, n, norm, workspace, workspace_bytes, false);
     if (st != EP_OK) return st;
-    return from_cuda(ep::launch_grad_clip(tensors, n, false, 0.0f, norm, static_cast<float *>(workspace), stream));
+    return from_cuda(ep::launch_grad_clip(tensors, n, false, 0.0f, norm, static_cast<double *>(workspace), stream));
 }
 
 ep_status ep_grad_clip(const ep_grad_tensor *tensors, int32_t n, float max_norm, float *norm, void *workspace,
@@ -167,7 +167,7 @@ ep_status ep_grad_clip(const ep_grad_tensor *tensors, int32_t n, float max_norm,
     if (!(max_norm >= 0.0f)) return EP_ERR_INVALID_ARG;
     const ep_status st = check_grads(tensors, n, norm, workspace, workspace_bytes, true);
     if (st != EP_OK) return st;
-    return from_cuda(ep::launch_grad_clip(tensors, n, true, max_norm, norm, static_cast<float *>(workspace), stream));
+    return from_cuda(ep::launch_grad_clip(tensors, n, true, max_norm, norm, static_cast<double *>(workspace), stream));
 }
 
 }  // extern "C"

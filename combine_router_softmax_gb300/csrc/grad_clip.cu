@@ -92,31 +92,40 @@ __device__ __forceinline__ int64_t values_to_boundary(const V *p) {
     return (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(V);
 }
 
-// The sum of the squares of n values, this thread's part: four independent sums of fp32, of at most
-// chunk / kClipThreads / 4 values each.
-template <typename V>
-__device__ float square_sum(const V *p, int64_t n) {
+// The sum of the squares of n values (SCALED: times `scale`), this thread's part: four independent sums of
+// fp32, of at most chunk / kClipThreads / 4 values each. `bits` gets those of all values' magnitudes.
+template <bool SCALED, typename V>
+__device__ __forceinline__ float square_sum(const V *p, int n, float scale, uint32_t &bits) {
     constexpr int kVec = Io<V>::kVec;
     float acc[4] = {0, 0, 0, 0};
-    const int64_t head = min(values_to_boundary(p), n);
+    const int head = min((int)values_to_boundary(p), n);
     if (threadIdx.x < head) {
-        const float v = Io<V>::load(p + threadIdx.x);
+        const float v = Io<V>::load(p + threadIdx.x) * (SCALED ? scale : 1.0f);
         acc[0] = v * v;
+        bits |= __float_as_uint(v) << 1;
     }
     const uint4 *q = reinterpret_cast<const uint4 *>(p + head);
-    const int64_t vecs = (n - head) / kVec;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < vecs; i += kClipThreads) {
+    const int vecs = (n - head) / kVec;
+    uint32_t words = 0;
+#pragma unroll(SCALED ? 1 : 4)
+    for (int i = threadIdx.x; i < vecs; i += kClipThreads) {
+        const uint4 w = q[i];
         float v[kVec];
-        Io<V>::unpack(q[i], v);
+        Io<V>::unpack(w, v);
+        words |= w.x | w.y | w.z | w.w;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) acc[j % 4] = fmaf(v[j], v[j], acc[j % 4]);
+        for (int j = 0; j < kVec; ++j) {
+            if (SCALED) v[j] *= scale;
+            acc[j % 4] = fmaf(v[j], v[j], acc[j % 4]);
+        }
     }
-    const int64_t tail = head + vecs * kVec + threadIdx.x;
+    const int tail = head + vecs * kVec + threadIdx.x;
     if (tail < n) {
-        const float v = Io<V>::load(p + tail);
+        const float v = Io<V>::load(p + tail) * (SCALED ? scale : 1.0f);
         acc[1] = fmaf(v, v, acc[1]);
+        bits |= __float_as_uint(v) << 1;
     }
+    bits |= words & (sizeof(V) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu);  // without the signs
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -166,12 +175,9 @@ __device__ float cta_sum(float v) {
     return v;
 }
 
-// partial[blockIdx.x] = the sum of the squares of this CTA's chunks. fp32 throughout: the chains are
-// short (some hundred steps in a thread, ten in the tree), and the 64-bit units are few: with the
-// tree in 64 bits it took longer than the values (300 tensors, 14 MB, both kernels: 36 us).
-__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ ClipTable tab, float *partial) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+// This thread's part of the sum of the squares of the CTA's chunks.
+template <bool SCALED>
+__device__ __forceinline__ float share_sum(const ClipTable &tab, float scale, uint32_t &bits) {
     float sum = 0;
     const int end_tensor = tab.tensor[blockIdx.x + 1], end_at = tab.at[blockIdx.x + 1];
     int i = tab.tensor[blockIdx.x], c = tab.at[blockIdx.x];
@@ -181,26 +187,57 @@ __global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_
         const int64_t begin = (int64_t)c * tab.chunk, end = min((int64_t)stop * tab.chunk, t.numel);
         // chunk by chunk, so that no fp32 sum grows long
         for (int64_t v = begin; v < end; v += tab.chunk) {
-            const int64_t n = min((int64_t)tab.chunk, end - v);
+            const int n = (int)min((int64_t)tab.chunk, end - v);
             if (t.dtype == EP_F32)
-                sum += square_sum(static_cast<const float *>(t.data) + v, n);
+                sum += square_sum<SCALED>(static_cast<const float *>(t.data) + v, n, scale, bits);
             else if (t.dtype == EP_BF16)
-                sum += square_sum(static_cast<const __nv_bfloat16 *>(t.data) + v, n);
+                sum += square_sum<SCALED>(static_cast<const __nv_bfloat16 *>(t.data) + v, n, scale, bits);
             else
-                sum += square_sum(static_cast<const __half *>(t.data) + v, n);
+                sum += square_sum<SCALED>(static_cast<const __half *>(t.data) + v, n, scale, bits);
         }
         ++i;
         c = 0;
     }
-    sum = cta_sum(sum);
-    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+    return sum;
+}
+__device__ __noinline__ float scaled_share_sum(const ClipTable &tab, float scale) {
+    uint32_t bits = 0;
+    return share_sum<true>(tab, scale, bits);
+}
+
+// partial[blockIdx.x] = the sum of the squares of this CTA's chunks. fp32 up to the CTA's sum: the chains are
+// short (some hundred steps in a thread, ten in the tree), and the 64-bit units are few: with the
+// tree in 64 bits it took longer than the values (300 tensors, 14 MB, both kernels: 36 us).
+// Where the squares leave fp32's range the CTA reads its values again, times 2^90 or 2^-90. Below kLeast the
+// squares lost, each by half of fp32's smallest step, 2^-150, of up to 2^40 values could be 2^-20 of the sum;
+// above kMost some may have overflowed. Zeros are told from values that are lost by their bits.
+// Four CTAs an SM, as many as the grid has, leave 32 registers a thread; with three, 0.8 GB take 5% longer.
+constexpr float kLeast = 0x1p-90f, kMost = 0x1p126f;
+
+__global__ void __launch_bounds__(kClipThreads, 4) grad_square_kernel(const __grid_constant__ ClipTable tab, double *partial) {
+    __shared__ int scale_by;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    uint32_t bits = 0;
+    const float mine = share_sum<false>(tab, 1.0f, bits);
+    const bool values = __syncthreads_or(bits != 0);
+    const float sum = cta_sum(mine);
+    if (threadIdx.x == 0) {
+        partial[blockIdx.x] = sum;
+        scale_by = sum < kLeast ? values ? 1 : 0 : sum <= kMost ? 0 : -1;  // -1: also infinities and NaN
+    }
+    __syncthreads();
+    if (scale_by != 0) {
+        const float scaled = cta_sum(scaled_share_sum(tab, scale_by > 0 ? 0x1p90f : 0x1p-90f));
+        if (threadIdx.x == 0) partial[blockIdx.x] = scaled * (scale_by > 0 ? 0x1p-180 : 0x1p180);
+    }
 }
 
 // norm = sqrt of the partials' sum; out = data * min(1, max_norm / (norm + 1e-6)). Every CTA adds
 // the partials up for itself, all in the same order. A CTA takes its chunks from the last to the
 // first: the last ones are what the sum of squares read last, and so what the L2 cache still holds.
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ ClipTable tab,
-                                                                  const float *partial, int partials, float max_norm,
+                                                                  const double *partial, int partials, float max_norm,
                                                                   float *norm) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -280,7 +317,7 @@ int32_t fill_table(ClipTable &tab, const ep_grad_tensor *t, int32_t n, int32_t f
 
 size_t grad_workspace_bytes(int32_t n) {
     const size_t launches = n > 0 ? ((size_t)n + kClipTensors - 1) / kClipTensors : 1;
-    return launches * (size_t)kClipGrid * sizeof(float);
+    return launches * (size_t)kClipGrid * sizeof(double);
 }
 
 namespace {
@@ -301,7 +338,7 @@ cudaError_t launch_clip(const void *kernel, int grid, void **args, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm, float *partial,
+cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm, double *partial,
                              cudaStream_t s) {
     ClipTable tab;
     tab.n = 0;
@@ -311,7 +348,7 @@ cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, flo
         filled_from = i;
         i = fill_table(tab, t, n, i);
         if (tab.n == 0) break;
-        float *to = partial + partials;
+        double *to = partial + partials;
         void *args[] = {&tab, &to};
         const cudaError_t e = launch_clip((const void *)grad_square_kernel, tab.grid, args, s);
         if (e != cudaSuccess) return e;
@@ -326,7 +363,7 @@ cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, flo
             i = n;
         else if (n > 0)
             i = fill_table(tab, t, n, i);
-        const float *sums = partial;
+        const double *sums = partial;
         void *args[] = {&tab, &sums, &partials, &max_norm, &norm};
         const cudaError_t e = launch_clip((const void *)grad_scale_kernel, tab.n == 0 ? 1 : tab.grid, args, s);
         if (e != cudaSuccess) return e;

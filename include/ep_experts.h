@@ -206,10 +206,11 @@ ep_status ep_grad_workspace_size(int32_t n, size_t *bytes);
 
 /*
  * ep_grad_norm -- norm[0] = sqrt(sum of the squares of all values of all
- * tensors), fp32. Values are squared and added up in fp32 (one beyond 1.8e19
- * gives infinity), in short chains whose sums are joined in 64 bits, in an order
- * that depends on the sizes and on the tensors' alignment only: the result
- * repeats bit by bit, and is within 2e-5 of exact.
+ * tensors), fp32. Values are squared and added up in fp32, in short chains whose
+ * sums are joined in 64 bits, in an order that depends on the sizes and on the
+ * tensors' alignment only. Values whose squares leave fp32's range are scaled by
+ * 2^90 or 2^-90 first. The result repeats bit by bit and is within 2e-5 of
+ * exact at any size of the values, infinite where the norm itself is beyond fp32.
  *
  * tensors   : HOST array of n records (n >= 0), read during the call
  * workspace : device, 8-byte aligned, >= ep_grad_workspace_size bytes
