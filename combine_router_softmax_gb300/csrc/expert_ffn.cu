@@ -64,7 +64,8 @@ cudaError_t launch(GemmParams &p, int64_t most_tiles, cudaStream_t s) {
     cudaError_t e = expert_error_word(&p.error);
     if (e != cudaSuccess) return e;
     const size_t smem = Sh::smem_bytes(p.E);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SharedMemoryLimit limit;
+    e = limit.allow(kernel, smem);
     if (e != cudaSuccess) return e;
     const int sms = current_device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;

@@ -394,7 +394,8 @@ cudaError_t launch_stream(StreamParams &p, const void *w0, const void *w1, cudaS
     if (GATED && !make_map(&p.w[1], w1, kBytes, row, p.N, p.E, 128 / kBytes, kBoxRows)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)kStreamStages * kStreamStageBytes + kStreamRed * sizeof(float) +
                         (size_t)p.E * sizeof(StreamExpert);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SharedMemoryLimit limit;
+    e = limit.allow(kernel, smem);
     if (e != cudaSuccess) return e;
     constexpr int kOut = GATED ? kStreamRows / 2 : kStreamRows;
     const int64_t most = (int64_t)(p.E < p.S ? p.E : p.S) * ((p.N + kOut - 1) / kOut);
