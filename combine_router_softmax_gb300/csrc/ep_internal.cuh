@@ -348,9 +348,10 @@ cudaError_t launch_combine_backward(const ep_config &c, const ep_bf16 *d_out, co
 cudaError_t launch_route_backward(const ep_config &c, const float *logits, const int32_t *idx, const float *w,
                                   const float *d_w, float *d_logits, cudaStream_t s);
 
-// Gradient norm and clipping (grad_clip.cu); scale false: the norm alone.
+// Gradient norm and clipping (grad_clip.cu); scale false: the norm alone; launch_grad_scale: by a given norm.
 size_t grad_workspace_bytes(int32_t n);
 cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm,
                              double *partial, cudaStream_t s);
+cudaError_t launch_grad_scale(const ep_grad_tensor *t, int32_t n, float max_norm, const float *norm, cudaStream_t s);
 
 }  // namespace ep

@@ -41,8 +41,8 @@ ep_status check_layer(const ep_config *c, bool needs_rows) {
     return EP_OK;
 }
 
-ep_status check_grads(const ep_grad_tensor *t, int32_t n, const float *norm, const void *ws, size_t bytes, bool clip) {
-    if (n < 0 || (n > 0 && !t) || !norm || !ws || (reinterpret_cast<uintptr_t>(ws) & 7u) != 0) return EP_ERR_INVALID_ARG;
+ep_status check_grad_list(const ep_grad_tensor *t, int32_t n, const float *norm, bool clip) {
+    if (n < 0 || (n > 0 && !t) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return EP_ERR_INVALID_ARG;
     for (int32_t i = 0; i < n; ++i) {
         if (t[i].dtype != EP_F32 && t[i].dtype != EP_BF16 && t[i].dtype != EP_F16) return EP_ERR_INVALID_ARG;
         const uintptr_t size = t[i].dtype == EP_F32 ? 4 : 2;
@@ -51,6 +51,13 @@ ep_status check_grads(const ep_grad_tensor *t, int32_t n, const float *norm, con
         if (!t[i].data || reinterpret_cast<uintptr_t>(t[i].data) % size != 0) return EP_ERR_INVALID_ARG;
         if (clip && (!t[i].out || reinterpret_cast<uintptr_t>(t[i].out) % size != 0)) return EP_ERR_INVALID_ARG;
     }
+    return EP_OK;
+}
+
+ep_status check_grads(const ep_grad_tensor *t, int32_t n, const float *norm, const void *ws, size_t bytes, bool clip) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 7u) != 0) return EP_ERR_INVALID_ARG;
+    const ep_status st = check_grad_list(t, n, norm, clip);
+    if (st != EP_OK) return st;
     return bytes < ep::grad_workspace_bytes(n) ? EP_ERR_CAPACITY : EP_OK;
 }
 
@@ -168,6 +175,14 @@ ep_status ep_grad_clip(const ep_grad_tensor *tensors, int32_t n, float max_norm,
     const ep_status st = check_grads(tensors, n, norm, workspace, workspace_bytes, true);
     if (st != EP_OK) return st;
     return from_cuda(ep::launch_grad_clip(tensors, n, true, max_norm, norm, static_cast<double *>(workspace), stream));
+}
+
+ep_status ep_grad_clip_with_norm(const ep_grad_tensor *tensors, int32_t n, float max_norm, const float *norm,
+                                 cudaStream_t stream) {
+    if (!(max_norm >= 0.0f)) return EP_ERR_INVALID_ARG;
+    const ep_status st = check_grad_list(tensors, n, norm, true);
+    if (st != EP_OK) return st;
+    return from_cuda(ep::launch_grad_scale(tensors, n, max_norm, norm, stream));
 }
 
 }  // extern "C"

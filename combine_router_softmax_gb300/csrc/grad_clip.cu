@@ -233,16 +233,18 @@ __global__ void __launch_bounds__(kClipThreads, 4) grad_square_kernel(const __gr
     }
 }
 
-// norm = sqrt of the partials' sum; out = data * min(1, max_norm / (norm + 1e-6)). Every CTA adds
-// the partials up for itself, all in the same order. A CTA takes its chunks from the last to the
+// norm = sqrt of the partials' sum, or the one that is given; out = data * min(1, max_norm / (norm + 1e-6)). Every
+// CTA adds the partials up for itself, all in the same order. A CTA takes its chunks from the last to the
 // first: the last ones are what the sum of squares read last, and so what the L2 cache still holds.
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ ClipTable tab,
                                                                   const double *partial, int partials, float max_norm,
-                                                                  float *norm) {
+                                                                  float *norm, const float *given) {
     grid_dependency_wait();
     grid_launch_dependents();
     __shared__ float total_shared;
-    if (threadIdx.x < 32) {  // one warp, in 64 bits: the CTAs' sums may be many
+    if (given) {
+        if (threadIdx.x == 0) total_shared = *given;
+    } else if (threadIdx.x < 32) {  // one warp, in 64 bits: the CTAs' sums may be many
         double v = 0;
         for (int i = threadIdx.x; i < partials; i += 32) v += partial[i];
         for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
     }
     __syncthreads();
     const float total = total_shared;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    if (!given && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     if (tab.n == 0) return;
     float coef = max_norm / (total + 1e-6f);
     if (coef > 1.0f) coef = 1.0f;  // a NaN stays one
@@ -364,10 +366,26 @@ cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, flo
         else if (n > 0)
             i = fill_table(tab, t, n, i);
         const double *sums = partial;
-        void *args[] = {&tab, &sums, &partials, &max_norm, &norm};
+        const float *given = nullptr;
+        void *args[] = {&tab, &sums, &partials, &max_norm, &norm, &given};
         const cudaError_t e = launch_clip((const void *)grad_scale_kernel, tab.n == 0 ? 1 : tab.grid, args, s);
         if (e != cudaSuccess) return e;
     } while (scale && i < n);
+    return cudaSuccess;
+}
+
+cudaError_t launch_grad_scale(const ep_grad_tensor *t, int32_t n, float max_norm, const float *norm, cudaStream_t s) {
+    ClipTable tab;
+    for (int32_t i = 0; i < n;) {
+        i = fill_table(tab, t, n, i);
+        if (tab.n == 0) break;
+        const double *sums = nullptr;
+        int partials = 0;
+        float *out = nullptr;
+        void *args[] = {&tab, &sums, &partials, &max_norm, &out, &norm};
+        const cudaError_t e = launch_clip((const void *)grad_scale_kernel, tab.grid, args, s);
+        if (e != cudaSuccess) return e;
+    }
     return cudaSuccess;
 }
 

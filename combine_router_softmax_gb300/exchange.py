@@ -21,10 +21,14 @@ experts of virtual ranks [p R / P, (p + 1) R / P) -- E / P consecutive experts
    segments, which puts every output row into the source's ``y`` at the
    send-buffer row it was dispatched from; ep_combine then reduces them.
 
-Nothing here computes: the two all-to-alls move bytes only, through
+Nothing of it computes: the two all-to-alls move bytes only, through
 torch.distributed (NCCL between GPUs, gloo between CPU processes in the
 tests). The split sizes of an all-to-all-v are host integers, so step 1 ends
 with a device-to-host copy of the counts (one synchronisation per layer).
+
+Training: each process has the gradients of its own experts. Clipping goes by
+the norm of all of them: ep_grad_norm, ``reduce_grad_norm``, then
+ep_grad_clip_with_norm.
 """
 from __future__ import annotations
 
@@ -55,6 +59,15 @@ class Received:
 def _as_words(rows: torch.Tensor) -> torch.Tensor:
     """bf16 [n, H] viewed as int32 [n, H / 2]: the collective moves the bytes as they are."""
     return rows.view(torch.int32)
+
+
+def reduce_grad_norm(norm: torch.Tensor, group=None) -> torch.Tensor:
+    """norm (fp32 [1]) of each process's own gradients becomes that of all of them together, in place:
+    sqrt(sum norm^2), in 64 bits. A parameter that several processes hold must be in the norm of one of them
+    only. Nothing waits on the host with NCCL."""
+    squares = norm.double().square_()
+    dist.all_reduce(squares, group=group)
+    return norm.copy_(squares.sqrt_())
 
 
 class EpExchange:

@@ -15,7 +15,8 @@ import torch
 from . import EpConfig, _check, _device, _lib, _ptr, _stream
 
 EXPORTS = ("ep_expert_ffn", "ep_expert_ffn_backward", "ep_w4_sizes", "ep_w4_pack", "ep_w4_linear", "ep_expert_ffn_w4",
-           "ep_combine_backward", "ep_route_backward", "ep_grad_workspace_size", "ep_grad_norm", "ep_grad_clip")
+           "ep_combine_backward", "ep_route_backward", "ep_grad_workspace_size", "ep_grad_norm", "ep_grad_clip",
+           "ep_grad_clip_with_norm")
 __all__ = [*EXPORTS, "EpFfnConfig", "EpW4Config", "EpGradTensor", "GradList"]
 
 
@@ -58,6 +59,7 @@ def _declare() -> None:
     _lib.ep_grad_workspace_size.argtypes = [i32, P(size)]
     _lib.ep_grad_norm.argtypes = [grads, i32, vp, vp, size, vp]
     _lib.ep_grad_clip.argtypes = [grads, i32, ctypes.c_float, vp, vp, size, vp]
+    _lib.ep_grad_clip_with_norm.argtypes = [grads, i32, ctypes.c_float, vp, vp]
     _lib.ep_expert_ffn.argtypes = [ffn] + [vp] * 10
     _lib.ep_expert_ffn_backward.argtypes = [ffn] + [vp] * 16
     for name in EXPORTS:
@@ -239,6 +241,9 @@ class GradList:
     def clip(self, max_norm: float, norm, stream=None) -> None:
         ep_grad_clip(self, max_norm, norm, stream)
 
+    def clip_with_norm(self, max_norm: float, norm, stream=None) -> None:
+        ep_grad_clip_with_norm(self, max_norm, norm, stream)
+
 
 def ep_grad_norm(grads: GradList, norm, stream=None) -> None:
     """norm fp32 [1]: the 2-norm over all values of all tensors of the list."""
@@ -252,3 +257,10 @@ def ep_grad_clip(grads: GradList, max_norm: float, norm, stream=None) -> None:
     ws = grads.workspace
     _check(_lib.ep_grad_clip(grads.records, grads.n, float(max_norm), _ptr(norm, torch.float32, (1,), "norm"),
                              _ptr(ws, torch.uint8, None, "workspace"), ws.numel(), _stream(stream)), "ep_grad_clip")
+
+
+def ep_grad_clip_with_norm(grads: GradList, max_norm: float, norm, stream=None) -> None:
+    """Every tensor times min(1, max_norm / (norm + 1e-6)) to its ``out``, norm fp32 [1] given: that of all processes'
+    gradients, for instance (``exchange.reduce_grad_norm``)."""
+    _check(_lib.ep_grad_clip_with_norm(grads.records, grads.n, float(max_norm), _ptr(norm, torch.float32, (1,), "norm"),
+                                       _stream(stream)), "ep_grad_clip_with_norm")

@@ -223,10 +223,20 @@ ep_status ep_grad_norm(const ep_grad_tensor *tensors, int32_t n, float *norm, vo
  *   out = data min(1, max_norm / (norm + 1e-6))
  * in fp32, rounded to the tensor's type. No host synchronisation. A NaN in the
  * norm passes to every value; an infinite norm gives a factor of 0.
- * max_norm >= 0.
+ * max_norm >= 0. The norm is that of this list: where it is to span the
+ * gradients of several processes, use ep_grad_norm, join the processes' norms
+ * and call ep_grad_clip_with_norm.
  */
 ep_status ep_grad_clip(const ep_grad_tensor *tensors, int32_t n, float max_norm, float *norm, void *workspace,
                        size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * ep_grad_clip_with_norm -- ep_grad_clip's second half: the same for a norm that
+ * is given, norm[0] (const float, device, 4-byte aligned), read when the stream
+ * gets there. It may not be part of an output. No host synchronisation.
+ */
+ep_status ep_grad_clip_with_norm(const ep_grad_tensor *tensors, int32_t n, float max_norm, const float *norm,
+                                 cudaStream_t stream);
 
 #ifdef __cplusplus
 }
