@@ -12,9 +12,9 @@
 // bf16 weights run at HBM's rate (8 rows over 32 experts of 4096 / 1024 in 33 us, 5.4 TB/s with both
 // launches). 4-bit weights need more of L1: a load of activations by a warp touches eight rows, eight
 // lines for 512 bytes, and with 16 weight rows and half the k a warp they kept L1 81% busy. With twice the
-// rows they are loaded half as often: 8 rows over 64 experts of 7168 / 2048 55 -> 50 us, 512 rows of
-// 4096 / 1024 163 -> 133, of which 23 are one fragment at a time for more than 8 rows (both at once need
-// 48 registers more than the 96 a thread can have, with 18 warps on four quarters of an SM).
+// rows they are loaded half as often: 8 rows over 64 experts of 7168 / 2048 took 5 us less (52 now), 512 rows
+// of 4096 / 1024 30 us less (136 now), of which 23 are one fragment at a time for more than 8 rows (both at
+// once need 48 registers more than the 96 a thread can have, with 18 warps on four quarters of an SM).
 //
 // The product is the matrix instruction m16n8k16 with the weights as its 16 rows and 8 rows of x as
 // its columns. Which k a lane's register stands for is free as long as both operands agree, so a
@@ -24,8 +24,8 @@
 // bf16 value 128 + v by setting the bits 0x4300 over it (bf16 has 7 bits of fraction, so at 128 its
 // step is 1): one logic operation for two nibbles. What is over, 136, is taken off the values, exactly. Taken
 // off the sums, sum (128 + v) x - 136 sum x, it would save the subtraction (shifts, logic and subtraction take
-// two cycles a quarter of an SM each: 22 for a word of 8 nibbles, 14 without it) but leave the rounding of
-// 136 x behind, which an activation some hundred times the others' size makes larger than bf16's, and NaN of
+// two cycles a quarter of an SM each: 22 for a word of 8 nibbles, 14 without it; the 52 us would be 50) but
+// leave the rounding of 136 x behind, which an activation some hundred times the others' size makes larger than bf16's, and NaN of
 // an infinite one. Products with bf16 activations are exact in fp32; a group is summed in fp32 and
 // scaled as a whole.
 #pragma once

@@ -32,7 +32,8 @@ StreamParams stream_params(const ep_bf16 *s0, const ep_bf16 *s1, const ep_bf16 *
     return p;
 }
 
-// One warp packs one chunk of 128 k of one weight row; lane l holds k = 4 l .. 4 l + 3.
+// One warp packs one chunk of 128 k of one weight row; lane l holds k = 4 l .. 4 l + 3. Loads of two bytes
+// bound it: 64 x 2048 x 7168 weights, 2.4 GB in and out, in 2.1 ms = 1.1 TB/s; a model is packed once.
 __global__ void __launch_bounds__(256) w4_pack_kernel(int64_t rows, int K, int G, const __nv_bfloat16 *w, uint32_t *q,
                                                       __nv_bfloat16 *scale) {
     const int lane = threadIdx.x % 32;

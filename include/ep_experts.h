@@ -18,7 +18,8 @@
  * Bounds outside that are clamped into the buffer. expert_offset[0] need not
  * be 0: passing `expert_offset + e0`, weights from expert e0 on and a smaller E
  * runs part of the experts, one rank's for instance. Rows that no expert owns
- * are neither read nor written.
+ * are not written, and no result depends on what they hold (they may be fetched
+ * along with the rows beside them).
  */
 #ifndef EP_GB300_EXPERTS_H
 #define EP_GB300_EXPERTS_H
