@@ -123,7 +123,7 @@ const char *ep_status_string(int status) {
     }
 }
 
-int ep_version(void) { return 100; }
+int ep_version(void) { return 200; }
 
 ep_status ep_device_error(int32_t *flags) {
     if (!flags) return EP_ERR_INVALID_ARG;

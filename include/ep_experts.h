@@ -36,7 +36,8 @@ typedef struct ep_ffn_config {
     int32_t H;    /* hidden size (> 0, a multiple of 8)                                    */
     int32_t I;    /* width of the block between its projections (> 0, a multiple of 8)     */
     int32_t E;    /* experts (1 .. 1024)                                                   */
-    int32_t saved_bf16; /* g and u, kept for the backward pass: 0 IEEE halves, 1 bf16      */
+    int32_t saved_bf16; /* g and u, kept for the backward pass: 0 IEEE halves, 1 bf16
+                           (not there before ep_version 200)                             */
 } ep_ffn_config;
 
 /*
