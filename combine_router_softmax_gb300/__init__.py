@@ -605,3 +605,9 @@ from . import experts as _experts  # noqa: E402
 from .experts import *  # noqa: E402,F401,F403
 
 EXPORTS += _experts.EXPORTS
+
+# And what surrounds the layer (include/ep_layer.h).
+from . import layer as _layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+EXPORTS += _layer.EXPORTS

@@ -2,9 +2,10 @@
 //
 // Kernels live in route.cu, layout.cu, dispatch.cu, combine.cu, fused.cu,
 // gather.cu, sp.cu and tff.cu, those of the experts and of the backward pass in
-// expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu; each file exposes
-// its host launchers, declared here. The C entry points in ep_api.cu and
-// experts_api.cu validate arguments, then call the launchers.
+// expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu, those of what surrounds
+// the layer in norm.cu and balance.cu; each file exposes its host launchers, declared here.
+// The C entry points in ep_api.cu, experts_api.cu and layer_api.cu validate
+// arguments, then call the launchers.
 #pragma once
 
 #include <atomic>
@@ -15,6 +16,7 @@
 
 #include "ep.h"
 #include "ep_experts.h"
+#include "ep_layer.h"
 
 namespace ep {
 
@@ -353,5 +355,24 @@ size_t grad_workspace_bytes(int32_t n);
 cudaError_t launch_grad_clip(const ep_grad_tensor *t, int32_t n, bool scale, float max_norm, float *norm,
                              double *partial, cudaStream_t s);
 cudaError_t launch_grad_scale(const ep_grad_tensor *t, int32_t n, float max_norm, const float *norm, cudaStream_t s);
+
+// The norms around a block (norm.cu).
+size_t block_norm_workspace_bytes(const ep_norm_config &c);
+cudaError_t launch_block_norm(const ep_norm_config &c, const void *x, const ep_bf16 *y, const ep_bf16 *w_post, const void *gate,
+                              const ep_bf16 *w_next, void *out, ep_bf16 *n, float *rstd_post, float *rstd_next,
+                              cudaStream_t s);
+cudaError_t launch_block_norm_backward(const ep_norm_config &c, const void *x, const ep_bf16 *y, const ep_bf16 *w_post,
+                                       const void *gate, const ep_bf16 *w_next, const float *rstd_post,
+                                       const float *rstd_next, const void *d_out, const ep_bf16 *d_n, void *d_x, ep_bf16 *d_y,
+                                       float *d_w_post, void *d_gate, float *d_w_next, float *partial, cudaStream_t s);
+
+// The router's balance loss (balance.cu).
+size_t balance_workspace_bytes(const ep_config &c, int32_t n_seq);
+cudaError_t launch_balance(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *idx, const int32_t *seq_first,
+                           const int32_t *seq_len, int32_t *count, float *load, float *prob, float *loss, void *workspace,
+                           cudaStream_t s);
+cudaError_t launch_balance_backward(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *seq_first,
+                                    const int32_t *seq_len, const float *load, const float *d_loss, const float *d_in,
+                                    float *d_logits, cudaStream_t s);
 
 }  // namespace ep

@@ -479,4 +479,7 @@ ep_status ep_layout_static(const ep_config *cfg, const int32_t *topk_idx,
 /* The experts between dispatch and combine, and the backward pass. */
 #include "ep_experts.h"
 
+/* What surrounds the layer: norms, the balance loss, orthogonalised updates. */
+#include "ep_layer.h"
+
 #endif /* EP_GB300_H */
