@@ -3,7 +3,7 @@
 // Kernels live in route.cu, layout.cu, dispatch.cu, combine.cu, fused.cu,
 // gather.cu, sp.cu and tff.cu, those of the experts and of the backward pass in
 // expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu, those of what surrounds
-// the layer in norm.cu and balance.cu; each file exposes its host launchers, declared here.
+// the layer in norm.cu, balance.cu and ortho.cu; each file exposes its host launchers, declared here.
 // The C entry points in ep_api.cu, experts_api.cu and layer_api.cu validate
 // arguments, then call the launchers.
 #pragma once
@@ -284,6 +284,7 @@ constexpr int32_t kErrFusedWait = 2;     // a fused-dispatch CTA gave up waiting
 constexpr int32_t kErrSpWait = 4;        // a sentinel-polling CTA gave up waiting
 constexpr int32_t kErrGatherWait = 8;    // a schedule-driven dispatch CTA gave up waiting (or a bad table)
 constexpr int32_t kErrExpertWait = 16;   // an expert product's CTA gave up waiting
+constexpr int32_t kErrOrthoWait = 32;    // an orthogonalising product's CTA gave up waiting (the experts' word)
 cudaError_t dispatch_error_word(int32_t **addr);
 cudaError_t fused_error_word(int32_t **addr);
 cudaError_t sp_error_word(int32_t **addr);
@@ -374,5 +375,11 @@ cudaError_t launch_balance(const ep_config &c, int32_t n_seq, const float *logit
 cudaError_t launch_balance_backward(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *seq_first,
                                     const int32_t *seq_len, const float *load, const float *d_loss, const float *d_in,
                                     float *d_logits, cudaStream_t s);
+
+// Orthogonalised updates (ortho.cu); k: [steps][3] on the host.
+size_t ortho_workspace_bytes(const ep_ortho_config &c);
+bool ortho_fits(const float *k, int32_t steps);
+cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, void *workspace,
+                                 cudaStream_t s);
 
 }  // namespace ep

@@ -47,6 +47,18 @@ ep_status check_balance(const ep_config *c, int32_t n_seq, const int32_t *seq_fi
     return aligned(seq_first, 4) && aligned(seq_len, 4) ? EP_OK : EP_ERR_INVALID_ARG;
 }
 
+constexpr int kMaxOrthoSide = 65536, kMaxOrthoSteps = 64;
+// A quintic that lifts small singular values quickly and keeps the others near one, for every step.
+constexpr float kOrthoDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+
+ep_status check_ortho(const ep_ortho_config *c) {
+    if (!c) return EP_ERR_INVALID_ARG;
+    if (c->B < 0 || c->N <= 0 || c->K <= 0 || c->steps <= 0 || !(c->eps >= 0.0f && c->eps <= 3.4e38f)) return EP_ERR_INVALID_ARG;
+    if (c->dtype != EP_F32 && c->dtype != EP_BF16 && c->dtype != EP_F16) return EP_ERR_INVALID_ARG;
+    if (c->N > kMaxOrthoSide || c->K > kMaxOrthoSide || c->B > kMaxOrthoSide || c->steps > kMaxOrthoSteps) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -134,6 +146,28 @@ ep_status ep_balance_backward(const ep_config *cfg, int32_t n_seq, const float *
     for (const void *p : {(const void *)logits, (const void *)load, (const void *)d_loss, (const void *)d_in, (const void *)d_logits})
         if (!aligned(p, 4)) return EP_ERR_INVALID_ARG;
     return from_cuda(ep::launch_balance_backward(*cfg, n_seq, logits, seq_first, seq_len, load, d_loss, d_in, d_logits, stream));
+}
+
+ep_status ep_orthogonalize_workspace_size(const ep_ortho_config *cfg, size_t *bytes) {
+    const ep_status st = check_ortho(cfg);
+    if (st != EP_OK) return st;
+    if (!bytes) return EP_ERR_INVALID_ARG;
+    *bytes = ep::ortho_workspace_bytes(*cfg);
+    return EP_OK;
+}
+
+ep_status ep_orthogonalize(const ep_ortho_config *cfg, const float *coefficients, const void *m, ep_bf16 *out, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+    const ep_status st = check_ortho(cfg);
+    if (st != EP_OK) return st;
+    float k[3 * kMaxOrthoSteps];
+    for (int i = 0; i < 3 * cfg->steps; ++i) k[i] = coefficients ? coefficients[i] : kOrthoDefault[i % 3];
+    if (!ep::ortho_fits(k, cfg->steps)) return EP_ERR_UNSUPPORTED;
+    if (cfg->B == 0) return EP_OK;
+    if (!m || !aligned(m, cfg->dtype == EP_F32 ? 4 : 2) || !usable(out)) return EP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256)) return EP_ERR_INVALID_ARG;
+    if (workspace_bytes < ep::ortho_workspace_bytes(*cfg)) return EP_ERR_CAPACITY;
+    return from_cuda(ep::launch_orthogonalize(*cfg, k, m, out, workspace, stream));
 }
 
 }  // extern "C"

@@ -14,8 +14,8 @@ import torch
 from . import EpConfig, _check, _device, _lib, _ptr, _stream
 
 EXPORTS = ("ep_block_norm", "ep_block_norm_workspace_size", "ep_block_norm_backward", "ep_balance_workspace_size",
-           "ep_balance", "ep_balance_backward")
-__all__ = [*EXPORTS, "EpNormConfig", "EP_GATE_NONE", "EP_GATE_CHANNEL", "EP_GATE_TOKEN", "EP_GATE_ELEMENT"]
+           "ep_balance", "ep_balance_backward", "ep_orthogonalize_workspace_size", "ep_orthogonalize")
+__all__ = [*EXPORTS, "EpNormConfig", "EpOrthoConfig", "EP_GATE_NONE", "EP_GATE_CHANNEL", "EP_GATE_TOKEN", "EP_GATE_ELEMENT"]
 
 EP_GATE_NONE, EP_GATE_CHANNEL, EP_GATE_TOKEN, EP_GATE_ELEMENT = range(4)
 
@@ -31,6 +31,20 @@ class EpNormConfig(ctypes.Structure):
         return cls(T, H, gate, gate_sigmoid, residual_f32, eps, scale, weight_offset)
 
 
+_ORTHO_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class EpOrthoConfig(ctypes.Structure):
+    """``ep_ortho_config`` of include/ep_layer.h; ``dtype`` of make(): torch.float32, bfloat16 or float16."""
+    _fields_ = [*((n, ctypes.c_int32) for n in ("B", "N", "K", "dtype", "steps")), ("eps", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, *, B=1, N, K, dtype=torch.bfloat16, steps=5, eps=1e-7) -> "EpOrthoConfig":
+        if dtype not in _ORTHO_TYPES:
+            raise TypeError(f"dtype {dtype}: expected float32, bfloat16 or float16")
+        return cls(B, N, K, _ORTHO_TYPES[dtype], steps, eps)
+
+
 def _declare() -> None:
     P, vp, size = ctypes.POINTER, ctypes.c_void_p, ctypes.c_size_t
     norm = P(EpNormConfig)
@@ -41,6 +55,9 @@ def _declare() -> None:
     _lib.ep_balance_workspace_size.argtypes = [layer, i32, P(size)]
     _lib.ep_balance.argtypes = [layer, i32] + [vp] * 9 + [size, vp]
     _lib.ep_balance_backward.argtypes = [layer, i32] + [vp] * 8
+    ortho = P(EpOrthoConfig)
+    _lib.ep_orthogonalize_workspace_size.argtypes = [ortho, P(size)]
+    _lib.ep_orthogonalize.argtypes = [ortho, P(ctypes.c_float), vp, vp, vp, size, vp]
     for name in EXPORTS:
         getattr(_lib, name).restype = ctypes.c_int
 
@@ -141,3 +158,29 @@ def ep_balance_backward(cfg: EpConfig, logits, seq_first, seq_len, load, d_loss,
                                     _ptr(load, _F32, (S, E), "load", dev), _ptr(d_loss, _F32, (S, 2), "d_loss", dev),
                                     _ptr(d_in, _F32, (T, E), "d_in", dev), _ptr(d_logits, _F32, (T, E), "d_logits", dev),
                                     _stream(stream)), "ep_balance_backward")
+
+
+def ep_orthogonalize_workspace_size(cfg: EpOrthoConfig) -> int:
+    """Bytes of the workspace of ep_orthogonalize."""
+    b = ctypes.c_size_t(0)
+    _check(_lib.ep_orthogonalize_workspace_size(ctypes.byref(cfg), ctypes.byref(b)), "ep_orthogonalize_workspace_size")
+    return b.value
+
+
+def ep_orthogonalize(cfg: EpOrthoConfig, m, out, workspace, coefficients=None, stream=None) -> None:
+    """out = each matrix of m with its singular values drawn towards one, by cfg.steps Newton-Schulz steps.
+
+    m [B, N, K] (float32, bfloat16 or float16, as cfg says), out bf16 [B, N, K], may be m; coefficients: a sequence of
+    cfg.steps triples (a, b, c), None for the default."""
+    shape = (cfg.B, cfg.N, cfg.K)
+    dev = _device()
+    types = {v: t for t, v in _ORTHO_TYPES.items()}
+    k = None
+    if coefficients is not None:
+        flat = [float(v) for step in coefficients for v in step]
+        if len(flat) != 3 * cfg.steps:
+            raise ValueError(f"coefficients: {len(flat)} values, expected {cfg.steps} triples")
+        k = (ctypes.c_float * max(len(flat), 1))(*flat)
+    _check(_lib.ep_orthogonalize(ctypes.byref(cfg), k, _ptr(m, types.get(cfg.dtype, _F32), shape, "m", dev),
+                                 _ptr(out, _BF16, shape, "out", dev), *_workspace(workspace, dev), _stream(stream)),
+           "ep_orthogonalize")

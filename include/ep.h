@@ -114,6 +114,7 @@ int ep_version(void);
  *              or its chunk table named rows outside the send buffer.
  *   bit 4 (16): a CTA of an expert product (ep_experts.h) gave up waiting; its
  *              results were not all written.
+ *   bit 5 (32): the same for an orthogonalising product (ep_layer.h).
  * (ep_layout reports its own bounded wait through *n_chunks = -1.) */
 ep_status ep_device_error(int32_t *flags);
 

@@ -156,6 +156,47 @@ ep_status ep_balance_backward(const ep_config *cfg, int32_t n_seq, const float *
                               const int32_t *seq_len, const float *load, const float *d_loss, const float *d_in,
                               float *d_logits, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates
+ * ------------------------------------------------------------------------ */
+
+typedef struct ep_ortho_config {
+    int32_t B;     /* matrices (0 .. 65536)                                            */
+    int32_t N, K;  /* rows and columns of each (1 .. 65536)                            */
+    int32_t dtype; /* of m: ep_dtype                                                   */
+    int32_t steps; /* Newton-Schulz steps (1 .. 64)                                    */
+    float eps;     /* added to the norm (>= 0)                                         */
+} ep_ortho_config;
+
+/*
+ * ep_orthogonalize -- every matrix of a batch, the update of an expert's weight for
+ * instance, with its singular values drawn towards one and its singular vectors kept,
+ * by Newton-Schulz products. For each matrix M:
+ *   X = M / (|M| + eps), |M| the root of the sum of its squares
+ *   step i: A = X X^T, X = a_i X + (b_i A + c_i A A) X     (with X^T X where N > K: the
+ *   same result)
+ *   out = X
+ * The products take operands of fp16 with the known bounds of X, A and B as their
+ * scale, the parts that matter most apart in higher precision, and are summed in fp32: before
+ * it is rounded to bf16 once the result is 0.05 to 0.1% off in norm for matrices of 64 rows and
+ * columns or more, 0.2% for one of half its rank; of very few rows single roundings show (8 x 8
+ * 0.1% in the mean, 0.4% at most of 4000). |M| is right at any size of the values. A matrix of zeros gives
+ * zeros (eps > 0), a NaN or infinity makes its own matrix NaN. Results repeat bit by bit.
+ *
+ * coefficients : HOST float [steps][3] = (a, b, c) of each step, read during the call;
+ *                NULL: (3.4445, -4.7750, 2.0315) for all. EP_ERR_UNSUPPORTED where a
+ *                singular value of at most 1 could reach 4, or b u + c u^2 (u its square) 31
+ * m         : const [B, N, K] of cfg->dtype, aligned to its values
+ * out       : bf16 [B, N, K], 16-byte aligned; may be m
+ * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes (about 6 bytes a
+ *             value and 4 min(N, K)^2 a matrix)
+ * A CTA that gives up a bounded wait sets ep_device_error bit 5 (32).
+ */
+ep_status ep_orthogonalize_workspace_size(const ep_ortho_config *cfg, size_t *bytes);
+
+ep_status ep_orthogonalize(const ep_ortho_config *cfg, const float *coefficients, const void *m, ep_bf16 *out,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,216 @@
+"""ep_orthogonalize against Newton-Schulz steps in 64 bits.
+
+Two references. `rounded` does in 64 bits what the kernels do, with their roundings to halves; a kernel differs
+from it by its fp32 sums (a product of n terms is within n 2^-24 of the terms' magnitudes, a tenth of a half's rounding
+at n = 4096, so a tenth of the halves may be rounded the other way) and the last rounding to bf16: in norm at most
+2^-8 / sqrt(3) where the values are spread evenly between powers of two, 0.0023, and a tenth of the halves' 0.0015 on top.
+`exact` has no roundings; that the halves are close to it is a property of the method: `rounded` on the CPU was 0.0006 off
+at 512 x 1024, 0.0009 (at most 0.0011 of 100) at 64 x 64, 0.0009 (0.00145 of 4000) at 16 x 24. With fewer rows
+single roundings do not average out, and a nearly singular matrix of 2 x 2 magnifies them: no figure is held there."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gpu_harness import require_cuda
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+DEFAULT = [(3.4445, -4.7750, 2.0315)] * 5
+NORM_TOL = 0.0025
+
+
+@pytest.fixture(scope="module")
+def ep():
+    require_cuda()
+    import combine_router_softmax_gb300 as m
+
+    return m
+
+
+def wide(m):
+    return m.double().transpose(1, 2) if m.shape[1] > m.shape[2] else m.double()
+
+
+def exact(m, steps, eps=1e-7):
+    x = wide(m)
+    x = x / (x.square().sum((1, 2), keepdim=True).sqrt() + eps)
+    for a, b, c in steps:
+        g = x @ x.transpose(1, 2)
+        x = a * x + (b * g + c * g @ g) @ x
+    return x.transpose(1, 2) if m.shape[1] > m.shape[2] else x
+
+
+def rounded(m, steps, eps=1e-7):
+    half = lambda v, s: (v * s).to(F16).double() / s  # noqa: E731
+    x = wide(m)
+    x = x / (x.square().sum((1, 2), keepdim=True).sqrt() + eps)
+    eye = torch.eye(x.shape[1], dtype=torch.float64, device="cuda")
+    for a, b, c in steps:
+        hi = half(x, 8192.0)
+        lo = half((x - hi) * 1024, 8192.0) / 1024
+        g = hi @ hi.transpose(1, 2)
+        d = g.diagonal(dim1=1, dim2=2)
+        o = half(g * (1 - eye), 1024.0)
+        p = b * o + c * (o @ o + (d[:, :, None] + d[:, None, :]) * o) + torch.diag_embed(b * d + c * d * d)
+        e = p.diagonal(dim1=1, dim2=2)
+        p = half(p * (1 - eye), 2048.0)
+        x = (a + e)[:, :, None] * (hi + lo) + p @ hi
+    return x.transpose(1, 2) if m.shape[1] > m.shape[2] else x
+
+
+def run(ep, m, steps=None, eps=1e-7, out=None):
+    cfg = ep.EpOrthoConfig.make(B=m.shape[0], N=m.shape[1], K=m.shape[2], dtype=m.dtype, steps=5 if steps is None else len(steps), eps=eps)
+    out = torch.full(m.shape, float("nan"), dtype=BF16, device="cuda") if out is None else out
+    ws = torch.full((ep.ep_orthogonalize_workspace_size(cfg),), 255, dtype=torch.uint8, device="cuda")  # NaN, all of it
+    ep.ep_orthogonalize(cfg, m, out, ws, coefficients=steps)
+    assert ep.ep_device_error() == 0
+    return out
+
+
+def check(got, m, steps=None, eps=1e-7, close=None, most=2.0**-8):
+    """`close`: how far the halves may be from exact, in norm; `most`: a value from the rounded steps', of the matrix' rms."""
+    steps = DEFAULT if steps is None else steps
+    few = min(m.shape[1:])
+    close = close or (0.001 if few >= 128 else 0.0016 if few >= 16 else None)
+    r, e = rounded(m, steps, eps), exact(m, steps, eps)
+    for i in range(m.shape[0]):
+        g = got[i].double()
+        assert torch.isfinite(g).all(), i
+        norm = r[i].norm()
+        assert (g - r[i]).norm() <= NORM_TOL * norm, f"matrix {i}: {((g - r[i]).norm() / norm).item():g} off the rounded steps"
+        rms = norm / r[i].numel() ** 0.5
+        assert ((g - r[i]).abs() <= 2.0**-8 * r[i].abs() + most * rms).all(), i
+        assert close is None or (r[i] - e[i]).norm() <= close * e[i].norm(), f"matrix {i}: the halves are {((r[i] - e[i]).norm() / e[i].norm()).item():g} off"
+
+
+def normal(B, N, K, seed=0, dtype=BF16):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn((B, N, K), generator=gen, device="cuda") * 0.01).to(dtype)
+
+
+# one value, rows and columns alone, ragged, a tile and one more, several tiles, wide and tall
+@pytest.mark.parametrize("B,N,K", [(1, 1, 1), (4, 1, 37), (3, 41, 1), (3, 5, 3), (2, 8, 8), (2, 100, 130), (1, 128, 256),
+                                   (5, 129, 130), (3, 300, 77), (1, 64, 4000), (70, 96, 40), (1, 513, 520), (1, 1000, 130),
+                                   (2, 640, 1303)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_against_64_bits(ep, B, N, K, dtype):
+    m = normal(B, N, K, seed=N + K, dtype=dtype)
+    check(run(ep, m), m)
+
+
+@pytest.mark.parametrize("B,N,K", [(6, 1100, 1200), (6, 1289, 1100), (12, 600, 2000)])
+def test_pairs(ep, B, N, K):
+    """As many tiles as CTA pairs take: two CTAs a tile, ragged in both directions, and several tiles a pair."""
+    m = normal(B, N, K, seed=1)
+    check(run(ep, m), m)
+
+
+def test_uneven_singular_values(ep):
+    """Falling as 1/i and as i^-1.5, of half the rank, channels of different size, a large mean.
+
+    Where M has half its rank, what grows in the other half is the halves' roundings alone: `rounded`, in which the
+    kernels have no part, is 0.00166 off exact here (0.0013 at 512 x 1024), so 0.002 is the figure that is given
+    for such matrices (`close`). A sum that differs in its last bit makes other roundings of them: two independent ones
+    differ by sqrt(2) 0.002 of the rms, and of the 98304 values the largest difference is within 5.5 times that, 0.0156
+    (a normal value exceeds 5.5 once in 26 million)."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.float64)  # noqa: E731
+    N, K = 256, 384
+    u, v = torch.linalg.qr(n(N, N))[0], torch.linalg.qr(n(K, N))[0]
+    i = torch.arange(1, N + 1, device="cuda", dtype=torch.float64)
+    m = torch.stack([(u / i) @ v.T, (u * i**-1.5) @ v.T, n(N, N // 2) @ n(N // 2, K), n(N, K) * torch.exp(n(1, K)),
+                     n(N, K) + 3 * n(N, 1) @ n(1, K)]).to(F32)
+    check(run(ep, m), m, close=0.002, most=0.0156)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e12, 1e30])
+@pytest.mark.parametrize("N,K", [(70, 200), (200, 70)])
+def test_any_size_of_the_values(ep, scale, N, K):
+    m = (normal(2, N, K, seed=3, dtype=F32) * scale)
+    check(run(ep, m, eps=0.0), m, eps=0.0)
+
+
+def test_sum_of_squares_beyond_the_range(ep):
+    """The norm itself near the largest float."""
+    m = torch.full((1, 4, 6), 1e38, device="cuda")
+    m[0, 1:, ::2] *= -1
+    m[0, 2:, 1] = 0
+    check(run(ep, m), m)
+
+
+def test_zeros_and_what_is_not_finite(ep):
+    m = normal(5, 90, 140, seed=4)
+    want = run(ep, m)
+    m[1] = 0
+    m[2, 3, 4] = float("nan")
+    m[3, 89, 139] = float("inf")
+    got = run(ep, m)
+    assert (got[1] == 0).all() and torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[4], want[4])
+
+
+@pytest.mark.parametrize("steps", [[(1.5, -0.5, 0.0)], [(1.5, -0.5, 0.0)] * 12, [(3.4445, -4.7750, 2.0315)] * 3 + [(1.875, -1.25, 0.375)] * 2,
+                                   [(2.0, 0.0, 0.0)], [(0.0, 0.0, 1.0)]])
+def test_other_coefficients(ep, steps):
+    m = normal(2, 150, 130, seed=5)
+    check(run(ep, m, steps), m, steps, close=0.0015)
+
+
+def test_orthogonal(ep):
+    """What it is for: singular values near one. The default's lie within 0.66 and 1.21 once they have come that far,
+    here from 1e-2 of the norm on; bf16 moves them by less than 2^-8 of the largest times sqrt(2)."""
+    m = normal(1, 200, 800, seed=6, dtype=F32)
+    s = torch.linalg.svdvals(run(ep, m)[0].double())
+    assert 0.65 < s.min() and s.max() < 1.23
+
+
+def test_unaligned_input_and_in_place(ep):
+    for N, K in ((64, 72), (33, 57), (130, 40)):
+        for dtype in (BF16, F32):
+            flat = torch.empty(2 * N * K + 3, dtype=dtype, device="cuda")
+            m = flat[3:].view(2, N, K)
+            m.copy_(normal(2, N, K, seed=7, dtype=dtype))
+            assert torch.equal(run(ep, m), run(ep, m.clone()))
+        m = normal(2, N, K, seed=8)
+        want = run(ep, m)
+        run(ep, m, out=m)
+        assert torch.equal(m, want)
+
+
+def test_repeats_and_batches(ep):
+    """Bit by bit, whatever other matrices are in the batch."""
+    m = normal(40, 256, 300, seed=9)
+    want = run(ep, m)
+    assert torch.equal(run(ep, m), want)
+    one = run(ep, m[7:8].contiguous())
+    assert (one[0].double() - want[7].double()).abs().max() <= 2.0**-7 * want[7].abs().max().double()
+
+
+def test_no_matrices(ep):
+    run(ep, normal(0, 8, 8))
+
+
+def test_captured_and_two_streams(ep):
+    """In a graph on new values, while another call with its own workspace runs beside it."""
+    m, other = normal(3, 200, 500, seed=10), normal(3, 300, 310, seed=11)
+    want_other = run(ep, other)
+    cfg = ep.EpOrthoConfig.make(B=3, N=200, K=500)
+    cfg2 = ep.EpOrthoConfig.make(B=3, N=300, K=310)
+    ws, ws2 = (torch.empty((ep.ep_orthogonalize_workspace_size(c),), dtype=torch.uint8, device="cuda") for c in (cfg, cfg2))
+    out, out2 = torch.empty_like(m), torch.empty_like(other)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ep.ep_orthogonalize(cfg, m, out, ws)
+    new = normal(3, 200, 500, seed=12)
+    want = run(ep, new)
+    m.copy_(new)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        g.replay()
+        ep.ep_orthogonalize(cfg2, other, out2, ws2, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(out2, want_other)
+    assert ep.ep_device_error() == 0

@@ -181,3 +181,72 @@ def test_balance_binding_checks_tensors(ep):
         ep.ep_balance(cfg, l, idx, None, None, c, f, f, torch.zeros((1, 2)), None)  # on the CPU
     with pytest.raises(TypeError):
         ep.ep_balance(cfg, l.double(), idx, None, None, c, f, f, torch.zeros((1, 2)), None)
+
+
+# Orthogonalised updates --------------------------------------------------------
+
+def ortho_cfg(ep, **kw):
+    base = dict(B=2, N=16, K=24, dtype=1, steps=5, eps=1e-7)
+    base.update(kw)
+    return ep.EpOrthoConfig(*(base[k] for k in ("B", "N", "K", "dtype", "steps", "eps")))
+
+
+def ortho(ep, cfg, k=None, m=F, out=F, ws=F, nbytes=BIG):
+    return ep._lib.ep_orthogonalize(None if cfg is None else ctypes.byref(cfg), k, m, out, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("bad,expect", [
+    (dict(B=-1), "INVALID"), (dict(N=0), "INVALID"), (dict(K=-3), "INVALID"), (dict(dtype=3), "INVALID"), (dict(dtype=-1), "INVALID"),
+    (dict(steps=0), "INVALID"), (dict(eps=-1.0), "INVALID"), (dict(eps=float("nan")), "INVALID"), (dict(eps=float("inf")), "INVALID"),
+    (dict(N=65537), "UNSUPPORTED"), (dict(K=65537), "UNSUPPORTED"), (dict(B=65537), "UNSUPPORTED"), (dict(steps=65), "UNSUPPORTED"),
+])
+def test_ortho_shapes(ep, bad, expect):
+    want = expected(ep, expect)
+    cfg = ortho_cfg(ep, **bad)
+    assert ortho(ep, cfg) == want
+    assert ep._lib.ep_orthogonalize_workspace_size(ctypes.byref(cfg), ctypes.byref(ctypes.c_size_t(0))) == want
+
+
+def test_ortho_pointers(ep):
+    bad, cfg = ep.EP_ERR_INVALID_ARG, ortho_cfg(ep)
+    assert ortho(ep, None) == bad
+    assert ep._lib.ep_orthogonalize_workspace_size(ctypes.byref(cfg), None) == bad
+    for k in ("m", "out", "ws"):
+        assert ortho(ep, cfg, **{k: None}) == bad, k
+    assert ortho(ep, cfg, m=ctypes.c_void_p(0x10001)) == bad and ortho(ep, ortho_cfg(ep, dtype=0), m=ODD2) == bad
+    assert ortho(ep, cfg, out=ODD8) == bad and ortho(ep, cfg, ws=ctypes.c_void_p(0x10080)) == bad
+    assert ortho(ep, cfg, nbytes=ep.ep_orthogonalize_workspace_size(cfg) - 1) == ep.EP_ERR_CAPACITY
+    assert ortho(ep, ortho_cfg(ep, B=0), m=None, out=None, ws=None, nbytes=0) == ep.EP_OK
+
+
+@pytest.mark.parametrize("k,fits", [
+    ((3.4445, -4.7750, 2.0315), True), ((1.5, -0.5, 0.0), True), ((3.9, 0.0, 0.0), True), ((4.1, 0.0, 0.0), False),
+    ((1.0, 31.5, -31.5), False), ((1.0, -32.0, 0.5), False), ((float("nan"), 0.0, 0.0), False), ((1.0, float("inf"), 0.0), False),
+    ((0.0, 8.0, -8.0), True), ((3.0, 3.0, 3.0), False),
+])
+def test_ortho_coefficients(ep, k, fits):
+    """Refused where X or B could leave the halves' range: |X| < 4, |b u + c u^2| < 31 for u up to X's square.
+    s + 31.5 s^3 (1 - s^2) is 6.6 at s = 0.78; 8 s^3 (1 - s^2) is 1.5 there."""
+    want = ep.EP_OK if fits else ep.EP_ERR_UNSUPPORTED
+    cfg = ortho_cfg(ep, B=0, steps=1)  # nothing is enqueued
+    assert ortho(ep, cfg, (ctypes.c_float * 3)(*k)) == want
+
+
+def test_ortho_coefficients_step_by_step(ep):
+    """1.9 a step: 1.9, 3.6, 6.9."""
+    for steps, want in ((2, ep.EP_OK), (3, ep.EP_ERR_UNSUPPORTED)):
+        k = (ctypes.c_float * (3 * steps))(*([1.9, 0.0, 0.0] * steps))
+        assert ortho(ep, ortho_cfg(ep, B=0, steps=steps), k) == want
+
+
+def test_ortho_binding_checks_tensors(ep):
+    cfg = ep.EpOrthoConfig.make(B=1, N=8, K=8)
+    m = torch.zeros((1, 8, 8), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ep.ep_orthogonalize(cfg, m, m, None)  # on the CPU
+    with pytest.raises(TypeError):
+        ep.ep_orthogonalize(cfg, m.float(), m, None)
+    with pytest.raises(ValueError):
+        ep.ep_orthogonalize(cfg, m, m, None, coefficients=[(1.0, 0.0, 0.0)])  # one step of five
+    with pytest.raises(TypeError):
+        ep.EpOrthoConfig.make(N=8, K=8, dtype=torch.float64)
