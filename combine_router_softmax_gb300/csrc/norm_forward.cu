@@ -1,0 +1,191 @@
+// norm_forward.cu -- the norms around a block, forward (the kernels' frame: norm_rows.cuh).
+#include "norm_rows.cuh"
+
+namespace ep {
+
+namespace {
+
+template <bool F32, int FORM, bool WARP, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ? 3 : 1) block_norm_kernel(const NormArgs p, int stages) {
+    constexpr bool kY = FORM & kFormY, kPost = FORM & kFormPost, kGate = FORM & kFormGate, kKept = kept_factors(THREADS);
+    __shared__ Scratch scratch;
+    extern __shared__ uint4 ring_smem[];
+    clear_scratch<WARP>(scratch);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const Place<WARP> at;
+    const bool next = p.n != nullptr, element = kGate && p.kind == EP_GATE_ELEMENT, token = kY && !kGate && p.kind == EP_GATE_TOKEN;
+    const bool factors = kPost || (kGate && !element);
+    const Ring<F32, NV> ring(ring_smem, stages, kY, element, false, false);
+    const auto ask = [&](int64_t t, uint32_t stage) {
+        if (t < p.T) {
+            const size_t row = (size_t)t * p.vecs + at.first;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * at.stride + at.first >= p.vecs) continue;
+                ring.copy_stream(stage, 0, i, p.x, row + i * at.stride);
+                if constexpr (kY) ring.copy(stage, ring.y(), i, p.y, row + i * at.stride);
+                if (kGate && element) ring.copy(stage, ring.gate, i, p.gate, row + i * at.stride);
+            }
+        }
+        copies_commit();
+    };
+    for (int s = 0; s < stages; ++s) ask((int64_t)at.row + (int64_t)s * at.step, ring.stage(s));
+    if (kKept && factors) ring.template keep_factors<kPost, kGate>(p, at.first, at.stride);
+    int s = 0, turn = 0;
+    float token_gate = token && at.row < p.T ? static_cast<const float *>(p.gate)[at.row] : 1.0f, slope;
+    for (int64_t t = at.row; t < p.T; t += at.step) {
+        const size_t row = (size_t)t * p.vecs + at.first;
+        const uint32_t stage = ring.stage(s);
+        const float scale = token ? p.scale * gate_act(token_gate, p.sigmoid, slope) : p.scale;
+        if (token && t + at.step < p.T) token_gate = static_cast<const float *>(p.gate)[t + at.step];
+        copies_wait(stages - 1);
+        float r_y = 1.0f;
+        if constexpr (kPost) {
+            uint64_t squares = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * at.stride + at.first >= p.vecs) continue;
+                const V8 v = unpack8(ring.get(stage, ring.y(), i));
+                dot(squares, v, v);
+            }
+            r_y = rsqrtf(fmaf(group_sum<WARP>(total(squares), scratch, turn), p.inv_h, p.eps));
+            if (p.rstd_post && at.first == 0) p.rstd_post[t] = r_y;
+        }
+        V8 out[NV];
+        uint64_t squares = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * at.stride + at.first;
+            if (v >= p.vecs) continue;
+            out[i] = ring.get_stream(stage, 0, i);
+            if constexpr (kY) {
+                V8 z = unpack8(ring.get(stage, ring.y(), i));
+                if constexpr (kPost) times(z, r_y);
+                if (factors) times(z, ring.template get_factors<kKept, kPost, kGate>(p, i, v));
+                if (kGate && element) {
+                    V8 a = unpack8(ring.get(stage, ring.gate, i));
+                    gate_act(a, p.sigmoid);
+                    times(z, a);
+                }
+                add_scaled(out[i], scale, z);
+                Stream8<F32>::store(p.out, row + i * at.stride, out[i]);
+            }
+            dot(squares, out[i], out[i]);
+        }
+        ask(t + (int64_t)stages * at.step, stage);
+        s = s + 1 == stages ? 0 : s + 1;
+        if (!next) continue;
+        const float r = rsqrtf(fmaf(group_sum<WARP>(total(squares), scratch, turn), p.inv_h, p.eps));
+        if (p.rstd_next && at.first == 0) p.rstd_next[t] = r;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * at.stride + at.first;
+            if (v >= p.vecs) continue;
+            times(out[i], r);
+            weigh(out[i], __ldg(p.w_next + v), p.offset);  // weights come from L1: in registers they push others out
+            st_v4(p.n + row + i * at.stride, pack8(out[i]));
+        }
+    }
+}
+
+// Few rows: a CTA takes one, a thread one or two vectors of it, everything asked for at once.
+template <bool F32, int NV>
+__global__ void __launch_bounds__(1024) block_norm_few_kernel(const NormArgs p) {
+    __shared__ Scratch scratch;
+    clear_scratch<false>(scratch);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    int turn = 0;
+    const Place<false> at;
+    const int t = at.row;
+    const size_t row = (size_t)t * p.vecs;
+    Stream8<F32> x[NV];
+    uint4 y[NV], wp[NV], wn[NV], g[NV];
+    const bool has_y = p.y != nullptr, post = p.w_post != nullptr, next = p.n != nullptr;
+    const float token_gate = p.kind == EP_GATE_TOKEN ? static_cast<const float *>(p.gate)[t] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * at.stride + at.first;
+        const bool in = v < p.vecs;
+        x[i].clear();
+        y[i] = wp[i] = wn[i] = g[i] = make_uint4(0, 0, 0, 0);
+        if (!in) continue;
+        x[i].load(p.x, row + v);
+        if (has_y) y[i] = p.y[row + v];
+        if (post) wp[i] = p.w_post[v];
+        if (next) wn[i] = p.w_next[v];
+        if (p.kind == EP_GATE_CHANNEL) g[i] = static_cast<const uint4 *>(p.gate)[v];
+        if (p.kind == EP_GATE_ELEMENT) g[i] = static_cast<const uint4 *>(p.gate)[row + v];
+    }
+    float r_y = 1.0f;
+    if (post) {
+        uint64_t squares = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const V8 v = unpack8(y[i]);
+            dot(squares, v, v);
+        }
+        r_y = rsqrtf(fmaf(group_sum<false>(total(squares), scratch, turn), p.inv_h, p.eps));
+        if (p.rstd_post && at.first == 0) p.rstd_post[t] = r_y;
+    }
+    V8 out[NV];
+    uint64_t squares = 0;
+    float slope;
+    const float scale = p.kind == EP_GATE_TOKEN ? p.scale * gate_act(token_gate, p.sigmoid, slope) : p.scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * at.stride + at.first;
+        if (v >= p.vecs) continue;
+        out[i] = x[i].get();
+        if (has_y) {
+            V8 z = unpack8(y[i]);
+            if (post) {
+                times(z, r_y);
+                weigh(z, wp[i], p.offset);
+            }
+            if (p.kind == EP_GATE_CHANNEL || p.kind == EP_GATE_ELEMENT) {
+                V8 a = unpack8(g[i]);
+                gate_act(a, p.sigmoid);
+                times(z, a);
+            }
+            add_scaled(out[i], scale, z);
+            Stream8<F32>::store(p.out, row + v, out[i]);
+        }
+        dot(squares, out[i], out[i]);
+    }
+    if (!next) return;
+    const float r = rsqrtf(fmaf(group_sum<false>(total(squares), scratch, turn), p.inv_h, p.eps));
+    if (p.rstd_next && at.first == 0) p.rstd_next[t] = r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * at.stride + at.first;
+        if (v >= p.vecs) continue;
+        times(out[i], r);
+        weigh(out[i], wn[i], p.offset);
+        st_v4(p.n + row + v, pack8(out[i]));
+    }
+}
+
+struct Forward {
+    template <bool F32, int FORM, bool WARP, int NV, int THREADS>
+    static auto kernel() {
+        return block_norm_kernel<F32, FORM, WARP, NV, THREADS>;
+    }
+};
+
+template <bool F32>
+cudaError_t forward(const NormArgs &p, cudaStream_t s) {
+    // a CTA for every row, as long as each has an SM to itself
+    int ctas;
+    if (p.T > current_device_sm_count() || p.vecs <= 32) return run_any<Forward, F32>(p, false, false, false, INT32_MAX, &ctas, s);
+    if (p.vecs <= 1024)
+        return launch_dependent(block_norm_few_kernel<F32, 1>, dim3((unsigned)p.T), dim3((unsigned)((p.vecs + 31) / 32 * 32)), 0, s, p);
+    return launch_dependent(block_norm_few_kernel<F32, 2>, dim3((unsigned)p.T), dim3((unsigned)((p.vecs + 63) / 64 * 32)), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_forward(const NormArgs &p, bool f32, cudaStream_t s) { return f32 ? forward<true>(p, s) : forward<false>(p, s); }
+
+}  // namespace ep

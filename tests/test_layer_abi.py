@@ -109,7 +109,7 @@ def test_norm_without_rows_needs_nothing(ep):
 def test_norm_workspace(ep):
     for T, H in ((0, 8), (1, 64), (100, 7168), (100000, 16384)):
         n = ep.ep_block_norm_workspace_size(norm_cfg(ep, T=T, H=H))
-        assert 0 <= n <= 2 * 4 * H * min(T, 304) and (n > 0) == (T > 0)
+        assert 0 <= n <= 2 * 4 * H * min(T, 1216) and (n > 0) == (T > 0)
 
 
 def test_norm_binding_checks_tensors(ep):
