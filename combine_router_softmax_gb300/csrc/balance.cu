@@ -1,18 +1,24 @@
 // balance.cu -- the router's balance loss, the squared log-sum-exp loss, per-expert counts, and their gradient.
 //
-// Every row's softmax is a warp's: the logits are read once, a lane holds every 32nd. The sums over a
+// Every row's softmax is 2 to 32 lanes': the logits are read once, each lane holding some. The sums over a
 // sequence's rows are formed in registers, joined in shared memory, and left as one row of partial sums for
 // every pair of a tile of rows and a sequence that meet; a second kernel adds those up. Tile i and sequence s
-// write row i + s: as both only grow along the rows, no two pairs share one.
-#include "ep_internal.cuh"
+// write row i + s: as both only grow along the rows, no two pairs share one. The gradient computes the softmax again.
+//
+// HBM bounds both at many rows, the launches and a chain of dependent loads at few: forward 128 rows 5.3 us, 32768 x
+// 256 15.3 (of which joining the partial sums 5; 5.1 for its bytes at the copy rate), 131072 x 128 in 64 sequences 23.6
+// (10.5); backward 1.9, 18.1 (14.8), 25.4 (19.8).
+#include "pairs.cuh"
+#include "tcgen05.cuh"  // clusters
 
 namespace ep {
 
 namespace {
 
-constexpr int kBalWarps = 8;
+constexpr int kBalWarps = 8;  // of a CTA of the backward pass
 constexpr int kBalThreads = 32 * kBalWarps;
-constexpr int kFinishThreads = 1024;
+constexpr int kSumThreads = 384;      // of a large CTA of the forward pass: two an SM with 80 registers
+constexpr int kFinishThreads = 1024;  // at most
 
 struct Sequences {
     const int32_t *first, *len;
@@ -24,10 +30,26 @@ struct Sequences {
         const int e = max(min(max(first[s + 1], 0), T), b);
         return len ? (int)min((int64_t)e, (int64_t)b + max(len[s], 0)) : e;
     }
-    // The last sequence that begins at or before `row`; -1: none.
+    // The last sequence that begins at or before `row`, if it is one's (its bounds are asked then); -1: none. By a warp: every lane looks at one of 32 places
+    // at a time, as a search by halves is a chain of twice to five times as many loads.
     __device__ __forceinline__ int find(int row) const {
-        if (!first) return 0;
+        if (!first || n == 1) return 0;  // its bounds say the rest
         int lo = 0, hi = n;  // the first that begins after it lies in [lo, hi]
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32;
+            const int64_t at = lo + (int64_t)(threadIdx.x % 32) * step;
+            const int c = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && begin((int)at) <= row));
+            if (c == 0) break;
+            const int next = lo + (c - 1) * step + 1;
+            hi = (int)min((int64_t)hi, lo + (int64_t)c * step);
+            lo = next;
+        }
+        return lo - 1;
+    }
+    // The same by each lane for itself.
+    __device__ __forceinline__ int find_alone(int row) const {
+        if (!first || n == 1) return 0;
+        int lo = 0, hi = n;
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
             if (begin(mid) <= row)
@@ -49,45 +71,94 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-    return v;
-}
 
-template <int VPL>
-__device__ __forceinline__ void load_row(const float *l, int E, int lane, float (&p)[VPL]) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = i * 32 + lane < E ? l[i * 32 + lane] : -INFINITY;
-}
-// The softmax of a row in place; the log of the sum of exponentials. All zero where nothing is above -infinity.
-template <int VPL>
-__device__ __forceinline__ float softmax_row(float (&p)[VPL]) {
-    float top = p[0], sum = 0.0f;
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) top = fmaxf(top, p[i]);
-    top = warp_max(top);
-    const float base = top == -INFINITY ? 0.0f : top;  // exp(-inf - 0) = 0
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        p[i] = __expf(p[i] - base);
-        sum += p[i];
+// A row of logits over L lanes, NQ times four to a lane, so that a warp takes 32 / L rows together: what the
+// instructions are that a row takes whatever its length (shuffles, a logarithm, a quotient) is shared by them
+// (131072 rows of 128: 34 us by whole warps, which issue 120 instructions a row, 20 by 8 lanes). WIDE: rows begin on
+// 16-byte boundaries, and the four are neighbours; else they lie L apart, so that lanes read neighbours.
+template <int L, int NQ, bool WIDE>
+struct Row {
+    static constexpr int kRows = 32 / L;
+    uint64_t v[2 * NQ];  // pairs
+    static __device__ __forceinline__ int element(int i, int j) {
+        const int lane = threadIdx.x % L;
+        return WIDE ? (i * L + lane) * 4 + j : (i * 4 + j) * L + lane;
     }
-    sum = warp_sum(sum);
-    if (sum == 0.0f) return 0.0f;
-    const float inv = 1.0f / sum;
+    // The row at p; `none` where it has no element, and throughout unless `in` (p is a row all the same): behind a branch
+    // for each of them the loads would not go out together.
+    __device__ __forceinline__ void load(const float *p, int E, bool in, float none) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] *= inv;
-    return base + logf(sum);
+        for (int i = 0; i < NQ; ++i) {
+            if constexpr (WIDE) {
+                const int e = element(i, 0);
+                const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p + min(e, E - 4));
+                const bool there = in && e < E;
+                v[2 * i] = there ? q.x : pair(none, none);
+                v[2 * i + 1] = there ? q.y : pair(none, none);
+            } else {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = p[min(element(i, j), E - 1)];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = in && element(i, j) < E ? x[j] : none;
+                v[2 * i] = pair(x[0], x[1]), v[2 * i + 1] = pair(x[2], x[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 2 * NQ; ++i) v[i] = 0;
+    }
+    __device__ __forceinline__ void store(float *p, int E) const {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            if constexpr (WIDE) {
+                if (element(i, 0) < E) *reinterpret_cast<ulonglong2 *>(p + element(i, 0)) = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+            } else {
+                const float x[4] = {low(v[2 * i]), high(v[2 * i]), low(v[2 * i + 1]), high(v[2 * i + 1])};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (element(i, j) < E) p[element(i, j)] = x[j];
+            }
+        }
+    }
+};
+// exp2 of what is at most 0; results below fp32's normal range count as 0.
+__device__ __forceinline__ float exp2_flushed(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// exp(l - top) in place, top the row's largest value, and their sum, this lane's part.
+template <int L, int NQ, bool WIDE>
+__device__ __forceinline__ float exponentials(Row<L, NQ, WIDE> &r, float &top) {
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2 * NQ; ++i) top = fmaxf(top, fmaxf(low(r.v[i]), high(r.v[i])));
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    top = top == -INFINITY ? 0.0f : top;  // exp(-inf - 0) = 0
+    const uint64_t base = pair(-top, -top), log2e = pair(1.44269504f, 1.44269504f);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * NQ; ++i) {
+        // the difference first: it is exact near the top, where the large terms are
+        const uint64_t x = mul2(add2(r.v[i], base), log2e);
+        r.v[i] = pair(exp2_flushed(low(x)), exp2_flushed(high(x)));
+        sum = add2(sum, r.v[i]);
+    }
+    return total(sum);
 }
 
-template <int VPL>
-__global__ void __launch_bounds__(kBalThreads) balance_kernel(Sequences seq, int E, int k, int tile_rows, const float *logits,
-                                                              const int32_t *idx, Partials part) {
-    extern __shared__ unsigned char smem[];
-    float *sums = reinterpret_cast<float *>(smem);                  // [warp][E]
-    int32_t *count = reinterpret_cast<int32_t *>(sums + kBalWarps * E);  // [E]
-    __shared__ float z_sums[kBalWarps];
+template <int L, int NQ, bool WIDE>
+__global__ void __launch_bounds__(kSumThreads, NQ <= 4 ? 2 : 1) balance_kernel(Sequences seq, int E, int k, int tile_rows, const float *logits,
+                                                                      const int32_t *idx, Partials part) {
+    using R = Row<L, NQ, WIDE>;
+    extern __shared__ float smem[];
+    const int threads = blockDim.x, warps = threads / 32;
+    float *sums = smem;                                                // [warp][E]
+    int32_t *count = reinterpret_cast<int32_t *>(sums + warps * E);  // [E]
+    __shared__ float z_sums[32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -97,73 +168,105 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(Sequences seq, int
         if (seq.begin(s) >= end) break;
         const int lo = max(seq.begin(s), begin), hi = min(seq.end(s), end);
         if (lo >= hi) continue;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) count[e] = 0;
+        const int step = warps * R::kRows;
+        int64_t t = lo + warp * R::kRows + lane / L;  // this lane's rows; the next one is asked for ahead
+        R next;
+        const auto ask = [&](int64_t t) { next.load(logits + (size_t)min(t, (int64_t)hi - 1) * E, E, t < hi, -INFINITY); };
+        ask(t);
+        for (int e = threadIdx.x; e < E; e += threads) count[e] = 0;
         __syncthreads();
-        for (int64_t i = (int64_t)lo * k + threadIdx.x; i < (int64_t)hi * k; i += kBalThreads) {
-            const int e = idx[i];
-            if (e >= 0 && e < E) atomicAdd(&count[e], 1);
-        }
-        float acc[VPL], z = 0.0f;
+        for (int64_t i = (int64_t)lo * k + threadIdx.x; i < (int64_t)hi * k; i += 8 * threads) {
+            int e[8];  // asked for together
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
-        for (int64_t t = lo + warp; t < hi; t += kBalWarps) {
-            float p[VPL];
-            load_row(logits + (size_t)t * E, E, lane, p);
-            const float lse = softmax_row(p);
+            for (int j = 0; j < 8; ++j) e[j] = i + j * threads < (int64_t)hi * k ? idx[i + j * threads] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e[j] >= 0 && e[j] < E) atomicAdd(&count[e[j]], 1);
+        }
+        R acc;
+        float z = 0.0f;
+        acc.clear();
+        for (; t - lane / L < hi; t += step) {  // all lanes alike
+            R r = next;
+            ask(t + step);
+            float top, sum = exponentials(r, top);
+#pragma unroll
+            for (int d = L / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);  // 0: no row
+            const float lse = sum == 0.0f ? 0.0f : top + __logf(sum);
             z = fmaf(lse, lse, z);
+            const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) acc[i] += p[i];
+            for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = fma2(r.v[i], inv2, acc.v[i]);
         }
+        // over the warp's rows, then over the warps
+        z = lane % L == 0 ? z : 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (i * 32 + lane < E) sums[warp * E + i * 32 + lane] = acc[i];
+        for (int d = 16; d >= L; d /= 2) {
+            z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
+#pragma unroll
+            for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = add2(acc.v[i], __shfl_xor_sync(0xFFFFFFFFu, acc.v[i], d));
+        }
+        if (lane < L) acc.store(sums + warp * E, E);
         if (lane == 0) z_sums[warp] = z;
         __syncthreads();
         const size_t row = (size_t)blockIdx.x + s;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) {
+        for (int e = threadIdx.x; e < E; e += threads) {
             float v = 0.0f;
-            for (int w = 0; w < kBalWarps; ++w) v += sums[w * E + e];
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) v += sums[w * E + e];
             part.prob[row * E + e] = v;
             part.count[row * E + e] = count[e];
         }
         if (threadIdx.x == 0) {
             float v = 0.0f;
-            for (int w = 0; w < kBalWarps; ++w) v += z_sums[w];
+            for (int w = 0; w < warps; ++w) v += z_sums[w];
             part.z[row] = v;
         }
         __syncthreads();
     }
 }
 
-// One CTA a sequence.
-__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(Sequences seq, int E, int k, int tile_rows, Partials part,
+// A cluster of CTAs a sequence, each of which adds up a part of the columns; the first one joins the losses.
+// (One CTA for 256 columns of 304 partial rows took 28 us.)
+__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(Sequences seq, int E, int k, int tile_rows, int ctas, Partials part,
                                                                         int32_t *count, float *load, float *prob, float *loss) {
-    __shared__ float sums[kFinishThreads], inner[32];
+    __shared__ float sums[kFinishThreads], inner[32], z_sums[32], products[8];
     __shared__ int32_t counts[kFinishThreads];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int s = blockIdx.x;
+    const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
     const int begin = seq.begin(s), end = seq.end(s), rows = end - begin;
     const int first = begin / tile_rows, last = rows > 0 ? (end - 1) / tile_rows : first - 1;
     const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
     // threads: a power of two of columns, the rest of them takes the partial rows in turns
+    const int mine = (E + ctas - 1) / ctas;
     int columns = 32;
-    while (columns < E) columns *= 2;
-    const int turns = kFinishThreads / columns, e = threadIdx.x % columns, turn = threadIdx.x / columns;
+    while (columns < mine) columns *= 2;
+    const int turns = blockDim.x / columns, c0 = threadIdx.x % columns, turn = threadIdx.x / columns;
+    const int e = rank * mine + c0;
+    const bool in = c0 < mine && e < E;
     float v = 0.0f;
     int32_t c = 0;
-    if (e < E)
+    if (in)
+#pragma unroll 8
         for (int i = first + turn; i <= last; i += turns) {
             const size_t at = ((size_t)i + s) * E + e;
             v += part.prob[at];
             c += part.count[at];
         }
+    float z = 0.0f;
+    if (rank == 0)
+        for (int i = first + threadIdx.x; i <= last; i += blockDim.x) z += part.z[(size_t)i + s];
     sums[threadIdx.x] = v;
     counts[threadIdx.x] = c;
+    z = warp_sum(z);
+    if (threadIdx.x % 32 == 0) z_sums[threadIdx.x / 32] = z;
     __syncthreads();
     float product = 0.0f;
-    if (turn == 0 && e < E) {
-        for (int i = 1; i < turns; ++i) v += sums[i * columns + e], c += counts[i * columns + e];
+    if (turn == 0 && in) {
+#pragma unroll 4
+        for (int i = 1; i < turns; ++i) v += sums[i * columns + c0], c += counts[i * columns + c0];
         const float p = v * inv, f = rows > 0 ? (float)c / ((float)k * (float)rows) : 0.0f;
         count[(size_t)s * E + e] = c;
         load[(size_t)s * E + e] = f;
@@ -174,120 +277,214 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(Sequence
     if (threadIdx.x % 32 == 0) inner[threadIdx.x / 32] = product;
     __syncthreads();
     if (threadIdx.x < 32) {
-        product = warp_sum(inner[threadIdx.x]);
-        float z = 0.0f;
-        for (int i = first + threadIdx.x; i <= last; i += 32) z += part.z[(size_t)i + s];
-        z = warp_sum(z);
-        if (threadIdx.x == 0) {
-            loss[2 * (size_t)s] = (float)E * product;
-            loss[2 * (size_t)s + 1] = z * inv;
-        }
+        product = warp_sum(threadIdx.x < blockDim.x / 32 ? inner[threadIdx.x] : 0.0f);
+        if (threadIdx.x == 0)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_smem_u32(&products[rank], 0)), "f"(product) : "memory");
+    }
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        product = 0.0f;
+        for (int i = 0; i < ctas; ++i) product += products[i];
+        z = 0.0f;
+        for (int i = 0; i < blockDim.x / 32; ++i) z += z_sums[i];
+        loss[2 * (size_t)s] = (float)E * product;
+        loss[2 * (size_t)s + 1] = z * inv;
     }
 }
 
-// A warp takes `rows` consecutive rows.
-template <int VPL>
-__global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(Sequences seq, int E, int rows, const float *logits,
-                                                                       const float *load, const float *d_loss,
-                                                                       const float *d_in, float *d_logits) {
+// A warp takes `mine` consecutive rows.
+template <int L, int NQ, bool WIDE>
+__global__ void __launch_bounds__(kBalThreads, NQ <= 4 ? 2 : 1) balance_backward_kernel(Sequences seq, int E, int mine, const float *logits,
+                                                                                       const float *load, const float *d_loss,
+                                                                                       const float *d_in, float *d_logits) {
+    using R = Row<L, NQ, WIDE>;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x % 32;
-    const int64_t first = ((int64_t)blockIdx.x * kBalWarps + threadIdx.x / 32) * rows;
-    const int64_t stop = min(first + rows, (int64_t)seq.T);
+    const int64_t first = ((int64_t)blockIdx.x * kBalWarps + threadIdx.x / 32) * mine;
+    const int64_t stop = min(first + mine, (int64_t)seq.T);
+    int64_t t = first + lane / L;
+    R next, next_d;
+    const auto ask = [&](int64_t t) {
+        const size_t at = (size_t)min(t, (int64_t)seq.T - 1) * E;
+        next.load(logits + at, E, t < stop, -INFINITY);
+        if (d_in)
+            next_d.load(d_in + at, E, true, 0.0f);
+        else
+            next_d.clear();
+    };
+    ask(t);
     int begin = 0, end = 0;  // of the sequence that f, c0 and c1 are of
-    float f[VPL], c0 = 0.0f, c1 = 0.0f;
-    for (int64_t t64 = first; t64 < stop; ++t64) {
-        const int t = (int)t64;
-        float p[VPL], d[VPL];
-        load_row(logits + (size_t)t * E, E, lane, p);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] = d_in && i * 32 + lane < E ? d_in[(size_t)t * E + i * 32 + lane] : 0.0f;
-        if (t < begin || t >= end) {
-            const int s = seq.find(t);
+    R f;
+    float c0 = 0.0f, c1 = 0.0f;
+    for (; t - lane / L < stop; t += R::kRows) {
+        if (t < stop && (t < begin || t >= end)) {
+            const int s = L == 32 ? seq.find((int)t) : seq.find_alone((int)t);
             begin = end = 0;
             if (s >= 0 && t < seq.end(s)) {
                 begin = seq.begin(s), end = seq.end(s);
                 const float inv = 1.0f / (float)(end - begin);
                 c0 = d_loss[2 * (size_t)s] * (float)E * inv;
                 c1 = 2.0f * d_loss[2 * (size_t)s + 1] * inv;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) f[i] = i * 32 + lane < E ? load[(size_t)s * E + i * 32 + lane] : 0.0f;
+                f.load(load + (size_t)s * E, E, true, 0.0f);
             }
         }
-        if (end > begin) {
-            const float lse = softmax_row(p);
-            float mean = 0.0f;
+        if (L < 32) __syncwarp();
+        R r = next, d = next_d;
+        ask(t + R::kRows);
+        float top, sum = exponentials(r, top), dot = 0.0f;
+        const bool owned = t >= begin && t < end;
+        if (owned) {
+            uint64_t dots = 0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) mean = fmaf(f[i], p[i], mean);
-            mean = warp_sum(mean);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) d[i] = fmaf(p[i], fmaf(c0, f[i] - mean, c1 * lse), d[i]);
+            for (int i = 0; i < 2 * NQ; ++i) dots = fma2(f.v[i], r.v[i], dots);
+            dot = total(dots);
         }
+        if (L < 32) __syncwarp();
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (i * 32 + lane < E) d_logits[(size_t)t * E + i * 32 + lane] = d[i];
+        for (int k = L / 2; k > 0; k /= 2) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, k);
+        }
+        if (owned && sum != 0.0f) {
+            // p (c0 (f - mean) + c1 lse) = e (g f + h)
+            const float inv = __fdividef(1.0f, sum), g = c0 * inv, h = inv * fmaf(c1, top + __logf(sum), -g * dot);
+            const uint64_t g2 = pair(g, g), h2 = pair(h, h);
+#pragma unroll
+            for (int i = 0; i < 2 * NQ; ++i) d.v[i] = fma2(r.v[i], fma2(g2, f.v[i], h2), d.v[i]);
+        }
+        if (t < stop) d.store(d_logits + (size_t)t * E, E);
     }
 }
 
-// Rows of a tile: two tiles for every SM where there are enough rows, and no fewer than two rows a warp.
-int tile_rows(const ep_config &c) {
-    const int64_t sms = 152;
-    const int64_t rows = (c.T + 2 * sms - 1) / (2 * sms);
-    return (int)(rows < 2 * kBalWarps ? 2 * kBalWarps : rows);
+// The tiles of the forward pass: two for every SM, by CTAs of as many warps as fit, so that few partial sums are
+// left (607 rows of them, from four CTAs an SM, took longer to join than to make); with short sequences, which
+// leave most of such a CTA without rows, four by smaller CTAs. No fewer than 16 rows.
+struct Tiles {
+    int threads, rows, n;
+    size_t partials;  // rows of partial sums, at most
+};
+Tiles tiles(const ep_config &c, int32_t n_seq) {
+    Tiles t;
+    const bool large = c.T / n_seq >= 256;
+    t.threads = large ? kSumThreads : 128;
+    const int64_t n = 152 * (large ? 2 : 4);
+    const int64_t rows = (c.T + n - 1) / n;
+    t.rows = (int)(rows < 16 ? 16 : rows);
+    t.n = (c.T + t.rows - 1) / t.rows;
+    t.partials = (size_t)t.n + (size_t)n_seq;
+    return t;
 }
-int tiles(const ep_config &c) { return (c.T + tile_rows(c) - 1) / tile_rows(c); }
 
-template <int VPL>
-cudaError_t run_balance(const ep_config &c, const Sequences &seq, const float *logits, const int32_t *idx, const Partials &part,
-                        cudaStream_t s) {
-    const size_t smem = (size_t)(kBalWarps + 1) * c.E * sizeof(float);
-    return launch_dependent(balance_kernel<VPL>, dim3((unsigned)tiles(c)), dim3(kBalThreads), smem, s, seq, c.E, c.k, tile_rows(c),
-                            logits, idx, part);
+bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+struct ForwardCall {
+    const ep_config &c;
+    const Sequences &seq;
+    const float *logits;
+    const int32_t *idx;
+    const Partials &part;
+    cudaStream_t s;
+    bool wide() const { return c.E % 4 == 0 && on16(logits); }
+    template <int L, int NQ, bool WIDE>
+    cudaError_t run() const {
+        const Tiles t = tiles(c, seq.n);
+        const size_t smem = (size_t)(t.threads / 32 + 1) * c.E * sizeof(float);
+        static SharedMemoryLimit limit;
+        const cudaError_t e = limit.allow(balance_kernel<L, NQ, WIDE>, smem);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(balance_kernel<L, NQ, WIDE>, dim3((unsigned)t.n), dim3((unsigned)t.threads), smem, s, seq, c.E, c.k,
+                                t.rows, logits, idx, part);
+    }
+};
+struct BackwardCall {
+    const ep_config &c;
+    const Sequences &seq;
+    const float *logits, *load, *d_loss, *d_in;
+    float *d_logits;
+    cudaStream_t s;
+    bool wide() const { return c.E % 4 == 0 && on16(logits) && on16(load) && on16(d_in) && on16(d_logits); }
+    template <int L, int NQ, bool WIDE>
+    cudaError_t run() const {
+        // as many warps as fill the SMs, with equal numbers of rows
+        const int64_t warps = (NQ <= 4 ? 2 : 1) * (int64_t)current_device_sm_count() * kBalWarps;
+        const int64_t rows = ((c.T + warps - 1) / warps + 32 / L - 1) / (32 / L) * (32 / L);
+        const int64_t used = ((int64_t)c.T + rows - 1) / rows;
+        return launch_dependent(balance_backward_kernel<L, NQ, WIDE>, dim3((unsigned)((used + kBalWarps - 1) / kBalWarps)),
+                                dim3(kBalThreads), 0, s, seq, c.E, (int)rows, logits, load, d_loss, d_in, d_logits);
+    }
+};
+template <bool WIDE, typename Call>
+cudaError_t by_experts(const Call &call) {
+    if (call.c.E <= 32) return call.template run<2, 4, WIDE>();
+    if (call.c.E <= 64) return call.template run<4, 4, WIDE>();
+    if (call.c.E <= 128) return call.template run<8, 4, WIDE>();
+    if (call.c.E <= 256) return call.template run<16, 4, WIDE>();
+    if (call.c.E <= 512) return call.template run<32, 4, WIDE>();
+    return call.template run<32, kMaxE / 128, WIDE>();
 }
-template <int VPL>
-cudaError_t run_backward(const ep_config &c, const Sequences &seq, const float *logits, const float *load, const float *d_loss,
-                         const float *d_in, float *d_logits, cudaStream_t s) {
-    const int rows = c.T >= 16384 ? 4 : 1;
-    const int64_t warps = ((int64_t)c.T + rows - 1) / rows;
-    return launch_dependent(balance_backward_kernel<VPL>, dim3((unsigned)((warps + kBalWarps - 1) / kBalWarps)), dim3(kBalThreads),
-                            0, s, seq, c.E, rows, logits, load, d_loss, d_in, d_logits);
+template <typename Call>
+cudaError_t run_call(const Call &call) {
+    return call.wide() ? by_experts<true>(call) : by_experts<false>(call);
+}
+
+cudaError_t run_finish(const ep_config &c, const Sequences &seq, const Partials &part, int32_t *count, float *load, float *prob,
+                       float *loss, cudaStream_t s) {
+    // Few sequences: CTAs of 32 columns each, up to the eight of a cluster, with 32 rows of partial sums at a time.
+    // Many, of which each has few rows of them: one CTA for all columns.
+    const bool few = seq.n <= current_device_sm_count() / 2;
+    const int ctas = !few ? 1 : c.E >= 256 ? 8 : (c.E + 31) / 32;
+    // threads: as many turns of columns as a sequence has rows of partial sums, about
+    const int share = tiles(c, seq.n).n / seq.n + 1;
+    int threads = few ? 32 : 128;
+    if (few)
+        for (int turns = 1; turns < share && threads < kFinishThreads; turns *= 2) threads *= 2;
+    else
+        while (threads < c.E) threads *= 2;
+    const int columns = (c.E + ctas - 1) / ctas;  // of a CTA, each of which needs a thread
+    while (threads < columns) threads *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas * (unsigned)seq.n);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, balance_finish_kernel, seq, c.E, c.k, tiles(c, seq.n).rows, ctas, part, count, load, prob, loss);
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(const ep_config &c, int32_t n_seq) {
-    return ((size_t)tiles(c) + (size_t)n_seq) * (2 * (size_t)c.E + 1) * sizeof(float);
+    return tiles(c, n_seq).partials * (2 * (size_t)c.E + 1) * sizeof(float);
 }
 
 cudaError_t launch_balance(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *idx, const int32_t *seq_first,
                            const int32_t *seq_len, int32_t *count, float *load, float *prob, float *loss, void *workspace,
                            cudaStream_t s) {
     const Sequences seq{seq_first, seq_len, n_seq, c.T};
-    const size_t rows = (size_t)tiles(c) + (size_t)n_seq;
+    const size_t rows = tiles(c, n_seq).partials;
     Partials part;
     part.prob = static_cast<float *>(workspace);
     part.count = reinterpret_cast<int32_t *>(part.prob + rows * c.E);
     part.z = reinterpret_cast<float *>(part.count + rows * c.E);
     if (c.T > 0) {
-        const cudaError_t e = c.E <= 32    ? run_balance<1>(c, seq, logits, idx, part, s)
-                              : c.E <= 128 ? run_balance<4>(c, seq, logits, idx, part, s)
-                              : c.E <= 256 ? run_balance<8>(c, seq, logits, idx, part, s)
-                                           : run_balance<kMaxE / 32>(c, seq, logits, idx, part, s);
+        const cudaError_t e = run_call(ForwardCall{c, seq, logits, idx, part, s});
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(balance_finish_kernel, dim3((unsigned)n_seq), dim3(kFinishThreads), 0, s, seq, c.E, c.k, tile_rows(c),
-                            part, count, load, prob, loss);
+    return run_finish(c, seq, part, count, load, prob, loss, s);
 }
 
 cudaError_t launch_balance_backward(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *seq_first,
                                     const int32_t *seq_len, const float *load, const float *d_loss, const float *d_in,
                                     float *d_logits, cudaStream_t s) {
     const Sequences seq{seq_first, seq_len, n_seq, c.T};
-    if (c.E <= 32) return run_backward<1>(c, seq, logits, load, d_loss, d_in, d_logits, s);
-    if (c.E <= 128) return run_backward<4>(c, seq, logits, load, d_loss, d_in, d_logits, s);
-    if (c.E <= 256) return run_backward<8>(c, seq, logits, load, d_loss, d_in, d_logits, s);
-    return run_backward<kMaxE / 32>(c, seq, logits, load, d_loss, d_in, d_logits, s);
+    return run_call(BackwardCall{c, seq, logits, load, d_loss, d_in, d_logits, s});
 }
 
 }  // namespace ep

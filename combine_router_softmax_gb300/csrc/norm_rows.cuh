@@ -6,6 +6,7 @@
 // compile-time form. The rest is decided by branches that a whole CTA takes alike.
 #pragma once
 
+#include "pairs.cuh"
 #include "tcgen05.cuh"  // SharedMemoryLimit
 
 namespace ep {
@@ -47,28 +48,6 @@ cudaError_t launch_norm_backward(const NormArgs &p, bool f32, int most, int *cta
 struct V8 {
     uint64_t p[4];
 };
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
-}
-__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float total(uint64_t v) { return low(v) + high(v); }
-
 __device__ __forceinline__ V8 unpack8(const uint4 &q) {
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
     V8 v;
