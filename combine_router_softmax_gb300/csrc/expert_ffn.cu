@@ -37,16 +37,27 @@ EncodeTiled encoder() {
 
 }  // namespace
 
-bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by) {
+namespace {
+
+bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by,
+                CUtensorMapSwizzle swizzle) {
     EncodeTiled encode = encoder();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
     const cuuint64_t strides[2] = {(cuuint64_t)x * bytes, (cuuint64_t)x * (cuuint64_t)y * bytes};
     const cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1}, ones[3] = {1, 1, 1};
     return encode(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, z > 0 ? 3 : 2,
-                  const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by) {
+    return encode_map(m, base, bytes, x, y, z, bx, by, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool make_piece_map(CUtensorMap *m, const void *base, int64_t x, int64_t y, int64_t z) {
+    return encode_map(m, base, 2, x, y, z, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 namespace {

@@ -221,8 +221,8 @@ OrthoPlan plan_of(const ep_ortho_config &c) {
     p.lo = take(x);
     p.a = take(a);
     p.b = take(a);
-    p.da = take(batch * p.mp * sizeof(float));
-    p.db = take(batch * p.mp * sizeof(float));
+    p.da = take((batch * p.mp + 32) * sizeof(float));
+    p.db = take((batch * p.mp + 32) * sizeof(float));
     p.bytes = at;
     return p;
 }
@@ -248,14 +248,29 @@ cudaError_t make_x(const ep_ortho_config &c, const OrthoPlan &q, const void *m, 
                             ctas, q.parts, (const double *)partial, c.eps, hi, lo);
 }
 
+// What a product reads and writes, as tensors in global memory.
+struct OrthoOperands {
+    const uint16_t *a, *b;       // operands
+    const uint16_t *in[2];       // what its epilogue reads beside them
+    const uint16_t *out[2];      // what it writes; Apply's last step: the result
+};
+
 template <OrthoOp OP, int CG, int NB>
-cudaError_t product(OrthoParams &p, const uint16_t *a, const uint16_t *b, cudaStream_t s) {
+cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     using Sh = OrthoShape<OP, CG, NB>;
     // the maps' type says bf16: all that depends on it is what fills the outside, zeros for both
-    const int64_t x = OP == OrthoOp::kGram ? p.np : p.mp;
-    const bool ok = make_map(&p.a, a, 2, x, p.m, p.batch, kGemmBK, kGemmBM) &&
-                    (Sh::kBMn ? make_map(&p.b, b, 2, p.np, p.m, p.batch, 64, kGemmBK)
-                              : make_map(&p.b, b, 2, x, p.m, p.batch, kGemmBK, Sh::kBRows));
+    const int64_t x = OP == OrthoOp::kGram ? p.np : p.mp, wide = Sh::kSymmetric ? p.mp : p.np;
+    bool ok = make_map(&p.a, q.a, 2, x, p.m, p.batch, kGemmBK, kGemmBM) &&
+              (Sh::kBMn ? make_map(&p.b, q.b, 2, p.np, p.m, p.batch, 64, kGemmBK)
+                        : make_map(&p.b, q.b, 2, x, p.m, p.batch, kGemmBK, Sh::kBRows));
+    for (int i = 0; i < 2; ++i) {
+        if (q.in[i]) ok = ok && make_piece_map(&p.in[i], q.in[i], wide, p.m, p.batch);
+        if (!q.out[i]) continue;
+        if (!p.result)
+            ok = ok && make_piece_map(&p.out[i], q.out[i], wide, p.m, p.batch);
+        else if ((p.transposed ? p.m : p.n) % 8 == 0)  // else it is written value by value
+            ok = ok && make_piece_map(&p.out[i], q.out[i], p.transposed ? p.m : p.n, p.transposed ? p.n : p.m, p.batch);
+    }
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = ortho_gemm_kernel<OP, CG, NB>;
     static SharedMemoryLimit limit;
@@ -284,11 +299,11 @@ cudaError_t product(OrthoParams &p, const uint16_t *a, const uint16_t *b, cudaSt
 // The tile of a product: by CTA pairs of 256 x 256 where those are more than the SMs' pairs, else the
 // narrower one with which more SMs have work.
 template <OrthoOp OP>
-cudaError_t choose(OrthoParams &p, const uint16_t *a, const uint16_t *b, cudaStream_t s) {
+cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     const int64_t sms = current_device_sm_count();
-    if ((int64_t)OrthoWalk<OP, 2, 256>::tiles(p.m, p.n) * p.batch * 2 > sms) return product<OP, 2, 256>(p, a, b, s);
-    if ((int64_t)OrthoWalk<OP, 1, 64>::tiles(p.m, p.n) * p.batch <= sms) return product<OP, 1, 64>(p, a, b, s);
-    return product<OP, 1, 128>(p, a, b, s);
+    if ((int64_t)OrthoWalk<OP, 2, 256>::tiles(p.m, p.n) * p.batch * 2 > sms) return product<OP, 2, 256>(p, q, s);
+    if ((int64_t)OrthoWalk<OP, 1, 64>::tiles(p.m, p.n) * p.batch <= sms) return product<OP, 1, 64>(p, q, s);
+    return product<OP, 1, 128>(p, q, s);
 }
 
 }  // namespace
@@ -348,22 +363,17 @@ cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const
     for (int i = 0; i < c.steps; ++i) {
         const uint16_t *now = x[i % 2];
         p.ca = k[3 * i], p.cb = k[3 * i + 1], p.cc = k[3 * i + 2];
-        p.out = a;
         p.d_out = da;
-        e = choose<OrthoOp::kGram>(p, now, now, s);
+        e = choose<OrthoOp::kGram>(p, {now, now, {}, {a}}, s);
         if (e != cudaSuccess) return e;
-        p.o = a;
         p.d = da;
-        p.out = b;
         p.d_out = db;
-        e = choose<OrthoOp::kPoly>(p, a, a, s);
+        e = choose<OrthoOp::kPoly>(p, {a, a, {a}, {b}}, s);
         if (e != cudaSuccess) return e;
         p.d = db;
-        p.hi = now;
-        p.lo = p.lo_out = lo;
-        p.out = x[(i + 1) % 2];
-        p.result = i + 1 == c.steps ? out : nullptr;
-        e = choose<OrthoOp::kApply>(p, b, now, s);
+        const bool last = i + 1 == c.steps;
+        p.result = last ? out : nullptr;
+        e = choose<OrthoOp::kApply>(p, {b, now, {now, lo}, {last ? out : x[(i + 1) % 2], last ? nullptr : lo}}, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -21,6 +21,7 @@
 #pragma once
 
 #include "expert_gemm.cuh"
+#include "pairs.cuh"
 
 namespace ep {
 
@@ -30,17 +31,15 @@ enum class OrthoOp { kGram, kPoly, kApply };
 constexpr float kX = 8192.0f, kA = 1024.0f, kB = 2048.0f, kLo = 1024.0f;
 
 struct OrthoParams {
-    CUtensorMap a, b;
+    CUtensorMap a, b;        // operands
+    CUtensorMap in[2];       // Poly: A without its diagonal; Apply: hi and lo of X. Boxes of 32 x 32 of the tile
+    CUtensorMap out[2];      // Gram, Poly: A, B without its diagonal; Apply: hi and lo, or the result
     int32_t batch;
     int32_t m, n;    // of X
     int32_t mp, np;  // row lengths of A and B, and of X: m and n filled up to 8, with zeros
-    const uint16_t *o;      // Poly: A without its diagonal [batch, m, mp]
-    const float *d;         // Poly: A's diagonal; Apply: a + B's [batch, mp]
-    const uint16_t *hi, *lo;  // Apply: X [batch, m, np]
-    uint16_t *out;          // Gram, Poly: without the diagonal; Apply: hi
-    float *d_out;           // Gram, Poly
-    uint16_t *lo_out;       // Apply; may be lo
-    ep_bf16 *result;        // Apply: not null in the last step: [batch, m, n], or [batch, n, m] if `transposed`
+    const float *d;  // Poly: A's diagonal; Apply: a + B's [batch, mp], and 32 more values behind them
+    float *d_out;    // Gram, Poly
+    ep_bf16 *result; // Apply: not null in the last step: [batch, m, n], or [batch, n, m] if `transposed`
     int32_t transposed;
     float ca, cb, cc;
     int32_t *error;
@@ -54,10 +53,16 @@ struct OrthoShape {
     static constexpr int kBRows = NB / CG;
     static constexpr int kABytes = kGemmBM * 128;
     static constexpr int kStageBytes = kABytes + kBRows * 128;
-    static constexpr int kStages = 196608 / kStageBytes;
-    static_assert(kStages % kProducers == 0, "a stage has one producer");
+    // An epilogue warp's buffers, each two slabs: Apply hi and lo; Poly and Gram a tile and its mirror image. A pair has
+    // one, and six stages in its ring: its main loops are as long as an epilogue that waits for what it has asked
+    // for, and with four stages they take longer (Gram 185 -> 195 us). Single CTAs, which have the shorter tiles, have
+    // three where something is fetched: the one that is worked on, the next one's and the last one's.
+    static constexpr int kBuffers = OP == OrthoOp::kGram || CG == 2 ? 1 : 3;
+    static constexpr int kBufferBytes = 2 * kSlabBytes;
+    static constexpr int kInBytes = OP == OrthoOp::kGram ? 0 : OP == OrthoOp::kPoly ? kSlabBytes : 2 * kSlabBytes;
+    static constexpr int kStages = (kBuffers == 1 ? 196608 : 131072) / kStageBytes / kProducers * kProducers;
     static_assert(!kSymmetric || kBM % NB == 0, "tiles beside the diagonal blocks");
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpilogueWarps * kSlabBytes;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + (size_t)kEpilogueWarps * kBuffers * kBufferBytes;
 };
 
 struct OrthoTile {
@@ -107,13 +112,27 @@ constexpr uint32_t mma_idesc_f16(int m, int n, bool b_mn_major) {
     return 1u << 4 | (b_mn_major ? 1u : 0u) << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
-// The slab with rows and columns exchanged: this thread's row of 32 values becomes column `lane`.
+// An epilogue warp's tile of 32 x 32 halves lies in shared memory as TMA writes and reads a box of 64 bytes' width
+// swizzled over 64 bytes, which is slab_at: 2 KB, one row to a lane. It comes and goes by TMA: with loads and stores of
+// the warp's own, through registers, an epilogue took longer than the main loop of 2048 (Poly 113 us for 16 of 2048, Apply
+// 370 at 4096).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(smem_u32(src)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// What the warp has written to its slabs goes out by the copies that one lane issues next.
+__device__ __forceinline__ void slabs_to_copies() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+// Rows and columns exchanged: this thread's row of 32 values becomes column `lane`.
 __device__ __forceinline__ void slab_put_transposed(unsigned char *slab, int lane, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         *reinterpret_cast<uint16_t *>(slab + slab_at(i, lane / 8) + lane % 8 * 2) = (uint16_t)(v[i / 2] >> (i % 2 * 16));
 }
-// slab_store for rows of any length, value by value: columns [n, n + 32) of N.
+// To rows of any length, value by value: columns [n, n + 32) of N.
 __device__ __forceinline__ void slab_store_any(const unsigned char *slab, int lane, ep_bf16 *base, int N, int n, int rows) {
     __syncwarp();
     if (n + lane < N)
@@ -121,6 +140,36 @@ __device__ __forceinline__ void slab_store_any(const unsigned char *slab, int la
             base[(size_t)r * N + n + lane] = *reinterpret_cast<const uint16_t *>(slab + slab_at(r, lane / 8) + lane % 8 * 2);
     __syncwarp();
 }
+// Two halves as floats, and two registers as a pair.
+__device__ __forceinline__ uint64_t halves(uint32_t v) {
+    const float2 f = saved_values<false>(v);
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+
+// The 32 x 32 pieces of the tiles that an epilogue warp turns into results, in order.
+template <OrthoOp OP, int CG, int NB>
+struct OrthoPieces {
+    using Sh = OrthoShape<OP, CG, NB>;
+    OrthoWalk<OP, CG, NB> walk;
+    OrthoTile t;
+    int row, turn, width, m;  // the warp's first row of a tile; its turn of the columns
+    int c = 0, c_end = 0;     // column of the tile; not c < c_end: no tile yet, or done with it
+    __device__ OrthoPieces(const OrthoParams &p, int row_, int turn_)
+        : walk(p), row(row_), turn(turn_), width(Sh::kSymmetric ? p.mp : p.np), m(p.m) {}
+    __device__ bool next_tile() {
+        if (!walk.next(t)) return false;
+        c = turn * kCols;
+        c_end = t.m0 + row < m ? min(NB, width - t.n0) : 0;
+        return true;
+    }
+    __device__ bool next() {
+        c += 2 * kCols;
+        while (c >= c_end)
+            if (!next_tile()) return false;
+        return true;
+    }
+};
 
 template <OrthoOp OP, int CG, int NB>
 __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __grid_constant__ OrthoParams p) {
@@ -129,11 +178,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     extern __shared__ unsigned char smem_raw[];
     // CG = 2: both CTAs' copies report to the first CTA's `full`
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t in_full[kEpilogueWarps][Sh::kBuffers];
     __shared__ uint32_t tmem_addr;
     __shared__ volatile int failed;
 
     unsigned char *stages = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    unsigned char *slabs = stages + kStages * Sh::kStageBytes;
+    unsigned char *buffers = stages + kStages * Sh::kStageBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0;
     const int kb = ((OP == OrthoOp::kGram ? p.n : p.m) + kGemmBK - 1) / kGemmBK;
@@ -141,11 +191,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], kEpilogueWarps * CG);
+        for (int i = 0; i < kEpilogueWarps * Sh::kBuffers; ++i) mbar_init(&in_full[0][i], 1);
         mbar_init(&drained, 1);
         failed = 0;
         fence_mbar_init();
         tma_prefetch_map(&p.a);
         tma_prefetch_map(&p.b);
+        if (Sh::kInBytes > 0) tma_prefetch_map(&p.in[0]);
     }
     if (warp == 1) tmem_alloc<CG>(&tmem_addr, 2 * NB);
     tmem_fence_before();
@@ -161,7 +213,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     OrthoWalk<OP, CG, NB> walk(p);
     OrthoTile t;
     bool produces = false;
-    uint32_t it = 0;  // the next fill of this producer
+    uint32_t it = 0;     // the next fill of this producer
+    uint32_t asked = 0;  // pieces that this epilogue warp has asked for
 
     if (warp == 0 || warp > 1 + kEpilogueWarps) {
         // ---- producers: one lane each, which take the stages in turn
@@ -234,127 +287,161 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     } else {
         // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread, and
         // two warps take the same rows' columns in turns of 32
+        constexpr bool kFetches = Sh::kInBytes > 0;
         const int quarter = warp % 4, turn = (warp - 2) / 4;
-        unsigned char *slab = slabs + (warp - 2) * kSlabBytes;
-        uint32_t acc_it = 0;
-        while (walk.next(t)) {
+        const int row = (int)rank * kGemmBM + quarter * 32;  // of the tile
+        unsigned char *mine = buffers + (warp - 2) * Sh::kBuffers * Sh::kBufferBytes;
+        uint64_t *arrived = in_full[warp - 2];
+        OrthoPieces<OP, CG, NB> ahead(p, row, turn);  // what has been asked for
+        // The next piece into the buffer after the last one's. What was sent out from there has to have been read:
+        // with three buffers only the last piece's copies may still be under way.
+        const auto ask = [&]() {
+            if (!kFetches || !ahead.next()) return;
+            if (lane == 0) {
+                unsigned char *to = mine + asked % Sh::kBuffers * Sh::kBufferBytes;
+                uint64_t *bar = &arrived[asked % Sh::kBuffers];
+                bulk_wait_read<(Sh::kBuffers > 1)>();
+                mbar_arrive_expect_tx(bar, Sh::kInBytes);
+                const int x = ahead.t.n0 + ahead.c, y = ahead.t.m0 + row;
+                tma_load_3d<1>(to, &p.in[0], x, y, ahead.t.matrix, smem_u32(bar));
+                if (OP == OrthoOp::kApply) tma_load_3d<1>(to + kSlabBytes, &p.in[1], x, y, ahead.t.matrix, smem_u32(bar));
+            }
+            ++asked;
+        };
+        ask();
+        uint32_t acc_it = 0, piece = 0;
+        OrthoPieces<OP, CG, NB> at(p, row, turn);
+        bool ok = true;
+        while (ok && at.next_tile()) {
+            const OrthoTile &t = at.t;
             const uint32_t slot = acc_it & 1;
-            const int first = t.m0 + (int)rank * kGemmBM + quarter * 32;  // the warp's first row
-            const int i = first + lane;
-            const int rows = min(p.m - first, 32);
-            const int width = Sh::kSymmetric ? p.mp : p.np;
-            const int c_end = min(NB, width - t.n0);
+            const int first = t.m0 + row, i = first + lane;  // the warp's first row, and this thread's
             const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + slot * NB;
-            const size_t row = (size_t)t.matrix * p.m + first;  // of [batch, m]
             const size_t diag = (size_t)t.matrix * p.mp;
             float di = 0.0f;
             if (OP != OrthoOp::kGram && i < p.m) di = p.d[diag + i];
-            // what goes with the accumulator is asked for a turn ahead, the first before that is there
-            uint4 q0[4], q1[4];
-            const auto ask = [&](int c) {
-                if (OP == OrthoOp::kGram || rows <= 0 || c >= c_end) return;
-                if constexpr (OP == OrthoOp::kPoly) {
-                    slab_load(q0, lane, p.o + row * p.mp, p.mp, t.n0 + c, rows);
-                } else {
-                    slab_load(q0, lane, p.hi + row * p.np, p.np, t.n0 + c, rows);
-                    slab_load(q1, lane, p.lo + row * p.np, p.np, t.n0 + c, rows);
-                }
-            };
-            int c = turn * kCols;
-            ask(c);
-            bool ok = true;
             if (lane == 0) ok = mbar_wait_limited(&acc_full[slot], (acc_it / 2) & 1, &failed);
-            if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
             ++acc_it;
             tmem_fence_after();
-            for (; rows > 0 && c < c_end; c += 2 * kCols) {
-                const int n = t.n0 + c;
+            for (; at.c < at.c_end; at.c += 2 * kCols, ++piece) {
+                const int c = at.c, n = t.n0 + c;
+                unsigned char *slab = mine + piece % Sh::kBuffers * Sh::kBufferBytes, *second = slab + kSlabBytes;
                 uint32_t v[32], o[16];
+                float4 dj[8];  // Poly: A's diagonal at the piece's columns
+                if constexpr (OP == OrthoOp::kPoly) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dj[k] = *reinterpret_cast<const float4 *>(p.d + diag + n + 4 * k);
+                }
+                if (Sh::kBuffers > 1) ask();
+                if (kFetches) {
+                    ok = mbar_wait_warp(&arrived[piece % Sh::kBuffers], piece / Sh::kBuffers & 1, &failed);
+                    if (!ok) break;
+                }
                 if constexpr (OP == OrthoOp::kApply) {
                     uint32_t hi[16], lo[16];
-                    slab_fill(slab, lane, q0);
                     slab_get(slab, lane, hi);
-                    __syncwarp();
-                    slab_fill(slab, lane, q1);
-                    slab_get(slab, lane, lo);
-                    __syncwarp();
-                    ask(c + 2 * kCols);
+                    slab_get(second, lane, lo);
                     tmem_load_32(src + c, v);
                     tmem_wait_ld(v);
+                    const uint64_t d2 = pair(di, di), by_lo = pair(1.0f / kLo, 1.0f / kLo), by_b = pair(1.0f / kB, 1.0f / kB);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 h = saved_values<false>(hi[k]), l = saved_values<false>(lo[k]);
-                        const float x0 = fmaf(di, fmaf(l.x, 1.0f / kLo, h.x), __uint_as_float(v[2 * k]) * (1.0f / kB));
-                        const float x1 = fmaf(di, fmaf(l.y, 1.0f / kLo, h.y), __uint_as_float(v[2 * k + 1]) * (1.0f / kB));
+                        // a + B's diagonal times hi + lo, and the product
+                        const uint64_t x = fma2(d2, fma2(halves(lo[k]), by_lo, halves(hi[k])), mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b));
                         if (p.result) {
-                            o[k] = bf16_pair(x0 * (1.0f / kX), x1 * (1.0f / kX));
+                            const uint64_t y = mul2(x, pair(1.0f / kX, 1.0f / kX));
+                            o[k] = bf16_pair(low(y), high(y));
                         } else {
-                            o[k] = half_pair(x0, x1);
-                            const float2 r = saved_values<false>(o[k]);
-                            lo[k] = half_pair((x0 - r.x) * kLo, (x1 - r.y) * kLo);
+                            o[k] = half_pair(low(x), high(x));
+                            const uint64_t r = mul2(fma2(halves(o[k]), pair(-1.0f, -1.0f), x), pair(kLo, kLo));
+                            lo[k] = half_pair(low(r), high(r));
                         }
                     }
                     if (!p.result) {
                         slab_put(slab, lane, o);
-                        slab_store(slab, lane, p.out + row * p.np, p.np, n, rows);
-                        slab_put(slab, lane, lo);
-                        slab_store(slab, lane, p.lo_out + row * p.np, p.np, n, rows);
+                        slab_put(second, lane, lo);
+                        slabs_to_copies();
+                        if (lane == 0) {
+                            tma_store_3d(&p.out[0], slab, n, first, t.matrix);
+                            tma_store_3d(&p.out[1], second, n, first, t.matrix);
+                        }
                     } else if (p.transposed) {
+                        __syncwarp();  // other lanes' rows are written over
                         slab_put_transposed(slab, lane, o);
-                        ep_bf16 *base = p.result + ((size_t)t.matrix * p.n + n) * p.m;
-                        const int high = min(32, p.n - n);
-                        if (p.m % 8 == 0)
-                            slab_store(slab, lane, base, p.m, first, high);
-                        else
-                            slab_store_any(slab, lane, base, p.m, first, high);
+                        if (p.m % 8 == 0) {
+                            slabs_to_copies();
+                            if (lane == 0) tma_store_3d(&p.out[0], slab, first, n, t.matrix);
+                        } else {
+                            slab_store_any(slab, lane, p.result + ((size_t)t.matrix * p.n + n) * p.m, p.m, first, min(32, p.n - n));
+                        }
                     } else {
                         slab_put(slab, lane, o);
-                        if (p.n % 8 == 0)
-                            slab_store(slab, lane, p.result + row * p.n, p.n, n, rows);
-                        else
-                            slab_store_any(slab, lane, p.result + row * p.n, p.n, n, rows);
+                        if (p.n % 8 == 0) {
+                            slabs_to_copies();
+                            if (lane == 0) tma_store_3d(&p.out[0], slab, n, first, t.matrix);
+                        } else {
+                            slab_store_any(slab, lane, p.result + ((size_t)t.matrix * p.m + first) * p.n, p.n, n, min(32, p.m - first));
+                        }
                     }
                 } else {
-                    float x[32];
+                    uint64_t x[16];
                     if constexpr (OP == OrthoOp::kPoly) {
                         uint32_t a[16];
-                        slab_fill(slab, lane, q0);
                         slab_get(slab, lane, a);
-                        __syncwarp();
-                        ask(c + 2 * kCols);
-                        const float dj = n + lane < p.m ? p.d[diag + n + lane] : 0.0f;  // lane j: of column j
                         tmem_load_32(src + c, v);
                         tmem_wait_ld(v);
+                        // kB (A (b + c (di + dj)) + c acc), A and acc as they are stored
+                        const float by_a = kB / kA, base = by_a * fmaf(p.cc, di, p.cb);
+                        const uint64_t base2 = pair(base, base), cc2 = pair(by_a * p.cc, by_a * p.cc);
+                        const uint64_t acc2 = pair(p.cc * (kB / (kA * kA)), p.cc * (kB / (kA * kA)));
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float2 a2 = saved_values<false>(a[k / 2]);
-                            const float f = fmaf(p.cc, di + __shfl_sync(0xFFFFFFFFu, dj, k), p.cb);
-                            x[k] = fmaf(kB / kA * (k % 2 ? a2.y : a2.x), f, p.cc * (kB / (kA * kA)) * __uint_as_float(v[k]));
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t d2 = k % 2 ? pair(dj[k / 2].z, dj[k / 2].w) : pair(dj[k / 2].x, dj[k / 2].y);
+                            x[k] = fma2(halves(a[k]), fma2(cc2, d2, base2), mul2(pair_of(v[2 * k], v[2 * k + 1]), acc2));
                         }
                     } else {
                         tmem_load_32(src + c, v);
                         tmem_wait_ld(v);
+                        const uint64_t by = pair(kA / (kX * kX), kA / (kX * kX));
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k]) * (kA / (kX * kX));
+                        for (int k = 0; k < 16; ++k) x[k] = mul2(pair_of(v[2 * k], v[2 * k + 1]), by);
                     }
-                    // columns behind the last are zeros, the diagonal is apart
+                    if (n == first) {  // the diagonal is kept apart
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (n + k == i && i < p.m)
-                            p.d_out[diag + i] = OP == OrthoOp::kGram ? x[k] * (1.0f / kA)
-                                                                     : fmaf(x[k], 1.0f / kB, p.ca + fmaf(p.cc * di, di, p.cb * di));
-                        if (n + k == i || n + k >= p.m || i >= p.m) x[k] = 0.0f;
+                        for (int k = 0; k < 32; ++k) {
+                            const float e = k % 2 ? high(x[k / 2]) : low(x[k / 2]);
+                            if (k != lane) continue;
+                            if (i < p.m)
+                                p.d_out[diag + i] = OP == OrthoOp::kGram ? e * (1.0f / kA)
+                                                                         : fmaf(e, 1.0f / kB, p.ca + fmaf(p.cc * di, di, p.cb * di));
+                            x[k / 2] = k % 2 ? pair(low(x[k / 2]), 0.0f) : pair(0.0f, high(x[k / 2]));
+                        }
+                    }
+                    if (n + 32 > p.m) {  // zeros behind the last column
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            x[k] = pair(n + 2 * k < p.m ? low(x[k]) : 0.0f, n + 2 * k + 1 < p.m ? high(x[k]) : 0.0f);
                     }
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = half_pair(x[2 * k], x[2 * k + 1]);
+                    for (int k = 0; k < 16; ++k) o[k] = half_pair(low(x[k]), high(x[k]));
+                    if (!kFetches) {  // the buffer's last content has to be out
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
                     slab_put(slab, lane, o);
-                    slab_store(slab, lane, p.out + row * p.mp, p.mp, n, rows);
-                    if (t.mirror) {
-                        slab_put_transposed(slab, lane, o);
-                        slab_store(slab, lane, p.out + ((size_t)t.matrix * p.m + n) * p.mp, p.mp, first, min(32, p.m - n));
+                    if (t.mirror) slab_put_transposed(second, lane, o);
+                    slabs_to_copies();
+                    if (lane == 0) {
+                        tma_store_3d(&p.out[0], slab, n, first, t.matrix);
+                        if (t.mirror) tma_store_3d(&p.out[0], second, first, n, t.matrix);
                     }
                 }
+                if (lane == 0) bulk_commit();
+                if (Sh::kBuffers == 1) ask();
             }
+            if (!ok) break;
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -364,6 +451,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
                     mbar_arrive(&acc_empty[slot]);
             }
         }
+        if (lane == 0) bulk_wait<0>();
+        __syncwarp();
     }
 
     __syncthreads();
@@ -380,6 +469,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
             } else {  // copies for which the first CTA's barrier was not armed any more
                 for (int i = 0; i < 100; ++i) __nanosleep(10000);
             }
+        } else if (warp > 1 && warp < 2 + kEpilogueWarps) {
+            if (lane == 0) wait_for_fills(in_full[warp - 2], asked, 0, 1, Sh::kBuffers);
         } else if (warp == 1 && rank == 0) {
             if (elect_one()) mma_commit<CG>(&drained);
             __syncwarp();

@@ -13,6 +13,8 @@ namespace ep {
 // A dense matrix [y][x], or [z][y][x], of bf16 (bytes = 2) or bytes (1), to be read in boxes of bx by
 // by elements, 128 bytes wide and swizzled over 128 bytes. What lies outside reads as zero.
 bool make_map(CUtensorMap *m, const void *base, int bytes, int64_t x, int64_t y, int64_t z, int bx, int by);
+// A dense [z][y][x] of 16-bit values, to be read and written in boxes of 32 by 32, swizzled over their 64 bytes.
+bool make_piece_map(CUtensorMap *m, const void *base, int64_t x, int64_t y, int64_t z);
 
 // The dynamic shared memory that one kernel may have on each device. The limit is the kernel's and not the call's:
 // set by every call for itself, one thread's call could lower it between another's setting and launch. So it
