@@ -7,7 +7,7 @@
 #include <cmath>
 
 #include "ortho_gemm.cuh"
-#include "values.cuh"
+#include "ortho_values.cuh"
 
 namespace ep {
 
@@ -80,40 +80,16 @@ __global__ void __launch_bounds__(kSquareThreads) ortho_square_kernel(const V *m
     if (threadIdx.x == 0) partial[blockIdx.x] = sum * back;
 }
 
-// 1 / (norm + eps) as three factors, so that no product on the way leaves fp32's range.
-struct Scale {
-    float f, p1, p2;
-    __device__ float operator()(float v) const { return v * p1 * p2 * f; }
-};
-__device__ Scale matrix_scale(const double *partial, int parts, float eps) {
-    __shared__ Scale shared;
+__device__ OrthoScale matrix_scale(const double *partial, int parts, float eps) {
+    __shared__ OrthoScale shared;
     if (threadIdx.x < 32) {
         double v = 0;
         for (int i = threadIdx.x; i < parts; i += 32) v += partial[i];
         for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        if (threadIdx.x == 0) {
-            const double by = sqrt(v) + (double)eps;
-            if (by > 0 && by < 1e300) {
-                int e;
-                const double f = frexp(by, &e);
-                shared.f = (float)(1.0 / f);
-                shared.p1 = ldexpf(1.0f, -e / 2);
-                shared.p2 = ldexpf(1.0f, -(e - e / 2));
-            } else {  // 0 / 0, or not finite
-                shared.f = (float)(1.0 / by);
-                shared.p1 = shared.p2 = 1.0f;
-            }
-        }
+        if (threadIdx.x == 0) shared = ortho_scale(v, eps);
     }
     __syncthreads();
     return shared;
-}
-
-__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    x0 *= kX, x1 *= kX;
-    hi = half_pair(x0, x1);
-    const float2 r = saved_values<false>(hi);
-    lo = half_pair((x0 - r.x) * kLo, (x1 - r.y) * kLo);
 }
 
 constexpr int kSplitThreads = 256;
@@ -127,7 +103,7 @@ __global__ void __launch_bounds__(kSplitThreads) ortho_split_kernel(const V *m, 
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t matrix = blockIdx.x / ctas;
-    const Scale scale = matrix_scale(partial + matrix * parts, parts, eps);
+    const OrthoScale scale = matrix_scale(partial + matrix * parts, parts, eps);
     const V *src = m + matrix * rows * cols;
     const int words = pitch / 8;
     const int64_t total = (int64_t)rows * words;
@@ -168,7 +144,7 @@ __global__ void __launch_bounds__(kSplitThreads) ortho_split_transposed_kernel(c
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t matrix = blockIdx.x / ctas;
-    const Scale scale = matrix_scale(partial + matrix * parts, parts, eps);
+    const OrthoScale scale = matrix_scale(partial + matrix * parts, parts, eps);
     const V *src = m + matrix * N * K;
     const int across = (K + kSplitTile - 1) / kSplitTile;
     const int64_t tiles = (int64_t)across * ((N + kSplitTile - 1) / kSplitTile);
@@ -308,7 +284,7 @@ cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
 
 }  // namespace
 
-size_t ortho_workspace_bytes(const ep_ortho_config &c) { return plan_of(c).bytes; }
+size_t ortho_workspace_bytes(const ep_ortho_config &c) { return ortho_fits_fused(c) ? 256 : plan_of(c).bytes; }
 
 // Bounds of X, A and B over the steps, from |singular values| <= 1 on: whether they fit the halves.
 bool ortho_fits(const float *k, int32_t steps) {
@@ -341,6 +317,7 @@ bool ortho_fits(const float *k, int32_t steps) {
 
 cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, void *workspace,
                                  cudaStream_t s) {
+    if (ortho_fits_fused(c)) return launch_ortho_fused(c, k, m, out, s);
     const OrthoPlan q = plan_of(c);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };

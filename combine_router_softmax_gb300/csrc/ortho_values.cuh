@@ -1,0 +1,42 @@
+// ortho_values.cuh -- how the matrices to be orthogonalised come in: scaled by 1 / (norm + eps), as two halves.
+#pragma once
+
+#include "ortho_gemm.cuh"
+#include "values.cuh"
+
+namespace ep {
+
+// 1 / (norm + eps) as three factors, so that no product on the way leaves fp32's range.
+struct OrthoScale {
+    float f, p1, p2;
+    __device__ float operator()(float v) const { return v * p1 * p2 * f; }
+};
+__device__ __forceinline__ OrthoScale ortho_scale(double squares, float eps) {
+    const double by = sqrt(squares) + (double)eps;
+    OrthoScale s;
+    if (by > 0 && by < 1e300) {
+        int e;
+        const double f = frexp(by, &e);
+        s.f = (float)(1.0 / f);
+        s.p1 = ldexpf(1.0f, -e / 2);
+        s.p2 = ldexpf(1.0f, -(e - e / 2));
+    } else {  // 0 / 0, or not finite
+        s.f = (float)(1.0 / by);
+        s.p1 = s.p2 = 1.0f;
+    }
+    return s;
+}
+
+// Two values of X as they are held.
+__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    x0 *= kX, x1 *= kX;
+    hi = half_pair(x0, x1);
+    const float2 r = saved_values<false>(hi);
+    lo = half_pair((x0 - r.x) * kLo, (x1 - r.y) * kLo);
+}
+
+// Matrices that one cluster takes through all steps (ortho_fused.cu).
+bool ortho_fits_fused(const ep_ortho_config &c);
+cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, cudaStream_t s);
+
+}  // namespace ep
