@@ -1,11 +1,11 @@
 // ortho_fused.cu -- small matrices through all Newton-Schulz steps in one kernel.
 //
 // As three products a step, launched one after the other, a matrix of 128 rows takes 6 us a product whatever its
-// work: launch, first copies, last stores. Up to 128 rows (of the wide form) X stays in shared memory instead, the
-// same halves and roundings as in ortho_gemm.cuh: a cluster of up to eight CTAs takes a matrix, each CTA 256 of its
-// columns, and only the sums of A's parts pass between them. One copy of hi serves as both operands of A = X X^T
-// (128 bytes of a row's columns, swizzled) and, read the other way, as the second of B X. A and then B lie in
-// one place; lo is read and written by the thread that owns it alone.
+// work: launch, first copies, last stores. Up to 128 rows (of the wide form) X stays on the chip instead: a cluster of
+// up to eight CTAs takes a matrix, each CTA 256 of its columns, and only the sums of A's parts pass between them.
+// X itself is fp32, in registers (a thread has 64 columns of a row), so that there is no lo; its halves, rounded as
+// in ortho_gemm.cuh, lie in shared memory and serve as both operands of A = X X^T (128 bytes of a row's columns,
+// swizzled) and, read the other way, as the second of B X. A and then B lie in one place.
 //
 // What bounds it is the chain of a step: three waits for a few MMAs, three epilogues, as many fences and barriers.
 #include "ortho_values.cuh"
@@ -18,9 +18,10 @@ constexpr int kFusedThreads = 512;
 constexpr int kFusedRows = 128, kFusedCols = 256;  // of a CTA
 constexpr int kFusedCtas = 8;                      // of a cluster, at most
 constexpr int kBlock = kFusedRows * 128;           // bytes of 64 columns
-constexpr int kHalves = kFusedCols / 64 * kBlock;  // of hi, of lo
+constexpr int kHalves = kFusedCols / 64 * kBlock;  // of X's halves
 constexpr int kSquare = kFusedRows / 64 * kBlock;  // of A, B
 constexpr int kPart = kFusedRows * kFusedRows * 4;
+constexpr int kStaging = kFusedRows * kFusedCols * 4;  // the matrix as it comes in, before there is anything else
 constexpr int kFusedSteps = 64;
 
 struct FusedParams {
@@ -34,8 +35,9 @@ struct FusedParams {
 
 // 16 bytes of a row: the 8 columns from `col` on (of the CTA's).
 __device__ __forceinline__ int unit_at(int row, int col) { return col / 64 * kBlock + row * 128 + ((col % 64 / 8) ^ (row & 7)) * 16; }
-// Four floats of A's part.
+// Four floats of A's part, one of the matrix as it comes in.
 __device__ __forceinline__ int part_at(int row, int col) { return row * 512 + ((col / 4) ^ (row & 7)) * 16; }
+__device__ __forceinline__ int staging_at(int row, int col) { return row * 1024 + ((col / 4) ^ (row & 7)) * 16 + col % 4 * 4; }
 
 __device__ __forceinline__ void get_32(const unsigned char *p, int row, int col, uint32_t (&v)[16]) {
 #pragma unroll
@@ -49,9 +51,10 @@ __device__ __forceinline__ void put_32(unsigned char *p, int row, int col, const
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4 *>(p + unit_at(row, col + 8 * i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-__device__ __forceinline__ float ld_cluster_f32x4(uint32_t addr, float4 &v) {
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v.x;
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
     double v;
@@ -87,11 +90,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
     __shared__ __align__(16) float d[kFusedRows], dB[kFusedRows];  // A's diagonal; a + B's
     __shared__ float warp_sums[kFusedThreads / 32];
     __shared__ double squares;
-    __shared__ int out_of_range;
     __shared__ OrthoScale scale_shared;
 
     unsigned char *hi = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    unsigned char *lo = hi + kHalves, *square = lo + kHalves, *part = square + kSquare;
+    unsigned char *square = hi + kHalves, *part = square + kSquare, *staging = hi;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int ctas = p.ctas;
     const uint32_t rank = ctas > 1 ? cluster_cta_rank() : 0;
@@ -110,33 +112,95 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // ---- the norm. This thread's values of the CTA's part, X[i][c0 + j], i < m, j < cols, neighbours in memory to neighbours
-    const int along = tall ? m : cols, across = tall ? cols : m;  // in memory a line of `along` values, `across` of them
-    const int64_t line = tall ? m : p.K, first = tall ? (int64_t)c0 * m : c0;
-    const auto sum_squares = [&](float by, bool &any) {
-        float s = 0.0f;
-        for (int l = warp; l < across; l += kFusedThreads / 32)
-            for (int i = lane; i < along; i += 32) {
-                const float v = Io<V>::load(src + first + l * line + i);
-                any |= v != 0.0f;
-                s = fmaf(v * by, v * by, s);
+    // ---- X: this thread's row, columns [64 group, + 64) of the CTA's; zeros behind the last row and column
+    const int quarter = warp % 4, group = warp / 4;  // the TMEM lanes that this warp may read, its columns
+    const int row = quarter * 32 + lane;
+    uint64_t x_own[32];
+    if (tall) {  // a column is a line in memory: neighbours read neighbours
+        const V *line = src + (int64_t)(c0 + group * 64) * m + row;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const int col = group * 64 + 2 * k;
+            const bool in = row < m;
+            x_own[k] = pair(in && col < cols ? Io<V>::load(line + 2 * k * (int64_t)m) : 0.0f,
+                            in && col + 1 < cols ? Io<V>::load(line + (2 * k + 1) * (int64_t)m) : 0.0f);
+        }
+    } else {  // a row is one: read line by line and handed over
+        if (p.K % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+            constexpr int kVec = Io<V>::kVec, kPieces = 8 / kVec;  // 16 bytes hold kVec values
+            uint4 q[8][kPieces];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (tid + i * kFusedThreads) / 32, col = (tid + i * kFusedThreads) % 32 * 8;
+#pragma unroll
+                for (int h = 0; h < kPieces; ++h)
+                    q[i][h] = r < m && col < cols ? *reinterpret_cast<const uint4 *>(src + (int64_t)r * p.K + c0 + col + h * kVec)
+                                                  : make_uint4(0, 0, 0, 0);
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (tid + i * kFusedThreads) / 32, col = (tid + i * kFusedThreads) % 32 * 8;
+                float f[8];
+#pragma unroll
+                for (int h = 0; h < kPieces; ++h) {
+                    float u[kVec];
+                    Io<V>::unpack(q[i][h], u);
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) f[h * kVec + j] = u[j];
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float4 *>(staging + staging_at(r, col + 4 * h)) = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+            }
+        } else {
+            for (int r = warp; r < kFusedRows; r += 2 * kFusedThreads / 32) {  // 16 values asked for together
+                float f[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int at = r + h * kFusedThreads / 32, col = lane + 32 * u;
+                        f[h][u] = at < m && col < cols ? Io<V>::load(src + (int64_t)at * p.K + c0 + col) : 0.0f;
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        *reinterpret_cast<float *>(staging + staging_at(r + h * kFusedThreads / 32, lane + 32 * u)) = f[h][u];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const float4 f = *reinterpret_cast<const float4 *>(staging + staging_at(row, group * 64 + 4 * u));
+            x_own[2 * u] = pair(f.x, f.y), x_own[2 * u + 1] = pair(f.z, f.w);
+        }
+    }
+    // ---- the norm
+    const auto sum_squares = [&](float by) {
+        uint64_t s2 = 0;
+        const uint64_t by2 = pair(by, by);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const uint64_t v = mul2(x_own[k], by2);
+            s2 = fma2(v, v, s2);
+        }
+        float s = total(s2);
 #pragma unroll
         for (int k = 16; k > 0; k /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
         __syncthreads();
         if (lane == 0) warp_sums[warp] = s;
         __syncthreads();
         s = 0.0f;
+#pragma unroll
         for (int i = 0; i < kFusedThreads / 32; ++i) s += warp_sums[i];
         return s;
     };
-    bool any = false;
-    float sum = sum_squares(1.0f, any);
-    any = __syncthreads_or(any);
+    float sum = sum_squares(1.0f);
     double back = 1.0;
-    if (any && !(sum >= 0x1p-90f && sum <= 0x1p126f)) {  // the squares leave fp32's range: again, times a power of two
+    if (!(sum >= 0x1p-90f && sum <= 0x1p126f)) {  // all zeros, or the squares leave fp32's range: times a power of two
         const bool small = sum < 0x1p-90f;
-        sum = sum_squares(small ? 0x1p90f : 0x1p-90f, any);
+        sum = sum_squares(small ? 0x1p90f : 0x1p-90f);
         back = small ? 0x1p-180 : 0x1p180;
     }
     if (tid == 0) squares = sum * back;
@@ -150,27 +214,27 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
         scale_shared = ortho_scale(all, p.eps);
     }
     __syncthreads();
-    const OrthoScale scale = scale_shared;
+    const OrthoScale scale = scale_shared;  // and all have read what they stage
 
-    // ---- X as halves: zeros behind the last row and column
-    for (int i = tid; i < 2 * kHalves / 16; i += kFusedThreads) reinterpret_cast<uint4 *>(hi)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for (int l = warp; l < across; l += kFusedThreads / 32)
-        for (int i = lane; i < along; i += 32) {
-            uint32_t h, r;
-            split_pair(scale(Io<V>::load(src + first + l * line + i)), 0.0f, h, r);
-            const int row = tall ? i : l, col = tall ? l : i;
-            const int at = unit_at(row, col) + col % 8 * 2;
-            *reinterpret_cast<uint16_t *>(hi + at) = (uint16_t)h;
-            *reinterpret_cast<uint16_t *>(lo + at) = (uint16_t)r;
+    // ---- X, times kX from here on, and its halves
+    const auto put_halves = [&] {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = half_pair(low(x_own[16 * h + k]), high(x_own[16 * h + k]));
+            put_32(hi, row, group * 64 + 32 * h, o);
         }
+    };
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        x_own[k] = mul2(mul2(mul2(x_own[k], pair(scale.p1, scale.p1)), pair(scale.p2, scale.p2)), pair(scale.f * kX, scale.f * kX));
+    put_halves();
 
-    const int quarter = warp % 4, group = warp / 4;  // the TMEM lanes that this warp may read, its columns
-    const int row = quarter * 32 + lane;
     uint32_t phase = 0;
     // What all have written becomes operands: MMAs issued by one thread, waited for by all.
     const auto multiply = [&](auto issue) {
-        asm volatile("fence.proxy.async;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tmem_fence_before();
         __syncthreads();
         if (warp == 0 && elect_one()) {
@@ -179,7 +243,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
             mma_commit<1>(&done);
         }
         __syncwarp();
-        mbar_wait_warp(&done, phase, &failed);
+        if (lane == 0) mbar_poll_limited(&done, phase, &failed);
+        __syncwarp();
         phase ^= 1;
         tmem_fence_after();
     };
@@ -218,35 +283,27 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
                 *reinterpret_cast<uint4 *>(part + part_at(row, group * 32 + 4 * k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             cluster_sync();
             const int rows = (kFusedRows + ctas - 1) / ctas, r0 = (int)rank * rows;
-            for (int i = tid; i < rows * (kFusedRows / 8); i += kFusedThreads) {
-                const int r = r0 + i / (kFusedRows / 8), col = i % (kFusedRows / 8) * 8;
+            for (int i = tid; i < rows * (kFusedRows / 4); i += kFusedThreads) {
+                const int r = r0 + i / (kFusedRows / 4), col = i % (kFusedRows / 4) * 4;
                 if (r >= kFusedRows) break;
-                uint64_t x[4] = {0, 0, 0, 0};
-                for (int q = 0; q < ctas; ++q) {
+                float4 f[kFusedCtas];  // asked for together
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float4 f;
-                        ld_cluster_f32x4(cluster_smem_u32(part + part_at(r, col + 4 * h), q), f);
-                        x[2 * h] = add2(x[2 * h], pair(f.x, f.y));
-                        x[2 * h + 1] = add2(x[2 * h + 1], pair(f.z, f.w));
-                    }
-                }
+                for (int q = 0; q < kFusedCtas; ++q)
+                    f[q] = q < ctas ? ld_cluster_f32x4(cluster_smem_u32(part + part_at(r, col), q)) : make_float4(0, 0, 0, 0);
+                float x[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], by);
-                const bool mine = r >= col && r < col + 8;
+                for (int q = 0; q < kFusedCtas; ++q) x[0] += f[q].x, x[1] += f[q].y, x[2] += f[q].z, x[3] += f[q].w;
+                const bool mine = r >= col && r < col + 4;
                 float e = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (mine && k == r - col) {
-                        e = k % 2 ? high(x[k / 2]) : low(x[k / 2]);
-                        x[k / 2] = k % 2 ? pair(low(x[k / 2]), 0.0f) : pair(0.0f, high(x[k / 2]));
-                    }
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = half_pair(low(x[k]), high(x[k]));
+                for (int k = 0; k < 4; ++k) {
+                    x[k] *= kA / (kX * kX);
+                    if (mine && k == r - col) e = x[k], x[k] = 0.0f;
+                }
+                const uint32_t o[2] = {half_pair(x[0], x[1]), half_pair(x[2], x[3])};
                 for (int q = 0; q < ctas; ++q) {
-                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_smem_u32(square + unit_at(r, col), q)),
-                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_smem_u32(square + unit_at(r, col) + col % 8 * 2, q)),
+                                 "r"(o[0]), "r"(o[1])
                                  : "memory");
                     if (mine)
                         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_smem_u32(&d[r], q)), "f"(e * (1.0f / kA)) : "memory");
@@ -285,49 +342,56 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
                             mma_idesc_f16(128, 256, true), k > 0);
         });
         const float di = dB[row];
-        const uint64_t d2 = pair(di, di), by_lo = pair(1.0f / kLo, 1.0f / kLo), by_b = pair(1.0f / kB, 1.0f / kB);
-        const bool last = step + 1 == p.steps;
-        for (int col = group * 64; col < group * 64 + 64; col += 32) {
-            uint32_t h[16], l[16];
-            get_32(hi, row, col, h);
-            get_32(lo, row, col, l);
-            tmem_load_32(tmem + kColX + lanes + col, v);
+        const uint64_t d2 = pair(di, di), by_b = pair(1.0f / kB, 1.0f / kB);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            tmem_load_32(tmem + kColX + lanes + group * 64 + 32 * h, v);
             tmem_wait_ld(v);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const uint64_t x = fma2(d2, fma2(halves(l[k]), by_lo, halves(h[k])), mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b));
-                if (last) {
-                    const uint64_t y = mul2(x, pair(1.0f / kX, 1.0f / kX));
-                    h[k] = bf16_pair(low(y), high(y));
-                } else {
-                    h[k] = half_pair(low(x), high(x));
-                    const uint64_t r = mul2(fma2(halves(h[k]), pair(-1.0f, -1.0f), x), pair(kLo, kLo));
-                    l[k] = half_pair(low(r), high(r));
-                }
-            }
-            put_32(hi, row, col, h);
-            if (!last) put_32(lo, row, col, l);
+            for (int k = 0; k < 16; ++k) x_own[16 * h + k] = fma2(d2, x_own[16 * h + k], mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b));
         }
+        if (step + 1 < p.steps) put_halves();
     }
-
-    // ---- the result, rounded already, from hi's place
-    tmem_fence_before();
-    __syncthreads();
+    // ---- the result: by columns as X came in, by rows through the halves' place
     ep_bf16 *out = p.out + matrix * p.N * p.K;
-    if (!failed) {
-        if (!tall && p.K % 8 == 0) {
-            for (int i = tid; i < m * (cols / 8); i += kFusedThreads) {
-                const int r = i / (cols / 8), col = i % (cols / 8) * 8;
-                st_v4(reinterpret_cast<uint4 *>(out + (int64_t)r * p.K + c0 + col), *reinterpret_cast<const uint4 *>(hi + unit_at(r, col)));
+    const auto result = [&](int k) {
+        const uint64_t y = mul2(x_own[k], pair(1.0f / kX, 1.0f / kX));
+        return bf16_pair(low(y), high(y));
+    };
+    if (tall) {
+        ep_bf16 *line = out + (int64_t)(c0 + group * 64) * m + row;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const uint32_t o = result(k);
+            const int col = group * 64 + 2 * k;
+            if (row < m && !failed) {
+                if (col < cols) line[2 * k * (int64_t)m] = (ep_bf16)o;
+                if (col + 1 < cols) line[(2 * k + 1) * (int64_t)m] = (ep_bf16)(o >> 16);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = result(16 * h + k);
+            put_32(hi, row, group * 64 + 32 * h, o);
+        }
+        __syncthreads();
+        if (p.K % 8 == 0) {
+            for (int i = tid; i < m * 32; i += kFusedThreads) {
+                const int r = i / 32, col = i % 32 * 8;
+                if (col < cols && !failed)
+                    st_v4(reinterpret_cast<uint4 *>(out + (int64_t)r * p.K + c0 + col), *reinterpret_cast<const uint4 *>(hi + unit_at(r, col)));
             }
         } else {
-            for (int l = warp; l < across; l += kFusedThreads / 32)
-                for (int i = lane; i < along; i += 32) {
-                    const int r = tall ? i : l, col = tall ? l : i;
-                    out[first + l * line + i] = *reinterpret_cast<const uint16_t *>(hi + unit_at(r, col) + col % 8 * 2);
-                }
+            for (int r = warp; r < m; r += kFusedThreads / 32)
+                for (int col = lane; col < cols; col += 32)
+                    if (!failed) out[(int64_t)r * p.K + c0 + col] = *reinterpret_cast<const uint16_t *>(hi + unit_at(r, col) + col % 8 * 2);
         }
     }
+    tmem_fence_before();
+    __syncthreads();
     if (failed) {  // MMAs under way read shared memory and write TMEM
         if (tid == 0) {
             int gave_up = 0;
@@ -342,7 +406,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
 
 template <typename V>
 cudaError_t run_fused(const FusedParams &p, int batch, cudaStream_t s) {
-    const size_t smem = 1024 + 2 * (size_t)kHalves + kSquare + (p.ctas > 1 ? kPart : 0);
+    const size_t work = (size_t)kHalves + kSquare + (p.ctas > 1 ? kPart : 0), smem = 1024 + (work > kStaging ? work : kStaging);
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(ortho_fused_kernel<V>, smem);
     if (e != cudaSuccess) return e;

@@ -12,8 +12,13 @@ struct OrthoScale {
     __device__ float operator()(float v) const { return v * p1 * p2 * f; }
 };
 __device__ __forceinline__ OrthoScale ortho_scale(double squares, float eps) {
-    const double by = sqrt(squares) + (double)eps;
     OrthoScale s;
+    if (squares >= 0x1p-100 && squares <= 0x1p100) {  // the usual case, without the few 64-bit units' square root
+        s.f = 1.0f / (sqrtf((float)squares) + eps);
+        s.p1 = s.p2 = 1.0f;
+        return s;
+    }
+    const double by = sqrt(squares) + (double)eps;
     if (by > 0 && by < 1e300) {
         int e;
         const double f = frexp(by, &e);
