@@ -231,7 +231,7 @@ struct OrthoOperands {
     const uint16_t *out[2];      // what it writes; Apply's last step: the result
 };
 
-template <OrthoOp OP, int CG, int NB>
+template <OrthoOp OP, int CG, int NB, bool SPLIT = false>
 cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     using Sh = OrthoShape<OP, CG, NB>;
     // the maps' type says bf16: all that depends on it is what fills the outside, zeros for both
@@ -248,14 +248,15 @@ cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
             ok = ok && make_piece_map(&p.out[i], q.out[i], p.transposed ? p.m : p.n, p.transposed ? p.n : p.m, p.batch);
     }
     if (!ok) return cudaErrorInvalidValue;
-    auto kernel = ortho_gemm_kernel<OP, CG, NB>;
+    auto kernel = ortho_gemm_kernel<OP, CG, NB, SPLIT>;
     static SharedMemoryLimit limit;
     cudaError_t e = limit.allow(kernel, Sh::kSmem);
     if (e != cudaSuccess) return e;
     const int sms = current_device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int64_t tiles = (int64_t)OrthoWalk<OP, CG, NB>::tiles(p.m, p.n) * p.batch;
-    const int64_t grid = tiles * CG < sms ? tiles * CG : sms / CG * CG;
+    const int ctas = SPLIT ? p.split : CG;  // of a cluster
+    const int64_t grid = tiles * ctas < sms ? tiles * ctas : sms / ctas * ctas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kGemmThreads);
@@ -265,20 +266,27 @@ cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
+    cfg.numAttrs = ctas == 1 ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // The tile of a product: by CTA pairs of 256 x 256 where those are more than the SMs' pairs, else the
-// narrower one with which more SMs have work.
+// narrower one with which more SMs have work; a long contraction of few tiles is split over as many CTAs as leave
+// each four stages of it (256 x 256 from 7168: 23 us by one CTA a tile).
 template <OrthoOp OP>
 cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     const int64_t sms = current_device_sm_count();
     if ((int64_t)OrthoWalk<OP, 2, 256>::tiles(p.m, p.n) * p.batch * 2 > sms) return product<OP, 2, 256>(p, q, s);
-    if ((int64_t)OrthoWalk<OP, 1, 64>::tiles(p.m, p.n) * p.batch <= sms) return product<OP, 1, 64>(p, q, s);
+    const int64_t narrow = (int64_t)OrthoWalk<OP, 1, 64>::tiles(p.m, p.n) * p.batch;
+    if constexpr (OP == OrthoOp::kGram) {
+        const int64_t stages = (p.n + kGemmBK - 1) / kGemmBK;
+        for (p.split = 8; p.split > 1; p.split /= 2)
+            if (narrow * p.split <= sms && stages >= 4 * p.split) return product<OP, 1, 64, true>(p, q, s);
+    }
+    if (narrow <= sms) return product<OP, 1, 64>(p, q, s);
     return product<OP, 1, 128>(p, q, s);
 }
 
@@ -341,6 +349,7 @@ cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const
         const uint16_t *now = x[i % 2];
         p.ca = k[3 * i], p.cb = k[3 * i + 1], p.cc = k[3 * i + 2];
         p.d_out = da;
+        p.split_out = a;
         e = choose<OrthoOp::kGram>(p, {now, now, {}, {a}}, s);
         if (e != cudaSuccess) return e;
         p.d = da;

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
                         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_smem_u32(&d[r], q)), "f"(e * (1.0f / kA)) : "memory");
                 }
             }
-            asm volatile("fence.proxy.async;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
             cluster_sync();
         }
         // ---- B = b A + c A A

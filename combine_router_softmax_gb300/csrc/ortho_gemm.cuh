@@ -42,6 +42,8 @@ struct OrthoParams {
     ep_bf16 *result; // Apply: not null in the last step: [batch, m, n], or [batch, n, m] if `transposed`
     int32_t transposed;
     float ca, cb, cc;
+    int32_t split;        // SPLIT: CTAs of a tile (2, 4 or 8)
+    uint16_t *split_out;  // A without its diagonal
     int32_t *error;
 };
 
@@ -80,8 +82,8 @@ struct OrthoWalk {
         const int mt = (m + Sh::kBM - 1) / Sh::kBM;
         return Sh::kSymmetric ? mt * (mt + 1) / 2 * (Sh::kBM / NB) : mt * ((n + NB - 1) / NB);
     }
-    __device__ explicit OrthoWalk(const OrthoParams &p)
-        : tile(blockIdx.x / CG), step(gridDim.x / CG), mt((p.m + Sh::kBM - 1) / Sh::kBM), nt((p.n + NB - 1) / NB),
+    __device__ OrthoWalk(const OrthoParams &p, int ctas)  // ctas: of a tile
+        : tile(blockIdx.x / ctas), step(gridDim.x / ctas), mt((p.m + Sh::kBM - 1) / Sh::kBM), nt((p.n + NB - 1) / NB),
           per(tiles(p.m, p.n)) {
         total = (int64_t)per * p.batch;
     }
@@ -156,7 +158,7 @@ struct OrthoPieces {
     int row, turn, width, m;  // the warp's first row of a tile; its turn of the columns
     int c = 0, c_end = 0;     // column of the tile; not c < c_end: no tile yet, or done with it
     __device__ OrthoPieces(const OrthoParams &p, int row_, int turn_)
-        : walk(p), row(row_), turn(turn_), width(Sh::kSymmetric ? p.mp : p.np), m(p.m) {}
+        : walk(p, CG), row(row_), turn(turn_), width(Sh::kSymmetric ? p.mp : p.np), m(p.m) {}
     __device__ bool next_tile() {
         if (!walk.next(t)) return false;
         c = turn * kCols;
@@ -171,10 +173,52 @@ struct OrthoPieces {
     }
 };
 
-template <OrthoOp OP, int CG, int NB>
+// The CTAs of a cluster have added up a part of the contraction each (SPLIT), and left it in shared memory, a row of NB
+// floats after the other. Each adds some rows of all parts up, in the same order, and stores them as the epilogue
+// does. By `threads` threads.
+template <int NB>
+__device__ __forceinline__ int split_at(int row, int col) { return row * (NB * 4) + ((col / 4) ^ (row & 7)) * 16; }
+template <int NB>
+__device__ __forceinline__ void join_split(const OrthoParams &p, const OrthoTile &t, unsigned char *part, uint16_t *out, int rank, int ctas,
+                                           int thread, int threads) {
+    const int rows = kGemmBM / ctas;
+    for (int i = thread; i < rows * (NB / 4); i += threads) {
+        const int r = rank * rows + i / (NB / 4), c = i % (NB / 4) * 4;
+        float4 f[8];  // asked for together
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            f[q] = make_float4(0, 0, 0, 0);
+            if (q < ctas)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f[q].x), "=f"(f[q].y), "=f"(f[q].z), "=f"(f[q].w)
+                             : "r"(cluster_smem_u32(part + split_at<NB>(r, c), q)));
+        }
+        float x[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[0] += f[q].x, x[1] += f[q].y, x[2] += f[q].z, x[3] += f[q].w;
+        const int row = t.m0 + r, n = t.n0 + c;
+        if (row >= p.mp || n >= p.mp) continue;  // behind the last row: zeros, for the mirror image's last columns
+        const size_t first = (size_t)t.matrix * p.m;
+        alignas(8) __half h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float v = x[k] * (kA / (kX * kX));
+            if (n + k == row && row < p.m) p.d_out[(size_t)t.matrix * p.mp + row] = v * (1.0f / kA), v = 0.0f;  // the diagonal is kept apart
+            h[k] = __float2half_rn(v);
+        }
+        if (row < p.m) *reinterpret_cast<uint2 *>(out + (first + row) * p.mp + n) = *reinterpret_cast<const uint2 *>(h);
+        if (t.mirror)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[(first + n + k) * p.mp + row] = *reinterpret_cast<const uint16_t *>(&h[k]);
+    }
+}
+
+// SPLIT (Gram, CG = 1): a cluster takes a tile, each CTA a part of its contraction; one tile for each cluster.
+template <OrthoOp OP, int CG, int NB, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __grid_constant__ OrthoParams p) {
     using Sh = OrthoShape<OP, CG, NB>;
     constexpr int kStages = Sh::kStages;
+    static_assert(!SPLIT || (OP == OrthoOp::kGram && CG == 1), "the epilogue of a split product");
     extern __shared__ unsigned char smem_raw[];
     // CG = 2: both CTAs' copies report to the first CTA's `full`
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
@@ -186,7 +230,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     unsigned char *buffers = stages + kStages * Sh::kStageBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0;
-    const int kb = ((OP == OrthoOp::kGram ? p.n : p.m) + kGemmBK - 1) / kGemmBK;
+    const int kb_all = ((OP == OrthoOp::kGram ? p.n : p.m) + kGemmBK - 1) / kGemmBK;
+    // this CTA's stages of the contraction
+    const int part_of = SPLIT ? p.split : 1, part = SPLIT ? (int)cluster_cta_rank() : 0;
+    const int kb_first = kb_all * part / part_of, kb = kb_all * (part + 1) / part_of - kb_first;
 
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
@@ -210,7 +257,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     grid_dependency_wait();
     grid_launch_dependents();
 
-    OrthoWalk<OP, CG, NB> walk(p);
+    OrthoWalk<OP, CG, NB> walk(p, SPLIT ? p.split : CG);
     OrthoTile t;
     bool produces = false;
     uint32_t it = 0;     // the next fill of this producer
@@ -238,7 +285,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], Sh::kStageBytes * CG);
                     const uint32_t bar = CG == 2 ? cluster_smem_u32(&full[s], 0) : smem_u32(&full[s]);
                     unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
-                    const int k = b * kGemmBK;
+                    const int k = (kb_first + b) * kGemmBK;
                     tma_load_3d<CG>(sa, &p.a, k, t.m0 + (int)rank * kGemmBM, t.matrix, bar);
                     if constexpr (Sh::kBMn) {
 #pragma unroll
@@ -284,6 +331,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
             }
         }
         __syncwarp();
+    } else if constexpr (SPLIT) {
+        // ---- the accumulator as it is, into the stages' place: they have been read when it is complete
+        const int quarter = warp % 4, turn = (warp - 2) / 4, row = quarter * 32 + lane;
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait_limited(&acc_full[0], 0, &failed);
+        __syncwarp();
+        tmem_fence_after();
+        for (int c = turn * kCols; c < NB; c += 2 * kCols) {
+            uint32_t v[32];
+            tmem_load_32(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(stages + split_at<NB>(row, c + 4 * k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
     } else {
         // ---- epilogue: warp w reads lanes [32 (w mod 4), + 32) of the accumulators, one row a thread, and
         // two warps take the same rows' columns in turns of 32
@@ -456,6 +518,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     }
 
     __syncthreads();
+    if constexpr (SPLIT) {
+        cluster_sync();
+        walk.next(t);  // the cluster's tile
+        join_split<NB>(p, t, stages, p.split_out, part, part_of, threadIdx.x, kGemmThreads);
+        cluster_sync();  // no CTA may end while another one reads its memory
+    }
     if constexpr (CG == 2) {
         // a CTA that gave up tells the other one, whose memory its copies and MMAs may use
         if (threadIdx.x == 0 && failed) st_cluster(cluster_smem_u32(const_cast<int *>(&failed), rank ^ 1), 1);

@@ -92,7 +92,7 @@ def normal(B, N, K, seed=0, dtype=BF16):
 # one value, rows and columns alone, ragged, a tile and one more, several tiles, wide and tall
 @pytest.mark.parametrize("B,N,K", [(1, 1, 1), (4, 1, 37), (3, 41, 1), (3, 5, 3), (2, 8, 8), (2, 100, 130), (1, 128, 256),
                                    (5, 129, 130), (3, 300, 77), (1, 64, 4000), (70, 96, 40), (1, 513, 520), (1, 1000, 130),
-                                   (2, 640, 1303), (3, 128, 257), (2, 1500, 100), (4, 60, 2048), (2, 2049, 128), (1, 129, 2048)])
+                                   (2, 640, 1303), (3, 128, 257), (2, 1500, 100), (4, 60, 2048), (2, 2049, 128), (1, 129, 2048), (1, 256, 7000), (2, 136, 2600), (1, 300, 515)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_against_64_bits(ep, B, N, K, dtype):
     m = normal(B, N, K, seed=N + K, dtype=dtype)
