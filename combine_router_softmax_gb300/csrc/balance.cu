@@ -5,9 +5,9 @@
 // every pair of a tile of rows and a sequence that meet; a second kernel adds those up. Tile i and sequence s
 // write row i + s: as both only grow along the rows, no two pairs share one. The gradient computes the softmax again.
 //
-// HBM bounds both at many rows, the launches and a chain of dependent loads at few: forward 128 rows 5.3 us, 32768 x
-// 256 15.3 (of which joining the partial sums 5; 5.1 for its bytes at the copy rate), 131072 x 128 in 64 sequences 23.6
-// (10.5); backward 1.9, 18.1 (14.8), 25.4 (19.8).
+// HBM bounds both at many rows, the launches and a chain of dependent loads at few: forward 128 rows 3.4 us, 32768 x
+// 256 15.4 (of which joining the partial sums 5; 5.1 for its bytes at the copy rate), 131072 x 128 in 64 sequences 24.1
+// (10.5); backward 1.9, 18.1 (14.8), 25.2 (19.8).
 #include "pairs.cuh"
 #include "tcgen05.cuh"  // clusters
 
@@ -18,6 +18,7 @@ namespace {
 constexpr int kBalWarps = 8;  // of a CTA of the backward pass
 constexpr int kBalThreads = 32 * kBalWarps;
 constexpr int kSumThreads = 384;      // of a large CTA of the forward pass: two an SM with 80 registers
+constexpr int kShortThreads = 256;
 constexpr int kFinishThreads = 1024;  // at most
 
 struct Sequences {
@@ -150,9 +151,69 @@ __device__ __forceinline__ float exponentials(Row<L, NQ, WIDE> &r, float &top) {
     return total(sum);
 }
 
+// The sums of a CTA over rows first + i step, i = 0, 1, ..., below hi (`first` is this lane's) and over the ids
+// [id, id_end) in steps of `id_step`: probabilities to sums[0][E], counts to count[E], the squared log-sum-exps returned in
+// thread 0. sums: [warp][E] of shared memory.
+template <int L, int NQ, bool WIDE>
+__device__ __forceinline__ float sum_rows(const float *logits, const int32_t *idx, int E, int64_t t, int64_t step, int hi, int64_t id,
+                                          int64_t id_step, int64_t id_end, float *sums, int32_t *count, float *z_sums) {
+    using R = Row<L, NQ, WIDE>;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, threads = blockDim.x, warps = threads / 32;
+    R next;  // asked for ahead
+    const auto ask = [&](int64_t t) { next.load(logits + (size_t)min(t, (int64_t)hi - 1) * E, E, t < hi, -INFINITY); };
+    ask(t);
+    for (int e = threadIdx.x; e < E; e += threads) count[e] = 0;
+    __syncthreads();
+    for (; id < id_end; id += 8 * id_step) {
+        int e[8];  // asked for together
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = id + j * id_step < id_end ? idx[id + j * id_step] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e[j] >= 0 && e[j] < E) atomicAdd(&count[e[j]], 1);
+    }
+    R acc;
+    float z = 0.0f;
+    acc.clear();
+    for (; t - lane / L < hi; t += step) {  // all lanes alike
+        R r = next;
+        ask(t + step);
+        float top, sum = exponentials(r, top);
+#pragma unroll
+        for (int d = L / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);  // 0: no row
+        const float lse = sum == 0.0f ? 0.0f : top + __logf(sum);
+        z = fmaf(lse, lse, z);
+        const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = fma2(r.v[i], inv2, acc.v[i]);
+    }
+    // over the warp's rows, then over the warps
+    z = lane % L == 0 ? z : 0.0f;
+#pragma unroll
+    for (int d = 16; d >= L; d /= 2) {
+        z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
+#pragma unroll
+        for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = add2(acc.v[i], __shfl_xor_sync(0xFFFFFFFFu, acc.v[i], d));
+    }
+    if (lane < L) acc.store(sums + warp * E, E);
+    if (lane == 0) z_sums[warp] = z;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += threads) {
+        float v = 0.0f;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) v += sums[w * E + e];
+        sums[e] = v;
+    }
+    z = 0.0f;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < warps; ++w) z += z_sums[w];
+    return z;
+}
+
 template <int L, int NQ, bool WIDE>
 __global__ void __launch_bounds__(kSumThreads, NQ <= 4 ? 2 : 1) balance_kernel(Sequences seq, int E, int k, int tile_rows, const float *logits,
-                                                                      const int32_t *idx, Partials part) {
+                                                                              const int32_t *idx, Partials part) {
     using R = Row<L, NQ, WIDE>;
     extern __shared__ float smem[];
     const int threads = blockDim.x, warps = threads / 32;
@@ -168,62 +229,90 @@ __global__ void __launch_bounds__(kSumThreads, NQ <= 4 ? 2 : 1) balance_kernel(S
         if (seq.begin(s) >= end) break;
         const int lo = max(seq.begin(s), begin), hi = min(seq.end(s), end);
         if (lo >= hi) continue;
-        const int step = warps * R::kRows;
-        int64_t t = lo + warp * R::kRows + lane / L;  // this lane's rows; the next one is asked for ahead
-        R next;
-        const auto ask = [&](int64_t t) { next.load(logits + (size_t)min(t, (int64_t)hi - 1) * E, E, t < hi, -INFINITY); };
-        ask(t);
-        for (int e = threadIdx.x; e < E; e += threads) count[e] = 0;
-        __syncthreads();
-        for (int64_t i = (int64_t)lo * k + threadIdx.x; i < (int64_t)hi * k; i += 8 * threads) {
-            int e[8];  // asked for together
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = i + j * threads < (int64_t)hi * k ? idx[i + j * threads] : -1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (e[j] >= 0 && e[j] < E) atomicAdd(&count[e[j]], 1);
-        }
-        R acc;
-        float z = 0.0f;
-        acc.clear();
-        for (; t - lane / L < hi; t += step) {  // all lanes alike
-            R r = next;
-            ask(t + step);
-            float top, sum = exponentials(r, top);
-#pragma unroll
-            for (int d = L / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);  // 0: no row
-            const float lse = sum == 0.0f ? 0.0f : top + __logf(sum);
-            z = fmaf(lse, lse, z);
-            const uint64_t inv2 = pair(inv, inv);
-#pragma unroll
-            for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = fma2(r.v[i], inv2, acc.v[i]);
-        }
-        // over the warp's rows, then over the warps
-        z = lane % L == 0 ? z : 0.0f;
-#pragma unroll
-        for (int d = 16; d >= L; d /= 2) {
-            z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
-#pragma unroll
-            for (int i = 0; i < 2 * NQ; ++i) acc.v[i] = add2(acc.v[i], __shfl_xor_sync(0xFFFFFFFFu, acc.v[i], d));
-        }
-        if (lane < L) acc.store(sums + warp * E, E);
-        if (lane == 0) z_sums[warp] = z;
+        const float z = sum_rows<L, NQ, WIDE>(logits, idx, E, lo + warp * R::kRows + lane / L, warps * R::kRows, hi,
+                                              (int64_t)lo * k + threadIdx.x, threads, (int64_t)hi * k, sums, count, z_sums);
         __syncthreads();
         const size_t row = (size_t)blockIdx.x + s;
         for (int e = threadIdx.x; e < E; e += threads) {
-            float v = 0.0f;
-#pragma unroll 8
-            for (int w = 0; w < warps; ++w) v += sums[w * E + e];
-            part.prob[row * E + e] = v;
+            part.prob[row * E + e] = sums[e];
             part.count[row * E + e] = count[e];
         }
-        if (threadIdx.x == 0) {
-            float v = 0.0f;
-            for (int w = 0; w < warps; ++w) v += z_sums[w];
-            part.z[row] = v;
-        }
+        if (threadIdx.x == 0) part.z[row] = z;
         __syncthreads();
+    }
+}
+
+// Sequences of some hundred rows: a cluster takes one, and nothing is left to a second kernel. The CTAs share its rows,
+// then each adds up a part of the columns of all.
+template <int L, int NQ, bool WIDE>
+__global__ void __launch_bounds__(kShortThreads, NQ <= 4 ? 3 : 1) balance_short_kernel(Sequences seq, int E, int k, int ctas, const float *logits,
+                                                                                      const int32_t *idx, int32_t *count_out, float *load,
+                                                                                      float *prob, float *loss) {
+    using R = Row<L, NQ, WIDE>;
+    extern __shared__ float smem[];
+    constexpr int kWarps = kShortThreads / 32;
+    float *sums = smem;                                                 // [warp][E]
+    int32_t *count = reinterpret_cast<int32_t *>(sums + kWarps * E);  // [E]
+    __shared__ float z_sums[32], z_mine, products[8], inner[kWarps];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+    const int lo = seq.begin(s), hi = seq.end(s), rows = hi - lo;
+    float z = 0.0f;
+    if (rows > 0) {  // in all CTAs of the cluster alike
+        z = sum_rows<L, NQ, WIDE>(logits, idx, E, lo + (int64_t)(rank * kWarps + warp) * R::kRows + lane / L,
+                                  (int64_t)ctas * kWarps * R::kRows, hi, (int64_t)lo * k + rank * kShortThreads + threadIdx.x,
+                                  (int64_t)ctas * kShortThreads, (int64_t)hi * k, sums, count, z_sums);
+    } else {
+        for (int e = threadIdx.x; e < E; e += kShortThreads) sums[e] = 0.0f, count[e] = 0;
+    }
+    if (threadIdx.x == 0) z_mine = z;
+    if (ctas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const float inv = rows > 0 ? 1.0f / (float)rows : 0.0f;
+    const int mine = (E + ctas - 1) / ctas;
+    float product = 0.0f;
+    for (int e = rank * mine + threadIdx.x; e < min((rank + 1) * mine, E); e += kShortThreads) {
+        float v = 0.0f;
+        int32_t c = 0;
+        for (int q = 0; q < ctas; ++q) {
+            float f;
+            int32_t n;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(cluster_smem_u32(sums + e, q)));
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(cluster_smem_u32(count + e, q)));
+            v += f, c += n;
+        }
+        const float p = v * inv, f = rows > 0 ? (float)c / ((float)k * (float)rows) : 0.0f;
+        count_out[(size_t)s * E + e] = c;
+        load[(size_t)s * E + e] = f;
+        prob[(size_t)s * E + e] = p;
+        product = fmaf(f, p, product);
+    }
+    product = warp_sum(product);
+    if (lane == 0) inner[warp] = product;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        product = 0.0f;
+        for (int w = 0; w < kWarps; ++w) product += inner[w];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_smem_u32(&products[rank], 0)), "f"(product) : "memory");
+        if (rank == 0) {
+            z = 0.0f;
+            for (int q = 0; q < ctas; ++q) {
+                float f;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(cluster_smem_u32(&z_mine, q)));
+                z += f;
+            }
+        }
+    }
+    if (ctas > 1) cluster_sync();  // the products are there; no CTA ends while another one reads its memory
+    if (rank == 0 && threadIdx.x == 0) {
+        product = 0.0f;
+        for (int q = 0; q < ctas; ++q) product += products[q];
+        loss[2 * (size_t)s] = (float)E * product;
+        loss[2 * (size_t)s + 1] = z * inv;
     }
 }
 
@@ -357,23 +446,52 @@ __global__ void __launch_bounds__(kBalThreads, NQ <= 4 ? 2 : 1) balance_backward
     }
 }
 
-// The tiles of the forward pass: two for every SM, by CTAs of as many warps as fit, so that few partial sums are
-// left (607 rows of them, from four CTAs an SM, took longer to join than to make); with short sequences, which
-// leave most of such a CTA without rows, four by smaller CTAs. No fewer than 16 rows.
+// Lanes of a row: as many as hold it with 16 values each, all 32 beyond 256 experts.
+constexpr int lanes_of(int E) { return E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32; }
+
+// Whether a cluster takes each sequence: up to as many rows, in the mean, as its eight CTAs' warps take in eight
+// turns, if the clusters find an SM for every CTA, else in one turn. One sequence by a cluster and by tiles: 8
+// experts, 4096 rows 5.6 and 8.1 us, 8192 7.8 and 8.9; 128 experts, 512 rows 4.7 and 7.0, 2048 7.1 and 7.9, 4096 12.5 and
+// 8.9; 256 experts, 1024 rows 7.5 and 7.3. 64 sequences of 2048 rows, 128 experts: 35 and 24. A sequence that has
+// most of the rows among many short ones is slow here, not wrong.
+bool short_sequences(const ep_config &c, int32_t n_seq) {
+    const int rows = c.T / n_seq, turn = 8 * (kShortThreads / 32) * (32 / lanes_of(c.E));
+    return rows <= turn || (rows <= 8 * turn && 8 * (int64_t)n_seq <= 152);
+}
+
+// The tiles of the forward pass otherwise: two for every SM, by CTAs of as many warps as fit, so that few partial sums
+// are left (607 rows of them, from four CTAs an SM, took longer to join than to make).
 struct Tiles {
-    int threads, rows, n;
+    int rows, n;
     size_t partials;  // rows of partial sums, at most
 };
 Tiles tiles(const ep_config &c, int32_t n_seq) {
     Tiles t;
-    const bool large = c.T / n_seq >= 256;
-    t.threads = large ? kSumThreads : 128;
-    const int64_t n = 152 * (large ? 2 : 4);
+    const int64_t n = 152 * 2;
     const int64_t rows = (c.T + n - 1) / n;
     t.rows = (int)(rows < 16 ? 16 : rows);
     t.n = (c.T + t.rows - 1) / t.rows;
     t.partials = (size_t)t.n + (size_t)n_seq;
     return t;
+}
+
+// A launch by clusters along the grid's first dimension.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, size_t smem, int ctas, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -389,12 +507,31 @@ struct ForwardCall {
     template <int L, int NQ, bool WIDE>
     cudaError_t run() const {
         const Tiles t = tiles(c, seq.n);
-        const size_t smem = (size_t)(t.threads / 32 + 1) * c.E * sizeof(float);
+        const size_t smem = (size_t)(kSumThreads / 32 + 1) * c.E * sizeof(float);
         static SharedMemoryLimit limit;
         const cudaError_t e = limit.allow(balance_kernel<L, NQ, WIDE>, smem);
         if (e != cudaSuccess) return e;
-        return launch_dependent(balance_kernel<L, NQ, WIDE>, dim3((unsigned)t.n), dim3((unsigned)t.threads), smem, s, seq, c.E, c.k,
+        return launch_dependent(balance_kernel<L, NQ, WIDE>, dim3((unsigned)t.n), dim3(kSumThreads), smem, s, seq, c.E, c.k,
                                 t.rows, logits, idx, part);
+    }
+};
+struct ShortCall {
+    const ep_config &c;
+    const Sequences &seq;
+    const float *logits;
+    const int32_t *idx;
+    int32_t *count;
+    float *load, *prob, *loss;
+    cudaStream_t s;
+    bool wide() const { return c.E % 4 == 0 && on16(logits); }
+    template <int L, int NQ, bool WIDE>
+    cudaError_t run() const {
+        // as many CTAs as leave each warp two turns of rows in the mean
+        int ctas = 1;
+        while (ctas < 8 && (int64_t)ctas * (kShortThreads / 32) * (32 / L) * 2 * seq.n < c.T) ctas *= 2;
+        const size_t smem = (size_t)(kShortThreads / 32 + 1) * c.E * sizeof(float);
+        return launch_clusters(balance_short_kernel<L, NQ, WIDE>, (int64_t)ctas * seq.n, kShortThreads, smem, ctas, s, seq, c.E, c.k,
+                               ctas, logits, idx, count, load, prob, loss);
     }
 };
 struct BackwardCall {
@@ -430,53 +567,35 @@ cudaError_t run_call(const Call &call) {
 
 cudaError_t run_finish(const ep_config &c, const Sequences &seq, const Partials &part, int32_t *count, float *load, float *prob,
                        float *loss, cudaStream_t s) {
-    // Few sequences: CTAs of 32 columns each, up to the eight of a cluster, with 32 rows of partial sums at a time.
-    // Many, of which each has few rows of them: one CTA for all columns.
-    const bool few = seq.n <= current_device_sm_count() / 2;
-    const int ctas = !few ? 1 : c.E >= 256 ? 8 : (c.E + 31) / 32;
-    // threads: as many turns of columns as a sequence has rows of partial sums, about
-    const int share = tiles(c, seq.n).n / seq.n + 1;
-    int threads = few ? 32 : 128;
-    if (few)
-        for (int turns = 1; turns < share && threads < kFinishThreads; turns *= 2) threads *= 2;
-    else
-        while (threads < c.E) threads *= 2;
-    const int columns = (c.E + ctas - 1) / ctas;  // of a CTA, each of which needs a thread
+    // CTAs of 32 columns each, up to the eight of a cluster, with as many turns of rows as a sequence has rows of
+    // partial sums, about
+    const Tiles t = tiles(c, seq.n);
+    const int ctas = c.E >= 256 ? 8 : (c.E + 31) / 32, share = t.n / seq.n + 1, columns = (c.E + ctas - 1) / ctas;
+    int threads = 32;
     while (threads < columns) threads *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas * (unsigned)seq.n);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, balance_finish_kernel, seq, c.E, c.k, tiles(c, seq.n).rows, ctas, part, count, load, prob, loss);
+    for (int turns = 1; turns < share && threads < kFinishThreads; turns *= 2) threads *= 2;
+    return launch_clusters(balance_finish_kernel, (int64_t)ctas * seq.n, threads, 0, ctas, s, seq, c.E, c.k, t.rows, ctas, part, count,
+                           load, prob, loss);
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(const ep_config &c, int32_t n_seq) {
-    return tiles(c, n_seq).partials * (2 * (size_t)c.E + 1) * sizeof(float);
+    return short_sequences(c, n_seq) ? 256 : tiles(c, n_seq).partials * (2 * (size_t)c.E + 1) * sizeof(float);
 }
 
 cudaError_t launch_balance(const ep_config &c, int32_t n_seq, const float *logits, const int32_t *idx, const int32_t *seq_first,
                            const int32_t *seq_len, int32_t *count, float *load, float *prob, float *loss, void *workspace,
                            cudaStream_t s) {
     const Sequences seq{seq_first, seq_len, n_seq, c.T};
+    if (short_sequences(c, n_seq)) return run_call(ShortCall{c, seq, logits, idx, count, load, prob, loss, s});
     const size_t rows = tiles(c, n_seq).partials;
     Partials part;
     part.prob = static_cast<float *>(workspace);
     part.count = reinterpret_cast<int32_t *>(part.prob + rows * c.E);
     part.z = reinterpret_cast<float *>(part.count + rows * c.E);
-    if (c.T > 0) {
-        const cudaError_t e = run_call(ForwardCall{c, seq, logits, idx, part, s});
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = run_call(ForwardCall{c, seq, logits, idx, part, s});
+    if (e != cudaSuccess) return e;
     return run_finish(c, seq, part, count, load, prob, loss, s);
 }
 
