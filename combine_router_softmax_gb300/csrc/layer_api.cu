@@ -165,6 +165,8 @@ ep_status ep_orthogonalize(const ep_ortho_config *cfg, const float *coefficients
     if (!ep::ortho_fits(k, cfg->steps)) return EP_ERR_UNSUPPORTED;
     if (cfg->B == 0) return EP_OK;
     if (!m || !aligned(m, cfg->dtype == EP_F32 ? 4 : 2) || !usable(out)) return EP_ERR_INVALID_ARG;
+    // floats: one matrix's result would lie where another one is still to be read
+    if (m == out && cfg->dtype == EP_F32) return EP_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256)) return EP_ERR_INVALID_ARG;
     if (workspace_bytes < ep::ortho_workspace_bytes(*cfg)) return EP_ERR_CAPACITY;
     return from_cuda(ep::launch_orthogonalize(*cfg, k, m, out, workspace, stream));

@@ -170,7 +170,7 @@ def ep_orthogonalize_workspace_size(cfg: EpOrthoConfig) -> int:
 def ep_orthogonalize(cfg: EpOrthoConfig, m, out, workspace, coefficients=None, stream=None) -> None:
     """out = each matrix of m with its singular values drawn towards one, by cfg.steps Newton-Schulz steps.
 
-    m [B, N, K] (float32, bfloat16 or float16, as cfg says), out bf16 [B, N, K], may be m; coefficients: a sequence of
+    m [B, N, K] (float32, bfloat16 or float16, as cfg says), out bf16 [B, N, K], may be m where that is of 16 bits; coefficients: a sequence of
     cfg.steps triples (a, b, c), None for the default."""
     shape = (cfg.B, cfg.N, cfg.K)
     dev = _device()

@@ -187,7 +187,7 @@ typedef struct ep_ortho_config {
  *                NULL: (3.4445, -4.7750, 2.0315) for all. EP_ERR_UNSUPPORTED where a
  *                singular value of at most 1 could reach 4, or b u + c u^2 (u its square) 31
  * m         : const [B, N, K] of cfg->dtype, aligned to its values
- * out       : bf16 [B, N, K], 16-byte aligned; may be m
+ * out       : bf16 [B, N, K], 16-byte aligned; may be m where that is of 16 bits
  * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes (about 6 bytes a
  *             value and 4 min(N, K)^2 a matrix)
  * A CTA that gives up a bounded wait sets ep_device_error bit 5 (32).

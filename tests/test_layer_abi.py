@@ -219,6 +219,14 @@ def test_ortho_pointers(ep):
     assert ortho(ep, ortho_cfg(ep, B=0), m=None, out=None, ws=None, nbytes=0) == ep.EP_OK
 
 
+def test_ortho_in_place_takes_16_bits(ep):
+    """The results of floats are half as long: the second one would lie in the first matrix."""
+    cfg = ortho_cfg(ep, dtype=0)
+    assert ortho(ep, cfg, nbytes=0) == ep.EP_ERR_INVALID_ARG
+    assert ortho(ep, cfg, out=ctypes.c_void_p(0x20000), nbytes=0) == ep.EP_ERR_CAPACITY
+    assert ortho(ep, ortho_cfg(ep), nbytes=0) == ep.EP_ERR_CAPACITY
+
+
 @pytest.mark.parametrize("k,fits", [
     ((3.4445, -4.7750, 2.0315), True), ((1.5, -0.5, 0.0), True), ((3.9, 0.0, 0.0), True), ((4.1, 0.0, 0.0), False),
     ((1.0, 31.5, -31.5), False), ((1.0, -32.0, 0.5), False), ((float("nan"), 0.0, 0.0), False), ((1.0, float("inf"), 0.0), False),
