@@ -470,7 +470,7 @@ Tiles tiles(const ep_config &c, int32_t n_seq) {
     const int64_t n = 152 * 2;
     const int64_t rows = (c.T + n - 1) / n;
     t.rows = (int)(rows < 16 ? 16 : rows);
-    t.n = (c.T + t.rows - 1) / t.rows;
+    t.n = (int)(((int64_t)c.T + t.rows - 1) / t.rows);
     t.partials = (size_t)t.n + (size_t)n_seq;
     return t;
 }

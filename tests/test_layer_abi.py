@@ -183,6 +183,13 @@ def test_balance_binding_checks_tensors(ep):
         ep.ep_balance(cfg, l.double(), idx, None, None, c, f, f, torch.zeros((1, 2)), None)
 
 
+def test_balance_workspace_of_the_most_rows(ep):
+    """Rows of partial sums: one of every tile, 304 at most, and one for every sequence, of 2 E + 1 values."""
+    for T in (2**31 - 1, 2**31 - 2**20, 2**30):
+        n = ep.ep_balance_workspace_size(layer_cfg(ep, T=T, E=2, k=1), 1)
+        assert 300 * 5 * 4 < n <= 305 * 5 * 4, T
+
+
 # Orthogonalised updates --------------------------------------------------------
 
 def ortho_cfg(ep, **kw):
