@@ -337,7 +337,7 @@ cudaError_t run_rows(const NormArgs &p, int arrays, size_t least, int most, int 
     if (e != cudaSuccess) return e;
     const int per_sm = max_blocks_per_sm((const void *)kernel, threads, smem), sms = current_device_sm_count();
     if (per_sm <= 0 || sms <= 0) return cudaErrorInvalidConfiguration;
-    const int rows = WARP ? (p.T + kNormWarps - 1) / kNormWarps : p.T;
+    const int rows = WARP ? (p.T - 1) / kNormWarps + 1 : p.T;
     *ctas = min(min(rows, per_sm * sms), most);
     return launch_dependent(kernel, dim3((unsigned)*ctas), dim3((unsigned)threads), smem, s, p, stages);
 }

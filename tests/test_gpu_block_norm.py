@@ -199,6 +199,22 @@ def test_many_rows(ep, T, H):
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
+def test_the_most_rows(ep):
+    """2^31 - 1 rows, of 8: the first and the last ones as in a call of their own."""
+    T, H = 2**31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 90 * 2**30:
+        pytest.skip("not enough memory")
+    x, w = torch.ones((T, H), dtype=BF16, device="cuda"), torch.full((H,), 0.5, dtype=BF16, device="cuda")
+    rows = torch.randn((2, 1000, H), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(BF16)
+    x[:1000], x[-1000:] = rows[0], rows[1]
+    n = torch.full((T, H), float("nan"), dtype=BF16, device="cuda")
+    ep.ep_block_norm(ep.EpNormConfig.make(T=T, H=H), x, w_next=w, n=n)
+    want = torch.empty_like(rows)
+    ep.ep_block_norm(ep.EpNormConfig.make(T=2000, H=H), rows.view(2000, H), w_next=w, n=want.view(2000, H))
+    assert torch.equal(n[:1000], want[0]) and torch.equal(n[-1000:], want[1])
+    assert torch.equal(n[T // 2 : T // 2 + 1000], torch.full((1000, H), 0.5, dtype=BF16, device="cuda"))
+
+
 def test_in_place(ep):
     for H in (256, 2992):
         p = Problem(ep, 65, H, gate="token", sigmoid=True, seed=7)
