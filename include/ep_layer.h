@@ -79,8 +79,8 @@ ep_status ep_block_norm_workspace_size(const ep_norm_config *cfg, size_t *bytes)
  *   d_y  = r(y) ew - y r(y)^3 mean(ew y)   (w_post NULL: d_y = ez)
  *   d_w_next = sum_t d_n out r;  d_w_post = sum_t ez y r(y)
  *   d_gate   = scale D z act'(gate), summed over what the gate is broadcast over
- * Sums over rows are fp32 in an order that depends on T, H and the device only:
- * results repeat bit by bit.
+ * Sums over rows are fp32 in an order that depends on the configuration, on which
+ * arguments are given and on the device only: results repeat bit by bit.
  *
  * x, y, w_post, gate, w_next, rstd_* : as for / from ep_block_norm (rstd_post with
  *             w_post, rstd_next with d_n)
@@ -188,8 +188,9 @@ typedef struct ep_ortho_config {
  *                singular value of at most 1 could reach 4, or b u + c u^2 (u its square) 31
  * m         : const [B, N, K] of cfg->dtype, aligned to its values
  * out       : bf16 [B, N, K], 16-byte aligned; may be m where that is of 16 bits
- * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes (about 6 bytes a
- *             value and 4 min(N, K)^2 a matrix)
+ * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes: about 6 bytes a
+ *             value and 4 min(N, K)^2 a matrix, 256 where a matrix stays on the chip
+ *             (min(N, K) <= 128 and max(N, K) <= 2048)
  * A CTA that gives up a bounded wait sets ep_device_error bit 5 (32).
  */
 ep_status ep_orthogonalize_workspace_size(const ep_ortho_config *cfg, size_t *bytes);
