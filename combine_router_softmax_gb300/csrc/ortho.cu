@@ -275,7 +275,8 @@ cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
 }
 
 // The tile of a product: by CTA pairs of 256 x 256 where those are more than the SMs' pairs, else the
-// narrower one with which more SMs have work; a long contraction of few tiles is split over as many CTAs as leave
+// narrower one where that leaves fewer columns for the SM that has most (7 of 1000 x 360 145 -> 142 us, 5 of 384 x 1536
+// 139 -> 134); a long contraction of few tiles is split over as many CTAs as leave
 // each four stages of it (256 x 256 from 7168: 23 us by one CTA a tile).
 template <OrthoOp OP>
 cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
@@ -287,7 +288,8 @@ cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
         for (p.split = 8; p.split > 1; p.split /= 2)
             if (narrow * p.split <= sms && stages >= 4 * p.split) return product<OP, 1, 64, true>(p, q, s);
     }
-    if (narrow <= sms) return product<OP, 1, 64>(p, q, s);
+    const int64_t wide = (int64_t)OrthoWalk<OP, 1, 128>::tiles(p.m, p.n) * p.batch;
+    if ((narrow + sms - 1) / sms < 2 * ((wide + sms - 1) / sms)) return product<OP, 1, 64>(p, q, s);
     return product<OP, 1, 128>(p, q, s);
 }
 
