@@ -2,13 +2,14 @@
 //
 // As three products a step, launched one after the other, a matrix of 128 rows takes 6 us a product whatever its
 // work: launch, first copies, last stores. Up to 128 rows (of the wide form) X stays on the chip instead: a cluster of
-// up to eight CTAs takes a matrix, each CTA 256 of its columns, and only the sums of A's parts pass between them.
+// up to sixteen CTAs takes a matrix, each CTA 256 of its columns, and only the sums of A's parts pass between them.
 // X itself is fp32, in registers (a thread has 64 columns of a row), so that there is no lo; its halves, rounded as
 // in ortho_gemm.cuh, lie in shared memory and serve as both operands of A = X X^T (128 bytes of a row's columns,
 // swizzled) and, read the other way, as the second of B X. A and then B lie in one place.
 //
 // What bounds it is the chain of a step: three waits for a few MMAs, three epilogues, as many fences and barriers.
-// 64 matrices of 128 x 256 take 27 us for five steps (100 by products of their own).
+// 64 matrices of 128 x 256 take 27 us for five steps (84 by products of their own, in a graph), 1024 of them 193 (1119), one
+// of 128 x 4096 by sixteen CTAs 56 (76), 32 of those 280 (431).
 #include "ortho_values.cuh"
 
 namespace ep {
@@ -17,7 +18,7 @@ namespace {
 
 constexpr int kFusedThreads = 512;
 constexpr int kFusedRows = 128, kFusedCols = 256;  // of a CTA
-constexpr int kFusedCtas = 8;                      // of a cluster, at most
+constexpr int kFusedCtas = 16;                     // of a cluster, at most
 constexpr int kBlock = kFusedRows * 128;           // bytes of 64 columns
 constexpr int kHalves = kFusedCols / 64 * kBlock;  // of X's halves
 constexpr int kSquare = kFusedRows / 64 * kBlock;  // of A, B
@@ -287,13 +288,17 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
             for (int i = tid; i < rows * (kFusedRows / 4); i += kFusedThreads) {
                 const int r = r0 + i / (kFusedRows / 4), col = i % (kFusedRows / 4) * 4;
                 if (r >= kFusedRows) break;
-                float4 f[kFusedCtas];  // asked for together
-#pragma unroll
-                for (int q = 0; q < kFusedCtas; ++q)
-                    f[q] = q < ctas ? ld_cluster_f32x4(cluster_smem_u32(part + part_at(r, col), q)) : make_float4(0, 0, 0, 0);
                 float x[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int q = 0; q < kFusedCtas; ++q) x[0] += f[q].x, x[1] += f[q].y, x[2] += f[q].z, x[3] += f[q].w;
+                for (int q0 = 0; q0 < kFusedCtas; q0 += 8) {
+                    if (q0 >= ctas) break;
+                    float4 f[8];  // asked for together
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        f[q] = q0 + q < ctas ? ld_cluster_f32x4(cluster_smem_u32(part + part_at(r, col), q0 + q)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[0] += f[q].x, x[1] += f[q].y, x[2] += f[q].z, x[3] += f[q].w;
+                }
                 const bool mine = r >= col && r < col + 4;
                 float e = 0.0f;
 #pragma unroll
@@ -411,6 +416,10 @@ cudaError_t run_fused(const FusedParams &p, int batch, cudaStream_t s) {
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(ortho_fused_kernel<V>, smem);
     if (e != cudaSuccess) return e;
+    if (p.ctas > 8) {  // more than every device takes has to be asked for
+        const cudaError_t e = cudaFuncSetAttribute(ortho_fused_kernel<V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)batch * (unsigned)p.ctas);
     cfg.blockDim = dim3(kFusedThreads);

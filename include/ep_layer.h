@@ -190,7 +190,7 @@ typedef struct ep_ortho_config {
  * out       : bf16 [B, N, K], 16-byte aligned; may be m where that is of 16 bits
  * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes: about 6 bytes a
  *             value and 4 min(N, K)^2 a matrix, 256 where a matrix stays on the chip
- *             (min(N, K) <= 128 and max(N, K) <= 2048)
+ *             (min(N, K) <= 128 and max(N, K) <= 4096)
  * A CTA that gives up a bounded wait sets ep_device_error bit 5 (32).
  */
 ep_status ep_orthogonalize_workspace_size(const ep_ortho_config *cfg, size_t *bytes);

@@ -99,6 +99,20 @@ def test_against_64_bits(ep, B, N, K, dtype):
     check(run(ep, m), m)
 
 
+@pytest.mark.parametrize("B,N,K", [(1, 128, 4096), (11, 128, 4096), (3, 4096, 33), (2, 7, 2300), (2, 3100, 128), (1, 100, 4097), (20, 72, 2049), (2, 4100, 16)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_long_rows_of_few(ep, B, N, K, dtype):
+    """Up to sixteen CTAs a matrix, more of them than run at a time, and just beyond."""
+    m = normal(B, N, K, seed=N + K, dtype=dtype)
+    check(run(ep, m), m)
+
+
+@pytest.mark.parametrize("B,N,K", [(7, 1000, 360), (5, 384, 1500), (3, 700, 2000)])
+def test_several_tiles_a_cta(ep, B, N, K):
+    m = normal(B, N, K, seed=2)
+    check(run(ep, m), m)
+
+
 @pytest.mark.parametrize("B,N,K", [(6, 1100, 1200), (6, 1289, 1100), (12, 600, 2000)])
 def test_pairs(ep, B, N, K):
     """As many tiles as CTA pairs take: two CTAs a tile, ragged in both directions, and several tiles a pair."""
