@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
 }
 
 struct Backward {
-    template <bool F32, int FORM, bool WARP, int NV, int THREADS>
+    static constexpr bool kAhead = false;
+    template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>
     static auto kernel() {
         return block_norm_backward_kernel<F32, FORM, WARP, NV, THREADS>;
     }

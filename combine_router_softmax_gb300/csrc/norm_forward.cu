@@ -1,7 +1,7 @@
 // norm_forward.cu -- the norms around a block, forward (the kernels' frame: norm_rows.cuh).
 //
 // 16384 rows of 4096 with a plain residual take 80 us, 79 at the copy rate. With a norm of the block's result and a gate a row
-// has two sums over the CTA instead of one, and twice the instructions: 4096 of 7168 46 us, 35 at the copy rate (issue slots
+// has two sums over the CTA instead of one, and twice the instructions: 4096 of 7168 44 us, 35 at the copy rate (issue slots
 // 57 % busy, the rest waits for copies and barriers). One row of 7168: 2.4 us, a launch.
 #include "norm_rows.cuh"
 
@@ -9,7 +9,9 @@ namespace ep {
 
 namespace {
 
-template <bool F32, int FORM, bool WARP, int NV, int THREADS>
+// AHEAD: a row's two sums over the CTA, y's and out's, are not one behind the other, but the next row's first is made with
+// this row's second. That is one barrier a row, and y is asked for a row further ahead.
+template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ? 3 : 1) block_norm_kernel(const NormArgs p, int stages) {
     constexpr bool kY = FORM & kFormY, kPost = FORM & kFormPost, kGate = FORM & kFormGate, kKept = kept_factors(THREADS);
     __shared__ Scratch scratch;
@@ -20,7 +22,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ?
     const Place<WARP> at;
     const bool next = p.n != nullptr, element = kGate && p.kind == EP_GATE_ELEMENT, token = kY && !kGate && p.kind == EP_GATE_TOKEN;
     const bool factors = kPost || (kGate && !element);
-    const Ring<F32, NV> ring(ring_smem, stages, kY, element, false, false);
+    const Ring<F32, NV> ring(ring_smem, stages, kY, element, false, false, AHEAD);
+    const auto ask_y = [&](int64_t t, uint32_t place) {
+        if (t >= p.T) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i * at.stride + at.first < p.vecs) ring.copy(place, 0, i, p.y, (size_t)t * p.vecs + at.first + i * at.stride);
+    };
     const auto ask = [&](int64_t t, uint32_t stage) {
         if (t < p.T) {
             const size_t row = (size_t)t * p.vecs + at.first;
@@ -28,15 +36,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ?
             for (int i = 0; i < NV; ++i) {
                 if (i * at.stride + at.first >= p.vecs) continue;
                 ring.copy_stream(stage, 0, i, p.x, row + i * at.stride);
-                if constexpr (kY) ring.copy(stage, ring.y(), i, p.y, row + i * at.stride);
+                if constexpr (kY && !AHEAD) ring.copy(stage, ring.y(), i, p.y, row + i * at.stride);
                 if (kGate && element) ring.copy(stage, ring.gate, i, p.gate, row + i * at.stride);
             }
         }
         copies_commit();
     };
-    for (int s = 0; s < stages; ++s) ask((int64_t)at.row + (int64_t)s * at.step, ring.stage(s));
+    const auto y_squares = [&](uint32_t place) {
+        uint64_t squares = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i * at.stride + at.first >= p.vecs) continue;
+            const V8 v = unpack8(ring.get(place, 0, i));
+            dot(squares, v, v);
+        }
+        return total(squares);
+    };
+    const auto root = [&](float sum) { return rsqrtf(fmaf(sum, p.inv_h, p.eps)); };
+    if constexpr (AHEAD) ask_y(at.row, ring.y_place(0));
+    for (int s = 0; s < stages; ++s) {
+        if constexpr (AHEAD) ask_y((int64_t)at.row + (int64_t)(s + 1) * at.step, ring.y_place(s + 1));
+        ask((int64_t)at.row + (int64_t)s * at.step, ring.stage(s));
+    }
     if (kKept && factors) ring.template keep_factors<kPost, kGate>(p, at.first, at.stride);
-    int s = 0, turn = 0;
+    int s = 0, turn = 0, place = 0;  // this row's places: of the stage, and (AHEAD) of y
+    float r_y = 1.0f;
+    if constexpr (AHEAD) {
+        copies_wait(stages - 1);
+        if (at.row < p.T) r_y = root(group_sum<WARP>(y_squares(ring.y_place(0)), scratch, turn));
+    }
     float token_gate = token && at.row < p.T ? static_cast<const float *>(p.gate)[at.row] : 1.0f, slope;
     for (int64_t t = at.row; t < p.T; t += at.step) {
         const size_t row = (size_t)t * p.vecs + at.first;
@@ -44,18 +72,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ?
         const float scale = token ? p.scale * gate_act(token_gate, p.sigmoid, slope) : p.scale;
         if (token && t + at.step < p.T) token_gate = static_cast<const float *>(p.gate)[t + at.step];
         copies_wait(stages - 1);
-        float r_y = 1.0f;
-        if constexpr (kPost) {
-            uint64_t squares = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (i * at.stride + at.first >= p.vecs) continue;
-                const V8 v = unpack8(ring.get(stage, ring.y(), i));
-                dot(squares, v, v);
-            }
-            r_y = rsqrtf(fmaf(group_sum<WARP>(total(squares), scratch, turn), p.inv_h, p.eps));
-            if (p.rstd_post && at.first == 0) p.rstd_post[t] = r_y;
-        }
+        const uint32_t y = AHEAD ? ring.y_place(place) : stage + ring.y();
+        if constexpr (kPost && !AHEAD) r_y = root(group_sum<WARP>(y_squares(y), scratch, turn));
+        if (kPost && p.rstd_post && at.first == 0) p.rstd_post[t] = r_y;
         V8 out[NV];
         uint64_t squares = 0;
 #pragma unroll
@@ -64,7 +83,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ?
             if (v >= p.vecs) continue;
             out[i] = ring.get_stream(stage, 0, i);
             if constexpr (kY) {
-                V8 z = unpack8(ring.get(stage, ring.y(), i));
+                V8 z = unpack8(ring.get(y, 0, i));
                 if constexpr (kPost) times(z, r_y);
                 if (factors) times(z, ring.template get_factors<kKept, kPost, kGate>(p, i, v));
                 if (kGate && element) {
@@ -77,10 +96,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : THREADS == 256 ?
             }
             dot(squares, out[i], out[i]);
         }
+        if constexpr (AHEAD) ask_y(t + (int64_t)(stages + 1) * at.step, y);
         ask(t + (int64_t)stages * at.step, stage);
         s = s + 1 == stages ? 0 : s + 1;
-        if (!next) continue;
-        const float r = rsqrtf(fmaf(group_sum<WARP>(total(squares), scratch, turn), p.inv_h, p.eps));
+        float r;
+        if constexpr (AHEAD) {
+            place = place == stages ? 0 : place + 1;
+            // the row after the last one: what lies there is not used
+            float both[2] = {total(squares), y_squares(ring.y_place(place))};
+            group_sum<WARP, 2>(both, scratch, turn);
+            r = root(both[0]);
+            r_y = root(both[1]);
+            if (!next) continue;
+        } else {
+            if (!next) continue;
+            r = root(group_sum<WARP>(total(squares), scratch, turn));
+        }
         if (p.rstd_next && at.first == 0) p.rstd_next[t] = r;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -172,9 +203,10 @@ __global__ void __launch_bounds__(1024) block_norm_few_kernel(const NormArgs p) 
 }
 
 struct Forward {
-    template <bool F32, int FORM, bool WARP, int NV, int THREADS>
+    static constexpr bool kAhead = true;
+    template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>
     static auto kernel() {
-        return block_norm_kernel<F32, FORM, WARP, NV, THREADS>;
+        return block_norm_kernel<F32, FORM, WARP, NV, THREADS, AHEAD>;
     }
 };
 

@@ -239,16 +239,18 @@ struct Ring {
     uint32_t base, array_bytes, piece_bytes, stage_bytes;
     uint32_t gate, d_out, d_n;  // offsets within a stage; x is first, y next
     uint32_t factors;           // behind the stages: this thread's column factors, floats
-    __device__ Ring(const void *smem, int stages, bool y, bool element, bool d, bool n) {
+    uint32_t y_ahead;           // y's places where it is a row further ahead: stages + 1 of them, between the two
+    __device__ Ring(const void *smem, int stages, bool y, bool element, bool d, bool n, bool ahead = false) {
         piece_bytes = blockDim.x * 16;
         array_bytes = piece_bytes * NV;
         base = smem_u32(smem) + threadIdx.x * 16;
-        uint32_t at = array_bytes * kStream + (y ? array_bytes : 0);
+        uint32_t at = array_bytes * kStream + (y && !ahead ? array_bytes : 0);
         gate = at, at += element ? array_bytes : 0;
         d_out = at, at += d ? array_bytes * kStream : 0;
         d_n = at, at += n ? array_bytes : 0;
         stage_bytes = at;
-        factors = base + stages * at;
+        y_ahead = base + stages * at;
+        factors = y_ahead + (ahead ? (stages + 1) * array_bytes : 0);
     }
     // What of z = f y r(y) is the same for all rows, a value a column: the norm's weights and a channel gate's
     // factor. KEPT: as floats, as they would be unpacked, offset and put through the sigmoid for every row.
@@ -297,6 +299,7 @@ struct Ring {
     }
     __device__ __forceinline__ uint32_t stage(int s) const { return base + s * stage_bytes; }
     __device__ __forceinline__ uint32_t y() const { return array_bytes * kStream; }
+    __device__ __forceinline__ uint32_t y_place(int i) const { return y_ahead + i * array_bytes; }
     __device__ __forceinline__ void copy(uint32_t stage, uint32_t array, int i, const void *p, size_t at) const {
         copy16(stage + array + i * piece_bytes, static_cast<const uint4 *>(p) + at);
     }
@@ -320,18 +323,19 @@ __host__ __device__ constexpr bool kept_factors(int threads) { return threads <=
 // Shared memory that the rows in flight of a CTA may take.
 constexpr size_t kRingBytes = 225 * 1024;
 
-// Launches the kernel that LAUNCH::kernel<FORM, WARP, NV, THREADS>() names, for rows of p.vecs vectors, with two rows
+// Launches the kernel that LAUNCH::kernel<F32, FORM, WARP, NV, THREADS, AHEAD>() names, for rows of p.vecs vectors, with two rows
 // in flight (three took 56 us instead of 50 for 4096 rows of 7168: what shared memory they take is L1's, where
 // the weights are read from), one where two do not fit. least: bytes of shared memory that it needs anyway.
-template <typename LAUNCH, bool F32, int FORM, bool WARP, int NV, int THREADS>
+template <typename LAUNCH, bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD = false>
 cudaError_t run_rows(const NormArgs &p, int arrays, size_t least, int most, int *ctas, cudaStream_t s) {
-    const auto kernel = LAUNCH::template kernel<F32, FORM, WARP, NV, THREADS>();
+    const auto kernel = LAUNCH::template kernel<F32, FORM, WARP, NV, THREADS, AHEAD>();
     const int threads = WARP ? THREADS : (p.vecs + 32 * NV - 1) / (32 * NV) * 32;
     const size_t stage = (size_t)arrays * NV * threads * sizeof(uint4);
     const bool kept = kept_factors(THREADS) && (FORM & kFormPost || (FORM & kFormGate && p.kind == EP_GATE_CHANNEL));
     const size_t factors = kept ? (size_t)2 * NV * threads * sizeof(uint4) : 0;
-    const int stages = 2 * stage + factors <= kRingBytes ? 2 : 1;
-    const size_t smem = stages * stage + factors > least ? stages * stage + factors : least;
+    const size_t extra = factors + (AHEAD ? (size_t)NV * threads * sizeof(uint4) : 0);
+    const int stages = 2 * stage + extra <= kRingBytes ? 2 : 1;
+    const size_t smem = stages * stage + extra > least ? stages * stage + extra : least;
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -347,6 +351,16 @@ cudaError_t run_form(const NormArgs &p, int arrays, bool sums, int most, int *ct
     if (p.vecs <= 32)
         return run_rows<LAUNCH, F32, FORM, true, 1, 32 * kNormWarps>(p, arrays, sums ? (size_t)p.vecs * 64 : 0, most, ctas, s);
     if (p.vecs <= 256) return run_rows<LAUNCH, F32, FORM, false, 1, 256>(p, arrays, 0, most, ctas, s);
+    // AHEAD from four rows a CTA on, as its first row takes one more barrier (bf16, 7168 wide with a channel gate: 600 rows 9.9
+    // -> 10.6 us, 1216 16.6 -> 16.7, 4096 45.5 -> 44.0; float 83.4 -> 73.5, with a gate of elements 99 -> 79). What more of y it
+    // holds takes bf16 rows beside a gate of elements from L1 (7168 wide 48.4 -> 54.5), and more than 8192 columns (16384 51 -> 56).
+    if constexpr (LAUNCH::kAhead && FORM & kFormPost) {
+        if (p.T >= 8 * current_device_sm_count() && (F32 || p.kind != EP_GATE_ELEMENT || p.vecs <= 512)) {
+            if (p.vecs <= 512) return run_rows<LAUNCH, F32, FORM, false, 2, 256, true>(p, arrays, 0, most, ctas, s);
+            if (p.vecs <= 1024) return run_rows<LAUNCH, F32, FORM, false, 2, 512, true>(p, arrays, 0, most, ctas, s);
+            if constexpr (F32) return run_rows<LAUNCH, F32, FORM, false, 2, 1024, true>(p, arrays, 0, most, ctas, s);
+        }
+    }
     if (p.vecs <= 512) return run_rows<LAUNCH, F32, FORM, false, 2, 256>(p, arrays, 0, most, ctas, s);
     if (p.vecs <= 1024) return run_rows<LAUNCH, F32, FORM, false, 2, 512>(p, arrays, 0, most, ctas, s);
     return run_rows<LAUNCH, F32, FORM, false, 2, 1024>(p, arrays, 0, most, ctas, s);

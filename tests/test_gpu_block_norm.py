@@ -199,6 +199,19 @@ def test_many_rows(ep, T, H):
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
+@pytest.mark.parametrize("T,H", [(1216, 2056), (1300, 4104), (1217, 8200), (2500, 7168)])
+@pytest.mark.parametrize("gate", KINDS)
+@pytest.mark.parametrize("f32", [False, True])
+def test_many_rows_of_a_normed_block(ep, T, H, gate, f32):
+    """Rows whose first sum is made with the second one of the row before; then in place."""
+    p = Problem(ep, T, H, gate=gate, sigmoid=gate != "channel", f32=f32, seed=T)
+    f = p.forward()
+    check({**f, **p.backward(f)}, p.reference())
+    q = Problem(ep, T, H, gate=gate, sigmoid=gate != "channel", f32=f32, seed=T)
+    h = q.forward(out=q.x, n=q.y)
+    assert all(torch.equal(h[k], f[k]) for k in f)
+
+
 def test_the_most_rows(ep):
     """2^31 - 1 rows, of 8: the first and the last ones as in a call of their own."""
     T, H = 2**31 - 1, 8
