@@ -94,14 +94,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
                 }
                 times(D[i], rn);
                 gn[i] = unpack8(ring.get(stage, ring.d_n, i));
-                if (more) {
-                    ring.copy_stream(stage, 0, i, p.x, ahead + i * at.stride);
-                    ring.copy(stage, ring.d_n, i, p.d_n, ahead + i * at.stride);
-                }
                 add_product(acc_next[i], gn[i], D[i]);
                 weigh(gn[i], __ldg(p.w_next + v), p.offset);
                 dot(sum, gn[i], D[i]);
             }
+            if (more)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if (i * at.stride + at.first >= p.vecs) continue;
+                    ring.copy_stream(stage, 0, i, p.x, ahead + i * at.stride);
+                    ring.copy(stage, ring.d_n, i, p.d_n, ahead + i * at.stride);
+                }
             c = group_sum<WARP>(total(sum), scratch, turn) * p.inv_h;
         }
         uint64_t sum_y = 0, sum_gate = 0;
@@ -112,7 +115,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
             V8 d;
             if (has_d) {
                 d = ring.get_stream(stage, ring.d_out, i);
-                if (more) ring.copy_stream(stage, ring.d_out, i, p.d_out, ahead + i * at.stride);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d.p[j] = 0;
@@ -160,6 +162,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
                 D[i] = d;
             }
         }
+        if (more && has_d)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i * at.stride + at.first < p.vecs) ring.copy_stream(stage, ring.d_out, i, p.d_out, ahead + i * at.stride);
         if constexpr (kY) {
             float s_y = total(sum_y), s_gate = total(sum_gate);
             const bool token_sum = token && p.d_gate;

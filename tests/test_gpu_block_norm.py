@@ -212,6 +212,21 @@ def test_many_rows_of_a_normed_block(ep, T, H, gate, f32):
     assert all(torch.equal(h[k], f[k]) for k in f)
 
 
+@pytest.mark.parametrize("T,H", [(5, 72), (400, 1000), (300, 7168)])
+def test_float_stream_on_16_bytes(ep, T, H):
+    """Aligned to 16 bytes, as is asked for, and not to 32."""
+    p = Problem(ep, T, H, gate="channel", f32=True, seed=9)
+    f = p.forward()
+    a = p.backward(f)
+    off = lambda: torch.full((T * H + 4,), float("nan"), device="cuda")[4:].view(T, H)  # noqa: E731
+    assert off().data_ptr() % 32 == 16
+    for name in ("x", "d_out"):
+        setattr(p, name, off().copy_(getattr(p, name)))
+    g = p.forward(out=off())
+    b = p.backward(g, d_x=off())
+    assert all(torch.equal(g[k], f[k]) for k in f) and all(torch.equal(b[k], a[k]) for k in a)
+
+
 def test_the_most_rows(ep):
     """2^31 - 1 rows, of 8: the first and the last ones as in a call of their own."""
     T, H = 2**31 - 1, 8
