@@ -11,7 +11,7 @@ namespace {
 // gate: its factor and slope come with the finish, as they are the same for all rows) or ez y r(y) for d_w_post. A
 // thread holds those of its columns over all its rows.
 template <bool F32, int FORM, bool WARP, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_backward_kernel(const NormArgs p, int stages) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 320 ? 2 : 1) block_norm_backward_kernel(const NormArgs p, int stages) {
     constexpr bool kY = FORM & kFormY, kPost = FORM & kFormPost, kGate = FORM & kFormGate, kKept = kept_factors(THREADS);
     __shared__ Scratch scratch;
     extern __shared__ uint4 ring_smem[];  // at the end, WARP: [sums][H] of the CTA
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
         // Floats: a piece's place is filled for the row after next as soon as the piece has been read for the last
         // time, as two rows of them are too little in flight otherwise (8192 rows of 7168, both directions, 411 -> 365
         // us; a stream of bf16, for which it is more instructions alone, 254 -> 271: there all at the row's end).
-        constexpr bool kEarly = F32;
+        constexpr bool kEarly = F32;  // Backward::early
         const int64_t t_ahead = t + (int64_t)stages * at.step;
         const bool more = kEarly && t_ahead < p.T;
         const size_t ahead = (size_t)t_ahead * p.vecs + at.first;
@@ -236,6 +236,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) block_norm_ba
 
 struct Backward {
     static constexpr bool kAhead = false;
+    template <bool F32>
+    static constexpr bool early() {
+        return F32;
+    }
     template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>
     static auto kernel() {
         return block_norm_backward_kernel<F32, FORM, WARP, NV, THREADS>;

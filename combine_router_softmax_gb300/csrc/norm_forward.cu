@@ -204,6 +204,10 @@ __global__ void __launch_bounds__(1024) block_norm_few_kernel(const NormArgs p) 
 
 struct Forward {
     static constexpr bool kAhead = true;
+    template <bool F32>
+    static constexpr bool early() {
+        return false;
+    }
     template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>
     static auto kernel() {
         return block_norm_kernel<F32, FORM, WARP, NV, THREADS, AHEAD>;

@@ -340,7 +340,11 @@ cudaError_t run_rows(const NormArgs &p, int arrays, size_t least, int most, int 
     const bool kept = kept_factors(THREADS) && (FORM & kFormPost || (FORM & kFormGate && p.kind == EP_GATE_CHANNEL));
     const size_t factors = kept ? (size_t)2 * NV * threads * sizeof(uint4) : 0;
     const size_t extra = factors + (AHEAD ? (size_t)NV * threads * sizeof(uint4) : 0);
-    const int stages = 2 * stage + extra <= kRingBytes ? 2 : 1;
+    int stages = 2 * stage + extra <= kRingBytes ? 2 : 1;
+    // Where a place is filled again at once, one row in flight if two of them take more than half an SM's shared memory: it has
+    // two CTAs then, or L1 has the rest (backward, 4096 rows of 4096 floats 76 -> 74 us, with a gate of elements 95 -> 79, of
+    // 7168 130 -> 123; of 2048, which stay with two, 39 and 40).
+    if (LAUNCH::template early<F32>() && 2 * stage + extra > 110 * 1024) stages = 1;
     const size_t smem = stages * stage + extra > least ? stages * stage + extra : least;
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(kernel, smem);
@@ -368,6 +372,11 @@ cudaError_t run_form(const NormArgs &p, int arrays, bool sums, int most, int *ct
         }
     }
     if (p.vecs <= 512) return run_rows<LAUNCH, F32, FORM, false, 2, 256>(p, arrays, 0, most, ctas, s);
+    // Backward: by their registers two CTAs of 320 threads fit an SM, by their shared memory with up to four arrays or with one
+    // stage (4096 rows of 5120, normed, bf16 82 -> 69 us; with five arrays, where one fits, 77 -> 115; as 384 threads 6144
+    // wide 76 -> 112).
+    if constexpr (!LAUNCH::kAhead)
+        if (p.vecs <= 640 && (F32 || arrays <= 4)) return run_rows<LAUNCH, F32, FORM, false, 2, 320>(p, arrays, 0, most, ctas, s);
     if (p.vecs <= 1024) return run_rows<LAUNCH, F32, FORM, false, 2, 512>(p, arrays, 0, most, ctas, s);
     return run_rows<LAUNCH, F32, FORM, false, 2, 1024>(p, arrays, 0, most, ctas, s);
 }

@@ -212,6 +212,15 @@ def test_many_rows_of_a_normed_block(ep, T, H, gate, f32):
     assert all(torch.equal(h[k], f[k]) for k in f)
 
 
+@pytest.mark.parametrize("post,gate", [(True, "none"), (True, "channel"), (True, "element"), (False, "token"), (False, "element")])
+@pytest.mark.parametrize("H", [4096, 4104, 5120, 5128])
+@pytest.mark.parametrize("f32", [False, True])
+def test_rows_of_two_ctas_an_sm(ep, post, gate, H, f32):
+    p = Problem(ep, 620, H, post=post, gate=gate, f32=f32, seed=H)
+    f = p.forward()
+    check({**f, **p.backward(f)}, p.reference())
+
+
 @pytest.mark.parametrize("T,H", [(5, 72), (400, 1000), (300, 7168)])
 def test_float_stream_on_16_bytes(ep, T, H):
     """Aligned to 16 bytes, as is asked for, and not to 32."""
