@@ -1,6 +1,7 @@
 // norm_backward.cu -- the norms around a block, backward (the kernels' frame: norm_rows.cuh).
 //
-// 16384 rows of 4096 with a plain residual: 126 us, 119 at the copy rate; joining the CTAs' sums over rows 5.
+// 16384 rows of 4096 with a plain residual, bf16: 140 us with the joining of the CTAs' sums over rows (5), 119 at the copy
+// rate; normed as well 155. 4096 of 7168: 67, normed and gated by channels 87 (52); fp32 110 and 123 (78).
 #include "norm_rows.cuh"
 
 namespace ep {
@@ -64,12 +65,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 320 ? 2 : 1) block_norm_ba
         const float scale = token ? p.scale * gate_act(token_gate, p.sigmoid, token_slope) : p.scale;  // with a token's gate
         scalars(t + at.step);
         copies_wait(stages - 1);
-        // Floats: a piece's place is filled for the row after next as soon as the piece has been read for the last
-        // time, as two rows of them are too little in flight otherwise (8192 rows of 7168, both directions, 411 -> 365
-        // us; a stream of bf16, for which it is more instructions alone, 254 -> 271: there all at the row's end).
-        constexpr bool kEarly = F32;  // Backward::early
+        // A piece's place is filled for a row ahead as soon as the pieces of its array have been read for the last time, as
+        // otherwise too little is in flight (floats, 8192 rows of 7168, both directions, 411 -> 365 us; bf16, 16384 of 4096,
+        // normed, backward 165 -> 155, 4096 of 2048 28.3 -> 26.9).
         const int64_t t_ahead = t + (int64_t)stages * at.step;
-        const bool more = kEarly && t_ahead < p.T;
+        const bool more = t_ahead < p.T;
         const size_t ahead = (size_t)t_ahead * p.vecs + at.first;
         // D: first out r(out), which is near 1 at any size of the values, as r^3 is not; gn beside it
         V8 D[NV], gn[NV];
@@ -192,10 +192,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 320 ? 2 : 1) block_norm_ba
                 st_v4(p.d_y + row + i * at.stride, pack8(D[i]));
             }
         }
-        if (kEarly)
-            copies_commit();
-        else
-            ask(t_ahead, stage);
+        copies_commit();
         s = s + 1 == stages ? 0 : s + 1;
     }
     // the CTA's row of partial sums
@@ -237,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 320 ? 2 : 1) block_norm_ba
 struct Backward {
     static constexpr bool kAhead = false;
     template <bool F32>
-    static constexpr bool early() {
+    static constexpr bool one_row() {
         return F32;
     }
     template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>

@@ -1,6 +1,6 @@
 // norm_forward.cu -- the norms around a block, forward (the kernels' frame: norm_rows.cuh).
 //
-// 16384 rows of 4096 with a plain residual take 80 us, 79 at the copy rate. With a norm of the block's result and a gate a row
+// 16384 rows of 4096 with a plain residual take 85 us, 79 at the copy rate. With a norm of the block's result and a gate a row
 // has two sums over the CTA instead of one, and twice the instructions: 4096 of 7168 44 us, 35 at the copy rate (issue slots
 // 57 % busy, the rest waits for copies and barriers). One row of 7168: 2.4 us, a launch.
 #include "norm_rows.cuh"
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(1024) block_norm_few_kernel(const NormArgs p) 
 struct Forward {
     static constexpr bool kAhead = true;
     template <bool F32>
-    static constexpr bool early() {
+    static constexpr bool one_row() {
         return false;
     }
     template <bool F32, int FORM, bool WARP, int NV, int THREADS, bool AHEAD>

@@ -341,10 +341,10 @@ cudaError_t run_rows(const NormArgs &p, int arrays, size_t least, int most, int 
     const size_t factors = kept ? (size_t)2 * NV * threads * sizeof(uint4) : 0;
     const size_t extra = factors + (AHEAD ? (size_t)NV * threads * sizeof(uint4) : 0);
     int stages = 2 * stage + extra <= kRingBytes ? 2 : 1;
-    // Where a place is filled again at once, one row in flight if two of them take more than half an SM's shared memory: it has
-    // two CTAs then, or L1 has the rest (backward, 4096 rows of 4096 floats 76 -> 74 us, with a gate of elements 95 -> 79, of
-    // 7168 130 -> 123; of 2048, which stay with two, 39 and 40).
-    if (LAUNCH::template early<F32>() && 2 * stage + extra > 110 * 1024) stages = 1;
+    // Backward, floats: one row in flight if two of them take more than half an SM's shared memory: it has
+    // two CTAs then, or L1 has the rest (4096 rows of 4096 76 -> 74 us, with a gate of elements 95 -> 79, of
+    // 7168 130 -> 123; of 2048, which stay with two, 39 and 40; bf16 as often slower as faster).
+    if (LAUNCH::template one_row<F32>() && 2 * stage + extra > 110 * 1024) stages = 1;
     const size_t smem = stages * stage + extra > least ? stages * stage + extra : least;
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(kernel, smem);
