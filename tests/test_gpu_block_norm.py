@@ -236,6 +236,16 @@ def test_float_stream_on_16_bytes(ep, T, H):
     assert all(torch.equal(g[k], f[k]) for k in f) and all(torch.equal(b[k], a[k]) for k in a)
 
 
+@pytest.mark.parametrize("T", [152, 153, 304, 305, 608, 609, 1217])
+@pytest.mark.parametrize("H", [264, 1000, 2048, 4096])
+def test_as_many_rows_as_run_at_once(ep, T, H):
+    """And one more: a CTA for each of them, or rows in turns."""
+    p = Problem(ep, T, H, gate="channel", f32=T % 2 == 0, seed=T)
+    f = p.forward()
+    r = p.reference()
+    check(f, {k: r[k] for k in f})
+
+
 def test_the_most_rows(ep):
     """2^31 - 1 rows, of 8: the first and the last ones as in a call of their own."""
     T, H = 2**31 - 1, 8
