@@ -123,6 +123,12 @@ def test_against_64_bits(ep, E, k, T):
     run(Problem(ep, T, E, k, seed=E + T), d_in=T != 50)
 
 
+@pytest.mark.parametrize("E,k", [(3, 1), (37, 6), (150, 8), (203, 2), (511, 8), (1001, 4)])
+def test_rows_on_no_boundary(ep, E, k):
+    """Rows of no multiple of four logits, by tiles of many and with ends of sequences inside, gradients added in place."""
+    run(Problem(ep, 20001, E, k, first=[0, 7000, 7013, 20001], seed=E))
+
+
 @pytest.mark.parametrize("T,first,length", [
     (100, [0, 100], None),
     (100, [0, 0, 0, 37, 38, 38, 100, 100], None),           # empty ones, one of a single row
