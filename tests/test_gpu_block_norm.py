@@ -246,6 +246,15 @@ def test_as_many_rows_as_run_at_once(ep, T, H):
     check(f, {k: r[k] for k in f})
 
 
+@pytest.mark.parametrize("T", [300, 1300])
+@pytest.mark.parametrize("H", [1000, 4096, 7168])
+def test_joined_without_a_next_norm(ep, T, H):
+    p = Problem(ep, T, H, gate="token", sigmoid=True, f32=True, next=False, seed=H)
+    f = p.forward(rstd_post=None)
+    assert torch.equal(f["out"], p.forward()["out"])
+    check({"out": f["out"]}, {"out": p.reference()["out"]})
+
+
 def test_the_most_rows(ep):
     """2^31 - 1 rows, of 8: the first and the last ones as in a call of their own."""
     T, H = 2**31 - 1, 8
