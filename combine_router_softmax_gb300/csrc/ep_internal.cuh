@@ -379,7 +379,7 @@ cudaError_t launch_balance_backward(const ep_config &c, int32_t n_seq, const flo
 
 // Orthogonalised updates (ortho.cu); k: [steps][3] on the host.
 size_t ortho_workspace_bytes(const ep_ortho_config &c);
-bool ortho_fits(const float *k, int32_t steps);
+bool ortho_fits(const float *k, int32_t steps);  // whether the operands' range takes the steps
 cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, void *workspace,
                                  cudaStream_t s);
 

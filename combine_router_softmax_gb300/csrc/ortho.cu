@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kSplitThreads) ortho_split_transposed_kernel(c
 struct OrthoPlan {
     int m, n, mp, np, parts;
     bool tall;
-    size_t partial, x0, x1, lo, a, b, da, db, bytes;  // offsets
+    size_t partial, x[2], lo[2], a, b, da, db, bytes;  // offsets
 };
 
 OrthoPlan plan_of(const ep_ortho_config &c) {
@@ -193,9 +193,10 @@ OrthoPlan plan_of(const ep_ortho_config &c) {
     };
     const size_t batch = (size_t)c.B, x = batch * p.m * p.np * 2, a = batch * p.m * p.mp * 2;
     p.partial = take(batch * p.parts * sizeof(double));
-    p.x0 = take(x);
-    p.x1 = take(x);
-    p.lo = take(x);
+    for (int i = 0; i < 2; ++i) {  // both halves: a step's are read by all while the next one's are written
+        p.x[i] = take(x);
+        p.lo[i] = take(x);
+    }
     p.a = take(a);
     p.b = take(a);
     p.da = take((batch * p.mp + 32) * sizeof(float));
@@ -227,7 +228,7 @@ cudaError_t make_x(const ep_ortho_config &c, const OrthoPlan &q, const void *m, 
 
 // What a product reads and writes, as tensors in global memory.
 struct OrthoOperands {
-    const uint16_t *a, *b;       // operands
+    const uint16_t *a, *b, *b_lo;  // operands
     const uint16_t *in[2];       // what its epilogue reads beside them
     const uint16_t *out[2];      // what it writes; Apply's last step: the result
 };
@@ -240,6 +241,7 @@ cudaError_t product(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
     bool ok = make_map(&p.a, q.a, 2, x, p.m, p.batch, kGemmBK, kGemmBM) &&
               (Sh::kBMn ? make_map(&p.b, q.b, 2, p.np, p.m, p.batch, 64, kGemmBK)
                         : make_map(&p.b, q.b, 2, x, p.m, p.batch, kGemmBK, Sh::kBRows));
+    if (OP == OrthoOp::kApply && p.form == OrthoForm::kWhole) ok = ok && make_map(&p.b_lo, q.b_lo, 2, p.np, p.m, p.batch, 64, kGemmBK);
     for (int i = 0; i < 2; ++i) {
         if (q.in[i]) ok = ok && make_piece_map(&p.in[i], q.in[i], wide, p.m, p.batch);
         if (!q.out[i]) continue;
@@ -297,10 +299,11 @@ cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
 
 size_t ortho_workspace_bytes(const ep_ortho_config &c) { return ortho_fits_fused(c) ? 256 : plan_of(c).bytes; }
 
-// Bounds of X, A and B over the steps, from |singular values| <= 1 on: whether they fit the halves.
-bool ortho_fits(const float *k, int32_t steps) {
-    double s = 1.0;
+bool ortho_steps(const float *k, int32_t steps, int32_t rows, OrthoForm *form) {
+    double s = 1.0, alike = 1.0 / std::sqrt((double)rows);  // the largest singular value; all of them, if they are alike
     for (int i = 0; i < steps; ++i) {
+        double growth = 1.0;  // by the later steps, of what X has none of
+        for (int j = i + 1; j < steps; ++j) growth *= std::fabs((double)k[3 * j]);
         const double a = k[3 * i], b = k[3 * i + 1], c = k[3 * i + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
         const double t = s * s;  // squares of singular values: [0, t]
@@ -320,11 +323,23 @@ bool ortho_fits(const float *k, int32_t steps) {
         }
         for (const double u : roots)
             if (u > 0 && u < t) next = std::fmax(next, value(u));
+        if (form) {
+            // kDiagonal: what it leaves is within 2^-12 `most` times X, and grows to 10 times 2^-12 X at most (the last two of
+            // the default steps; at 30, the last three, 64 x 256 of rank 16 is 0.19% off after five steps instead of 0.10).
+            // kUpper: B is about a third of a at most, so that 2^-12 B is little beside what A's and B's roundings leave (five
+            // steps of 256 x 384, the first two, free; the third as well would be 0.085% off instead of 0.067).
+            form[i] = most * growth <= 10                          ? OrthoForm::kDiagonal
+                      : poly(alike * alike) <= std::fabs(a) * 0.35 ? OrthoForm::kUpper
+                                                                   : OrthoForm::kWhole;
+        }
         s = next * 1.01;  // and roundings
+        alike = std::fmin(value(alike * alike), s);
         if (!(s < 4)) return false;
     }
     return true;
 }
+
+bool ortho_fits(const float *k, int32_t steps) { return ortho_steps(k, steps, 1, nullptr); }
 
 cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, void *workspace,
                                  cudaStream_t s) {
@@ -332,12 +347,12 @@ cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const
     const OrthoPlan q = plan_of(c);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
-    uint16_t *x[2] = {half(q.x0), half(q.x1)}, *lo = half(q.lo), *a = half(q.a), *b = half(q.b);
+    uint16_t *x[2] = {half(q.x[0]), half(q.x[1])}, *lo[2] = {half(q.lo[0]), half(q.lo[1])}, *a = half(q.a), *b = half(q.b);
     float *da = reinterpret_cast<float *>(ws + q.da), *db = reinterpret_cast<float *>(ws + q.db);
     double *partial = reinterpret_cast<double *>(ws + q.partial);
-    cudaError_t e = c.dtype == EP_F32    ? make_x<float>(c, q, m, partial, x[0], lo, s)
-                    : c.dtype == EP_BF16 ? make_x<__nv_bfloat16>(c, q, m, partial, x[0], lo, s)
-                                         : make_x<__half>(c, q, m, partial, x[0], lo, s);
+    cudaError_t e = c.dtype == EP_F32    ? make_x<float>(c, q, m, partial, x[0], lo[0], s)
+                    : c.dtype == EP_BF16 ? make_x<__nv_bfloat16>(c, q, m, partial, x[0], lo[0], s)
+                                         : make_x<__half>(c, q, m, partial, x[0], lo[0], s);
     if (e != cudaSuccess) return e;
     OrthoParams p = {};
     e = expert_error_word(&p.error);
@@ -348,21 +363,24 @@ cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const
     p.mp = q.mp;
     p.np = q.np;
     p.transposed = q.tall;
+    OrthoForm form[64];
+    ortho_steps(k, c.steps, q.m, form);
     for (int i = 0; i < c.steps; ++i) {
-        const uint16_t *now = x[i % 2];
+        const uint16_t *now = x[i % 2], *now_lo = lo[i % 2];
         p.ca = k[3 * i], p.cb = k[3 * i + 1], p.cc = k[3 * i + 2];
         p.d_out = da;
         p.split_out = a;
-        e = choose<OrthoOp::kGram>(p, {now, now, {}, {a}}, s);
+        e = choose<OrthoOp::kGram>(p, {now, now, nullptr, {}, {a}}, s);
         if (e != cudaSuccess) return e;
         p.d = da;
         p.d_out = db;
-        e = choose<OrthoOp::kPoly>(p, {a, a, {a}, {b}}, s);
+        e = choose<OrthoOp::kPoly>(p, {a, a, nullptr, {a}, {b}}, s);
         if (e != cudaSuccess) return e;
         p.d = db;
         const bool last = i + 1 == c.steps;
         p.result = last ? out : nullptr;
-        e = choose<OrthoOp::kApply>(p, {b, now, {now, lo}, {last ? out : x[(i + 1) % 2], last ? nullptr : lo}}, s);
+        p.form = form[i];
+        e = choose<OrthoOp::kApply>(p, {b, now, now_lo, {now, now_lo}, {last ? out : x[(i + 1) % 2], last ? nullptr : lo[(i + 1) % 2]}}, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

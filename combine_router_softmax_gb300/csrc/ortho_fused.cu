@@ -3,9 +3,10 @@
 // As three products a step, launched one after the other, a matrix of 128 rows takes 6 us a product whatever its
 // work: launch, first copies, last stores. Up to 128 rows (of the wide form) X stays on the chip instead: a cluster of
 // up to sixteen CTAs takes a matrix, each CTA 256 of its columns, and only the sums of A's parts pass between them.
-// X itself is fp32, in registers (a thread has 64 columns of a row), so that there is no lo; its halves, rounded as
+// X itself is fp32, in registers (a thread has 64 columns of a row); its halves, rounded as
 // in ortho_gemm.cuh, lie in shared memory and serve as both operands of A = X X^T (128 bytes of a row's columns,
-// swizzled) and, read the other way, as the second of B X. A and then B lie in one place.
+// swizzled) and, read the other way, as the second of B X. A and then B lie in one place. What the halves leave out becomes
+// halves of its own in the steps that take X whole (OrthoForm), where A's parts lie otherwise.
 //
 // What bounds it is the chain of a step: three waits for a few MMAs, three epilogues, as many fences and barriers.
 // 64 matrices of 128 x 256 take 27 us for five steps (84 by products of their own, in a graph), 1024 of them 193 (1119), one
@@ -23,8 +24,12 @@ constexpr int kBlock = kFusedRows * 128;           // bytes of 64 columns
 constexpr int kHalves = kFusedCols / 64 * kBlock;  // of X's halves
 constexpr int kSquare = kFusedRows / 64 * kBlock;  // of A, B
 constexpr int kPart = kFusedRows * kFusedRows * 4;
+static_assert(kPart == kHalves, "X's lower halves and A's parts take turns");
 constexpr int kStaging = kFusedRows * kFusedCols * 4;  // the matrix as it comes in, before there is anything else
 constexpr int kFusedSteps = 64;
+// Up to so many rows a step that takes X whole does so in A as well: an element of A is one of few then, and its
+// rounding is not lost among others' (16 x 24 of full rank, five steps: 0.09% off and 0.06; 8 x 8 0.14 and 0.12).
+constexpr int kFewRows = 16;
 
 struct FusedParams {
     const void *m;
@@ -33,6 +38,7 @@ struct FusedParams {
     float eps;
     int32_t *error;
     float k[kFusedSteps][3];
+    OrthoForm form[kFusedSteps];
 };
 
 // 16 bytes of a row: the 8 columns from `col` on (of the CTA's).
@@ -232,6 +238,19 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
     for (int k = 0; k < 32; ++k)
         x_own[k] = mul2(mul2(mul2(x_own[k], pair(scale.p1, scale.p1)), pair(scale.p2, scale.p2)), pair(scale.f * kX, scale.f * kX));
     put_halves();
+    // what they leave out
+    const auto put_rest = [&] {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint64_t x = x_own[16 * h + k], r = fma2(halves(half_pair(low(x), high(x))), pair(-1.0f, -1.0f), x);
+                o[k] = half_pair(low(r), high(r));
+            }
+            put_32(part, row, group * 64 + 32 * h, o);
+        }
+    };
 
     uint32_t phase = 0;
     // What all have written becomes operands: MMAs issued by one thread, waited for by all.
@@ -259,12 +278,20 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
 
     for (int step = 0; step < p.steps; ++step) {
         const float a = p.k[step][0], b = p.k[step][1], c = p.k[step][2];
+        const OrthoForm form = p.form[step];
         uint32_t v[32];
         // ---- A = X X^T
+        const bool whole = form == OrthoForm::kWhole, whole_a = whole && m <= kFewRows;
+        if (whole_a) put_rest();
         multiply([&] {
             for (int k = 0; k < k_cols; ++k) {
                 const uint64_t x = block_desc(hi, k);
                 mma_bf16<1>(tmem + kColA, x, x, mma_idesc_f16(128, 128, false), k > 0);
+                if (whole_a) {
+                    const uint64_t r = block_desc(part, k);
+                    mma_bf16<1>(tmem + kColA, x, r, mma_idesc_f16(128, kFewRows, false), true);
+                    mma_bf16<1>(tmem + kColA, r, x, mma_idesc_f16(128, kFewRows, false), true);
+                }
             }
         });
         const uint64_t by = pair(kA / (kX * kX), kA / (kX * kX));
@@ -342,19 +369,34 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
             if (put_square(square, row, group * 32, x, diagonal)) dB[row] = fmaf(diagonal, 1.0f / kB, a + fmaf(c * di, di, b * di));
         }
         // ---- X = a X + B X
+        if (whole && !(whole_a && ctas == 1)) put_rest();  // A's parts have taken its place
         multiply([&] {
             for (int k = 0; k < k_rows; ++k)
                 mma_bf16<1>(tmem + kColX, block_desc(square, k), smem_desc(smem_u32(hi) + k * 2048, kBlock),
                             mma_idesc_f16(128, 256, true), k > 0);
+            if (whole)
+                for (int k = 0; k < k_rows; ++k)
+                    mma_bf16<1>(tmem + kColX, block_desc(square, k), smem_desc(smem_u32(part) + k * 2048, kBlock),
+                                mma_idesc_f16(128, 256, true), true);
         });
         const float di = dB[row];
         const uint64_t d2 = pair(di, di), by_b = pair(1.0f / kB, 1.0f / kB);
+        const bool upper = form == OrthoForm::kUpper;
+        const uint64_t a2 = pair(a, a);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             tmem_load_32(tmem + kColX + lanes + group * 64 + 32 * h, v);
             tmem_wait_ld(v);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x_own[16 * h + k] = fma2(d2, x_own[16 * h + k], mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b));
+            for (int k = 0; k < 16; ++k) {
+                uint64_t x = x_own[16 * h + k], sum = mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b);
+                if (upper) {  // the diagonal times the upper half alone, a times both
+                    const uint64_t hi2 = halves(half_pair(low(x), high(x)));
+                    sum = fma2(a2, fma2(hi2, pair(-1.0f, -1.0f), x), sum);
+                    x = hi2;
+                }
+                x_own[16 * h + k] = fma2(d2, x, sum);
+            }
         }
         if (step + 1 < p.steps) put_halves();
     }
@@ -412,7 +454,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
 
 template <typename V>
 cudaError_t run_fused(const FusedParams &p, int batch, cudaStream_t s) {
-    const size_t work = (size_t)kHalves + kSquare + (p.ctas > 1 ? kPart : 0), smem = 1024 + (work > kStaging ? work : kStaging);
+    constexpr size_t work = (size_t)kHalves + kSquare + kPart, smem = 1024 + (work > kStaging ? work : kStaging);
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(ortho_fused_kernel<V>, smem);
     if (e != cudaSuccess) return e;
@@ -455,6 +497,7 @@ cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const v
     p.eps = c.eps;
     for (int i = 0; i < c.steps; ++i)
         for (int j = 0; j < 3; ++j) p.k[i][j] = k[3 * i + j];
+    ortho_steps(k, c.steps, c.N < c.K ? c.N : c.K, p.form);
     const cudaError_t e = expert_error_word(&p.error);
     if (e != cudaSuccess) return e;
     return c.dtype == EP_F32    ? run_fused<float>(p, c.B, s)

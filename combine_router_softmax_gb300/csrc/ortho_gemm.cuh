@@ -8,11 +8,11 @@
 // bf16 operands the result is 1% off for a matrix of independent values and up to 9% for one whose singular
 // values fall quickly. fp16 rounds eight times finer, its range is no limit (every value here has a known
 // bound, and a power of two that goes with it, kX, kA, kB), and three things keep its roundings out of the
-// result, 0.05% off before it is rounded itself:
-//   - X is two halves, hi + lo / 2^10. hi is the operand; a X is formed of both in fp32.
+// result, 0.05 to 0.1% off before it is rounded itself:
+//   - X is two halves, hi + lo. hi is the operand; a X is formed of both in fp32.
 //   - the diagonals of A and B, which are most of them once the singular values are alike, are fp32
 //     vectors; the halves hold the rest, with zeros there.
-//   - what of B lo is left out is then the rest's part alone.
+//   - what B X takes of lo goes by the step (OrthoForm).
 // Sums are fp32, in TMEM.
 //
 // One persistent CTA per SM (CG = 2: a pair, a tile of 256 x 256): two producer warps feed a ring of stages by
@@ -31,11 +31,25 @@ namespace ep {
 
 enum class OrthoOp { kGram, kPoly, kApply };
 
-// What is stored is the value times these: |X| < 4, |A| < 16 and |B| < 31 (ortho_fits) stay below 65504.
-constexpr float kX = 8192.0f, kA = 1024.0f, kB = 2048.0f, kLo = 1024.0f;
+// What B X takes of X's lower half. With D the diagonal of B, which is at hand in fp32:
+//   kDiagonal  a X + D X + (B - D) hi. What is missing, (B - D) lo, is little where the singular values are alike, as B
+//              is nearly its diagonal then. But it is noise in all directions, those included that X has none in, and
+//              there every later step multiplies it by its `a`: a matrix of half its rank is 5% off after eight steps.
+//   kUpper     a X + B hi. What is missing, B lo, is more, but has the directions of B's columns, which are X's: it turns
+//              them a little, and none grows. As cheap.
+//   kWhole     a X + B X, by a second pass over lo.
+// Which one is ortho_steps' rule: the diagonal's in the last steps, behind which nothing grows, before that the upper
+// half where B is small beside a for singular values that are all alike, else X whole. Off by (as the kernels round, before the
+// last rounding, default coefficients): 256 x 384 of rank 128, five steps 0.17% (kDiagonal alone), 0.11% (kUpper alone),
+// 0.10% (the rule); eight steps 5.6, 0.18, 0.14; of full rank 0.067, 0.127, 0.067.
+enum class OrthoForm : uint8_t { kDiagonal, kUpper, kWhole };
+
+// What is stored is the value times these: |X| < 4, |A| < 16 and |B| < 31 (ortho_steps) stay below 65504. lo, a 4096th of
+// X at most, has X's factor, so that both are terms of one sum: what fp16's range takes from it is below 2^-38 of X's bound.
+constexpr float kX = 8192.0f, kA = 1024.0f, kB = 2048.0f;
 
 struct OrthoParams {
-    CUtensorMap a, b;        // operands
+    CUtensorMap a, b, b_lo;  // operands; Apply that takes X whole: b_lo is its lower half
     CUtensorMap in[2];       // Poly: A without its diagonal; Apply: hi and lo of X. Boxes of 32 x 32 of the tile
     CUtensorMap out[2];      // Gram, Poly: A, B without its diagonal; Apply: hi and lo, or the result
     int32_t batch;
@@ -46,6 +60,7 @@ struct OrthoParams {
     ep_bf16 *result; // Apply: not null in the last step: [batch, m, n], or [batch, n, m] if `transposed`
     int32_t transposed;
     float ca, cb, cc;
+    OrthoForm form;       // Apply
     int32_t split;        // SPLIT: CTAs of a tile (2, 4 or 8)
     uint16_t *split_out;  // A without its diagonal
     int32_t *error;
@@ -234,7 +249,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
     unsigned char *buffers = stages + kStages * Sh::kStageBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0;
-    const int kb_all = ((OP == OrthoOp::kGram ? p.n : p.m) + kGemmBK - 1) / kGemmBK;
+    const int kb_once = ((OP == OrthoOp::kGram ? p.n : p.m) + kGemmBK - 1) / kGemmBK;
+    const int kb_all = OP == OrthoOp::kApply && p.form == OrthoForm::kWhole ? 2 * kb_once : kb_once;
     // this CTA's stages of the contraction
     const int part_of = SPLIT ? p.split : 1, part = SPLIT ? (int)cluster_cta_rank() : 0;
     const int kb_first = kb_all * part / part_of, kb = kb_all * (part + 1) / part_of - kb_first;
@@ -289,12 +305,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], Sh::kStageBytes * CG);
                     const uint32_t bar = CG == 2 ? cluster_smem_u32(&full[s], 0) : smem_u32(&full[s]);
                     unsigned char *sa = stages + s * Sh::kStageBytes, *sb = sa + Sh::kABytes;
-                    const int k = (kb_first + b) * kGemmBK;
+                    const bool lower = OP == OrthoOp::kApply && b >= kb_once;
+                    const int k = (kb_first + b - (lower ? kb_once : 0)) * kGemmBK;
                     tma_load_3d<CG>(sa, &p.a, k, t.m0 + (int)rank * kGemmBM, t.matrix, bar);
                     if constexpr (Sh::kBMn) {
+                        const CUtensorMap *x = lower ? &p.b_lo : &p.b;
 #pragma unroll
                         for (int i = 0; i < Sh::kBRows / 64; ++i)
-                            tma_load_3d<CG>(sb + i * 8192, &p.b, t.n0 + (int)rank * Sh::kBRows + 64 * i, k, t.matrix, bar);
+                            tma_load_3d<CG>(sb + i * 8192, x, t.n0 + (int)rank * Sh::kBRows + 64 * i, k, t.matrix, bar);
                     } else {
                         tma_load_3d<CG>(sb, &p.b, k, t.n0 + (int)rank * Sh::kBRows, t.matrix, bar);
                     }
@@ -411,17 +429,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ortho_gemm_kernel(const __gri
                     slab_get(second, lane, lo);
                     tmem_load_32(src + c, v);
                     tmem_wait_ld(v);
-                    const uint64_t d2 = pair(di, di), by_lo = pair(1.0f / kLo, 1.0f / kLo), by_b = pair(1.0f / kB, 1.0f / kB);
+                    const float dl = p.form == OrthoForm::kUpper ? p.ca : di;
+                    const uint64_t d2 = pair(di, di), dl2 = pair(dl, dl), by_b = pair(1.0f / kB, 1.0f / kB);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        // a + B's diagonal times hi + lo, and the product
-                        const uint64_t x = fma2(d2, fma2(halves(lo[k]), by_lo, halves(hi[k])), mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b));
+                        // a + B's diagonal times hi + lo (kUpper: a times lo), and the product
+                        const uint64_t x = fma2(d2, halves(hi[k]), fma2(dl2, halves(lo[k]), mul2(pair_of(v[2 * k], v[2 * k + 1]), by_b)));
                         if (p.result) {
                             const uint64_t y = mul2(x, pair(1.0f / kX, 1.0f / kX));
                             o[k] = bf16_pair(low(y), high(y));
                         } else {
                             o[k] = half_pair(low(x), high(x));
-                            const uint64_t r = mul2(fma2(halves(o[k]), pair(-1.0f, -1.0f), x), pair(kLo, kLo));
+                            const uint64_t r = fma2(halves(o[k]), pair(-1.0f, -1.0f), x);
                             lo[k] = half_pair(low(r), high(r));
                         }
                     }

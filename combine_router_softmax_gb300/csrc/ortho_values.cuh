@@ -37,8 +37,12 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t &hi, uin
     x0 *= kX, x1 *= kX;
     hi = half_pair(x0, x1);
     const float2 r = saved_values<false>(hi);
-    lo = half_pair((x0 - r.x) * kLo, (x1 - r.y) * kLo);
+    lo = half_pair(x0 - r.x, x1 - r.y);
 }
+
+// Whether the bounds of X, A and B over the steps, from |singular values| <= 1 on, fit the halves; and, where `form` is given,
+// what each step of matrices with so many rows does with X's lower half.
+bool ortho_steps(const float *k, int32_t steps, int32_t rows, OrthoForm *form);
 
 // Matrices that one cluster takes through all steps (ortho_fused.cu).
 bool ortho_fits_fused(const ep_ortho_config &c);
