@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(Sequence
                                                                         int32_t *count, float *load, float *prob, float *loss) {
     __shared__ float sums[kFinishThreads], inner[32], z_sums[32], products[8];
     __shared__ int32_t counts[kFinishThreads];
+    cluster_arrive();  // the others' memory is there from the wait below on: a CTA that starts late may still get it
     grid_dependency_wait();
     grid_launch_dependents();
     const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(Sequence
     product = warp_sum(product);
     if (threadIdx.x % 32 == 0) inner[threadIdx.x / 32] = product;
     __syncthreads();
+    cluster_wait();
     if (threadIdx.x < 32) {
         product = warp_sum(threadIdx.x < blockDim.x / 32 ? inner[threadIdx.x] : 0.0f);
         if (threadIdx.x == 0)
