@@ -223,7 +223,7 @@ template <int L, int NQ, bool WIDE>
 __global__ void __launch_bounds__(kSumThreads, NQ <= 4 ? 2 : 1) balance_kernel(Sequences seq, int E, int k, int tile_rows, const float *logits,
                                                                               const int32_t *idx, Partials part) {
     using R = Row<L, NQ, WIDE>;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];  // rows are stored 16 bytes at a time
     const int threads = blockDim.x, warps = threads / 32;
     float *sums = smem;                                                // [warp][E]
     int32_t *count = reinterpret_cast<int32_t *>(sums + warps * E);  // [E]
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kShortThreads, NQ <= 4 ? 3 : 1) balance_short_
                                                                                       const int32_t *idx, int32_t *count_out, float *load,
                                                                                       float *prob, float *loss) {
     using R = Row<L, NQ, WIDE>;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];  // rows are stored 16 bytes at a time
     constexpr int kWarps = kShortThreads / 32;
     float *sums = smem;                                                 // [warp][E]
     int32_t *count = reinterpret_cast<int32_t *>(sums + kWarps * E);  // [E]
