@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kSumThreads, NQ <= 4 ? 2 : 1) balance_kernel(S
         if (seq.begin(s) >= end) break;
         const int lo = max(seq.begin(s), begin), hi = min(seq.end(s), end);
         if (lo >= hi) continue;
-        const float z = sum_rows<L, NQ, WIDE>(logits, idx, E, lo + warp * R::kRows + lane / L, warps * R::kRows, hi,
+        const float z = sum_rows<L, NQ, WIDE>(logits, idx, E, (int64_t)lo + warp * R::kRows + lane / L, warps * R::kRows, hi,
                                               (int64_t)lo * k + threadIdx.x, threads, (int64_t)hi * k, sums, count, z_sums);
         __syncthreads();
         const size_t row = (size_t)blockIdx.x + s;
