@@ -7,58 +7,6 @@
 
 #include "ep_internal.cuh"
 
-namespace ep {
-
-namespace {
-constexpr int kMaxDevices = kMaxDevices_;
-std::atomic<int> g_sm_count[kMaxDevices];  // zero-initialised: not yet queried
-
-struct OccEntry {
-    const void *fn;
-    int dev;
-    int threads;
-    size_t smem;
-    int blocks;
-};
-std::mutex g_occ_mu;
-OccEntry g_occ[64];
-int g_occ_n = 0;
-}  // namespace
-
-int sm_count(int device) {
-    if (device < 0 || device >= kMaxDevices) return 0;
-    int v = g_sm_count[device].load(std::memory_order_relaxed);
-    if (v == 0) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
-        g_sm_count[device].store(v, std::memory_order_relaxed);
-    }
-    return v;
-}
-
-int current_device_sm_count() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    return sm_count(dev);
-}
-
-int max_blocks_per_sm(const void *fn, int threads, size_t smem) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    std::lock_guard<std::mutex> lock(g_occ_mu);
-    for (int i = 0; i < g_occ_n; ++i)
-        if (g_occ[i].fn == fn && g_occ[i].dev == dev && g_occ[i].threads == threads && g_occ[i].smem == smem)
-            return g_occ[i].blocks;
-    int b = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, smem) != cudaSuccess || b <= 0) {
-        cudaGetLastError();
-        b = 1;
-    }
-    if (g_occ_n < 64) g_occ[g_occ_n++] = OccEntry{fn, dev, threads, smem, b};
-    return b;
-}
-
-}  // namespace ep
-
 namespace {
 
 using ep::kMaxE;

@@ -5,6 +5,7 @@
 // expert_ffn.cu, expert_w4.cu, backward.cu and grad_clip.cu, those of what surrounds
 // the layer in norm.cu (with norm_forward.cu and norm_backward.cu), balance.cu and ortho.cu
 // (with ortho_fused.cu); each file exposes its host launchers, declared here.
+// device_info.cu answers what the host asks about a device.
 // The C entry points in ep_api.cu, experts_api.cu and layer_api.cu validate
 // arguments, then call the launchers.
 #pragma once
@@ -61,7 +62,7 @@ inline cudaError_t current_device(int *dev) {
     return (*dev < 0 || *dev >= kMaxDevices_) ? cudaErrorInvalidDevice : cudaSuccess;
 }
 
-// Cached device properties (per device ordinal).
+// Cached device properties (device_info.cu; per device ordinal).
 int sm_count(int device);
 int current_device_sm_count();
 // Resident CTAs per SM for a kernel (cached per kernel, device and launch shape).

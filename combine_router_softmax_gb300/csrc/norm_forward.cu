@@ -217,7 +217,9 @@ struct Forward {
 template <bool F32, int NV>
 cudaError_t few(const NormArgs &p, bool *took, cudaStream_t s) {
     const int threads = (p.vecs + 32 * NV - 1) / (32 * NV) * 32, sms = current_device_sm_count();
-    *took = p.T <= sms || p.T <= sms * max_blocks_per_sm((const void *)block_norm_few_kernel<F32, NV>, threads, 0);
+    // more of them than an SM's threads could hold are not asked for
+    *took = p.T <= sms || (p.T <= (int64_t)sms * (2048 / threads) &&
+                           p.T <= (int64_t)sms * max_blocks_per_sm((const void *)block_norm_few_kernel<F32, NV>, threads, 0));
     if (!*took) return cudaSuccess;
     return launch_dependent(block_norm_few_kernel<F32, NV>, dim3((unsigned)p.T), dim3((unsigned)threads), 0, s, p);
 }
