@@ -297,7 +297,7 @@ cudaError_t choose(OrthoParams &p, const OrthoOperands &q, cudaStream_t s) {
 
 }  // namespace
 
-size_t ortho_workspace_bytes(const ep_ortho_config &c) { return ortho_fits_fused(c) ? 256 : plan_of(c).bytes; }
+size_t ortho_workspace_bytes(const ep_ortho_config &c) { return ortho_fits_any_device(c) ? 256 : plan_of(c).bytes; }
 
 bool ortho_steps(const float *k, int32_t steps, int32_t rows, OrthoForm *form) {
     double s = 1.0, alike = 1.0 / std::sqrt((double)rows);  // the largest singular value; all of them, if they are alike
@@ -343,16 +343,21 @@ bool ortho_fits(const float *k, int32_t steps) { return ortho_steps(k, steps, 1,
 
 cudaError_t launch_orthogonalize(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, void *workspace,
                                  cudaStream_t s) {
-    if (ortho_fits_fused(c)) return launch_ortho_fused(c, k, m, out, s);
+    cudaError_t e;
+    if (ortho_fits_fused(c)) {
+        bool ran = false;
+        e = launch_ortho_fused(c, k, m, out, &ran, s);
+        if (e != cudaSuccess || ran) return e;
+    }
     const OrthoPlan q = plan_of(c);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
     uint16_t *x[2] = {half(q.x[0]), half(q.x[1])}, *lo[2] = {half(q.lo[0]), half(q.lo[1])}, *a = half(q.a), *b = half(q.b);
     float *da = reinterpret_cast<float *>(ws + q.da), *db = reinterpret_cast<float *>(ws + q.db);
     double *partial = reinterpret_cast<double *>(ws + q.partial);
-    cudaError_t e = c.dtype == EP_F32    ? make_x<float>(c, q, m, partial, x[0], lo[0], s)
-                    : c.dtype == EP_BF16 ? make_x<__nv_bfloat16>(c, q, m, partial, x[0], lo[0], s)
-                                         : make_x<__half>(c, q, m, partial, x[0], lo[0], s);
+    e = c.dtype == EP_F32    ? make_x<float>(c, q, m, partial, x[0], lo[0], s)
+        : c.dtype == EP_BF16 ? make_x<__nv_bfloat16>(c, q, m, partial, x[0], lo[0], s)
+                             : make_x<__half>(c, q, m, partial, x[0], lo[0], s);
     if (e != cudaSuccess) return e;
     OrthoParams p = {};
     e = expert_error_word(&p.error);

@@ -452,16 +452,16 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
     if (warp == 0) tmem_free<1>(tmem, 512);
 }
 
+constexpr int kAnyDeviceCtas = 8;  // clusters up to here run on every device
+
+// *ran: false, and nothing launched, where the device has no place for a cluster of so many CTAs (a partition of a GPU
+// with few SMs, for instance).
 template <typename V>
-cudaError_t run_fused(const FusedParams &p, int batch, cudaStream_t s) {
+cudaError_t run_fused(const FusedParams &p, int batch, bool *ran, cudaStream_t s) {
     constexpr size_t work = (size_t)kHalves + kSquare + kPart, smem = 1024 + (work > kStaging ? work : kStaging);
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.allow(ortho_fused_kernel<V>, smem);
     if (e != cudaSuccess) return e;
-    if (p.ctas > 8) {  // more than every device takes has to be asked for
-        const cudaError_t e = cudaFuncSetAttribute(ortho_fused_kernel<V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)batch * (unsigned)p.ctas);
     cfg.blockDim = dim3(kFusedThreads);
@@ -475,6 +475,26 @@ cudaError_t run_fused(const FusedParams &p, int batch, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.ctas == 1 ? 1 : 2;
+    *ran = true;
+    if (p.ctas > kAnyDeviceCtas) {
+        static std::atomic<int> places[kMaxDevices_][kFusedCtas + 1];  // clusters at a time, and one; 0: not asked yet
+        int dev = 0;
+        const cudaError_t e = current_device(&dev);
+        if (e != cudaSuccess) return e;
+        int n = places[dev][p.ctas].load(std::memory_order_acquire);
+        if (n == 0) {
+            if (cudaFuncSetAttribute(ortho_fused_kernel<V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&n, ortho_fused_kernel<V>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            places[dev][p.ctas].store(++n, std::memory_order_release);
+        }
+        if (n == 1) {
+            *ran = false;
+            return cudaSuccess;
+        }
+    }
     return cudaLaunchKernelEx(&cfg, ortho_fused_kernel<V>, p);
 }
 
@@ -485,7 +505,11 @@ bool ortho_fits_fused(const ep_ortho_config &c) {
     return m <= kFusedRows && n <= kFusedCtas * kFusedCols;
 }
 
-cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, cudaStream_t s) {
+bool ortho_fits_any_device(const ep_ortho_config &c) {
+    return ortho_fits_fused(c) && (c.N < c.K ? c.K : c.N) <= kAnyDeviceCtas * kFusedCols;
+}
+
+cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, bool *ran, cudaStream_t s) {
     FusedParams p = {};
     const int n = c.N < c.K ? c.K : c.N;
     p.m = m;
@@ -500,9 +524,9 @@ cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const v
     ortho_steps(k, c.steps, c.N < c.K ? c.N : c.K, p.form);
     const cudaError_t e = expert_error_word(&p.error);
     if (e != cudaSuccess) return e;
-    return c.dtype == EP_F32    ? run_fused<float>(p, c.B, s)
-           : c.dtype == EP_BF16 ? run_fused<__nv_bfloat16>(p, c.B, s)
-                                : run_fused<__half>(p, c.B, s);
+    return c.dtype == EP_F32    ? run_fused<float>(p, c.B, ran, s)
+           : c.dtype == EP_BF16 ? run_fused<__nv_bfloat16>(p, c.B, ran, s)
+                                : run_fused<__half>(p, c.B, ran, s);
 }
 
 }  // namespace ep

@@ -46,6 +46,9 @@ bool ortho_steps(const float *k, int32_t steps, int32_t rows, OrthoForm *form);
 
 // Matrices that one cluster takes through all steps (ortho_fused.cu).
 bool ortho_fits_fused(const ep_ortho_config &c);
-cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, cudaStream_t s);
+// And that one does on every device: the others need the products' workspace, in case this device has no place for it.
+bool ortho_fits_any_device(const ep_ortho_config &c);
+// *ran: false, with cudaSuccess, where it has none.
+cudaError_t launch_ortho_fused(const ep_ortho_config &c, const float *k, const void *m, ep_bf16 *out, bool *ran, cudaStream_t s);
 
 }  // namespace ep

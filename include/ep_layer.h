@@ -195,8 +195,8 @@ typedef struct ep_ortho_config {
  * m         : const [B, N, K] of cfg->dtype, aligned to its values
  * out       : bf16 [B, N, K], 16-byte aligned; may be m where that is of 16 bits
  * workspace : 256-byte aligned, >= ep_orthogonalize_workspace_size bytes: about 8 bytes a
- *             value and 4 min(N, K)^2 a matrix, 256 where a matrix stays on the chip
- *             (min(N, K) <= 128 and max(N, K) <= 4096)
+ *             value and 4 min(N, K)^2 a matrix, 256 for min(N, K) <= 128 and
+ *             max(N, K) <= 2048, where every device keeps a matrix on the chip (up to 4096 where it has the place)
  * A CTA that gives up a bounded wait sets ep_device_error bit 5 (32).
  */
 ep_status ep_orthogonalize_workspace_size(const ep_ortho_config *cfg, size_t *bytes);
