@@ -142,7 +142,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
-// What the warp has written to its slabs goes out by the copies that one lane issues next.
+// What the warp has written to its slabs, or read from them, comes before the copies that one lane issues next, out of
+// them or into them.
 __device__ __forceinline__ void slabs_to_copies() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -153,13 +154,13 @@ __device__ __forceinline__ void slab_put_transposed(unsigned char *slab, int lan
     for (int i = 0; i < 32; ++i)
         *reinterpret_cast<uint16_t *>(slab + slab_at(i, lane / 8) + lane % 8 * 2) = (uint16_t)(v[i / 2] >> (i % 2 * 16));
 }
-// To rows of any length, value by value: columns [n, n + 32) of N.
+// To rows of any length, value by value: columns [n, n + 32) of N. The slab is the next copies' from here on.
 __device__ __forceinline__ void slab_store_any(const unsigned char *slab, int lane, ep_bf16 *base, int N, int n, int rows) {
     __syncwarp();
     if (n + lane < N)
         for (int r = 0; r < rows; ++r)
             base[(size_t)r * N + n + lane] = *reinterpret_cast<const uint16_t *>(slab + slab_at(r, lane / 8) + lane % 8 * 2);
-    __syncwarp();
+    slabs_to_copies();
 }
 // Two halves as floats, and two registers as a pair.
 __device__ __forceinline__ uint64_t halves(uint32_t v) {
