@@ -48,7 +48,8 @@ ep_status check_balance(const ep_config *c, int32_t n_seq, const int32_t *seq_fi
 }
 
 constexpr int kMaxOrthoSide = 65536, kMaxOrthoSteps = 64;
-// A quintic that lifts small singular values quickly and keeps the others near one, for every step.
+// A quintic that lifts small singular values quickly and keeps the others near one, for every step: K. Jordan's published
+// coefficients (2024) for orthogonalising momentum by Newton-Schulz steps.
 constexpr float kOrthoDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
 ep_status check_ortho(const ep_ortho_config *c) {

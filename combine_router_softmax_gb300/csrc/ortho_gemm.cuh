@@ -20,8 +20,9 @@
 // wait has a time limit (kErrOrthoWait).
 //
 // 16 matrices of 2048 x 4096: Gram 186 us, Poly 101, Apply 370 (the last one 335), the tensor pipe 73 to 88 % busy; the
-// clock falls to 1.6 GHz, as power bounds them (a quarter fewer cycles for a tile left the time as it was). One matrix of
-// 256 x 7168 takes 102 us for five steps, 17 kernels one after another: launch, first copies, last stores of each.
+// clock falls to 1.6 GHz, as power bounds them (a quarter fewer cycles for a tile left the time as it was). No step of five
+// takes X whole there; three of eight do (7.0 ms instead of 6.2). One matrix of
+// 256 x 7168 takes 98 to 101 us for five steps, 17 kernels one after another: launch, first copies, last stores of each.
 #pragma once
 
 #include "expert_gemm.cuh"
