@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1) ortho_fused_kernel(const __g
                 const uint64_t x = block_desc(hi, k);
                 mma_bf16<1>(tmem + kColA, x, x, mma_idesc_f16(128, 128, false), k > 0);
                 if (whole_a) {
-                    const uint64_t r = block_desc(part, k);
-                    mma_bf16<1>(tmem + kColA, x, r, mma_idesc_f16(128, kFewRows, false), true);
-                    mma_bf16<1>(tmem + kColA, r, x, mma_idesc_f16(128, kFewRows, false), true);
+                    const uint64_t r = block_desc(part, k);  // of one shape: only such products are added in order
+                    mma_bf16<1>(tmem + kColA, x, r, mma_idesc_f16(128, 128, false), true);
+                    mma_bf16<1>(tmem + kColA, r, x, mma_idesc_f16(128, 128, false), true);
                 }
             }
         });
