@@ -478,20 +478,21 @@ cudaError_t run_fused(const FusedParams &p, int batch, bool *ran, cudaStream_t s
     cfg.numAttrs = p.ctas == 1 ? 1 : 2;
     *ran = true;
     if (p.ctas > kAnyDeviceCtas) {
-        static std::atomic<int> places[kMaxDevices_][kFusedCtas + 1];  // clusters at a time, and one; 0: not asked yet
+        static std::atomic<int> places[kMaxDevices_][kFusedCtas + 1];  // clusters at a time, and one; 0: no answer yet
         int dev = 0;
         const cudaError_t e = current_device(&dev);
         if (e != cudaSuccess) return e;
         int n = places[dev][p.ctas].load(std::memory_order_acquire);
         if (n == 0) {
-            if (cudaFuncSetAttribute(ortho_fused_kernel<V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-                cudaOccupancyMaxActiveClusters(&n, ortho_fused_kernel<V>, &cfg) != cudaSuccess) {
+            if (cudaFuncSetAttribute(ortho_fused_kernel<V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&n, ortho_fused_kernel<V>, &cfg) == cudaSuccess) {
+                places[dev][p.ctas].store(++n, std::memory_order_release);
+            } else {
                 cudaGetLastError();
                 n = 0;
             }
-            places[dev][p.ctas].store(++n, std::memory_order_release);
         }
-        if (n == 1) {
+        if (n <= 1) {
             *ran = false;
             return cudaSuccess;
         }

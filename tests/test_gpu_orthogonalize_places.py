@@ -31,9 +31,11 @@ def without(request, tmp_path_factory):
     b.build()
     path = tmp_path_factory.mktemp("places")
     (path / "fake.cu").write_text(FAKE)
-    objects = [str(b.BUILD / (s.stem + ".o")) for s in b.sources() if s.stem != "ortho_fused"]
+    objects = [b.BUILD / (s.stem + ".o") for s in b.sources() if s.stem != "ortho_fused"]
+    if not all(o.exists() for o in objects):
+        b.build(force=True)
     cmd = [b.nvcc_path(), *b.ARCH, "-O3", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared", f"-DFAIL={request.param}",
-           "-Xlinker", "-Bsymbolic", f"-I{b.ROOT / 'include'}", f"-I{b.CSRC}", str(path / "fake.cu"), *objects, "-o", str(path / "without.so")]
+           "-Xlinker", "-Bsymbolic", f"-I{b.ROOT / 'include'}", f"-I{b.CSRC}", str(path / "fake.cu"), *map(str, objects), "-o", str(path / "without.so")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     return ctypes.CDLL(str(path / "without.so"))
